@@ -18,9 +18,11 @@ def _proj(name, op, T, m, d, bits, group, rank, n, requests, x, y="", save_u=Fal
                 requests=requests, x=x, y=y or x, save_u=save_u)
 
 
-def _loss(name, T, V, K, x, tau, backward, full):
-    """full: the teacher's log-sum-exp over its whole vocabulary was stored with its top logits."""
-    return dict(name=name, op="distill", T=T, V=V, K=K, x=x, tau=tau, backward=backward, full=full)
+def _loss(name, T, V, K, x, tau, mode, full):
+    """mode: "loss" (validation), "step" (loss and gradient at once, the tokens' upstream gradients
+    known) or "backward" (the gradient afterwards, from the kept log-sum-exp).
+    full: the teacher's log-sum-exp over its whole vocabulary was stored with its top logits."""
+    return dict(name=name, op="distill", T=T, V=V, K=K, x=x, tau=tau, mode=mode, full=full)
 
 
 def listed():
@@ -42,10 +44,11 @@ def listed():
         _proj("backward 2048 q_proj", "backward", 2048, 4096, 4096, 4, 128, 16, 1, 1, "bf16"),
         _proj("backward 4096 down_proj", "backward", 4096, 4096, 11008, 4, 128, 32, 4, 4, "f16"),
         # a validation pass over a few tokens, fp32 logits
-        _loss("distill eval 5 x 32000", 5, 32000, 16, "f32", 1.0, False, False),
-        # training steps: an odd vocabulary with the teacher's full mass, and the largest
-        _loss("distill 1024 x 50257", 1024, 50257, 32, "f16", 2.0, True, True),
-        _loss("distill 4096 x 128000", 4096, 128000, 128, "bf16", 1.0, True, False),
+        _loss("distill eval 5 x 32000", 5, 32000, 16, "f32", 1.0, "loss", False),
+        # the gradient alone, an odd vocabulary and the teacher's full mass
+        _loss("distill backward 1024 x 50257", 1024, 50257, 32, "f16", 2.0, "backward", True),
+        # the largest training step
+        _loss("distill step 4096 x 128000", 4096, 128000, 128, "bf16", 1.0, "step", False),
     ]
 
 
@@ -62,9 +65,9 @@ def draw(rng):
     if op == "distill":
         V = _log(rng, 1000, 128000)
         T = min(_log(rng, 1, 4096), MOST_LOGITS // V)
-        backward = rng.random() < 0.75
         c = _loss("", T, V, min(_log(rng, 1, 256), V), rng.choice(["bf16", "f16", "f32"]),
-                  rng.choice([1.0, 2.0, 4.0]), backward, rng.random() < 0.5)
+                  rng.choice([1.0, 2.0, 4.0]), rng.choice(["loss", "step", "step", "backward"]),
+                  rng.random() < 0.5)
     else:
         m = _log(rng, 512, 12288)
         d = 32 * _log(rng, 16, 384) if rng.random() < 0.75 else 8 * _log(rng, 64, 1536)
@@ -145,6 +148,8 @@ def _prepare_distill(case, g):
     # the rest of the teacher's vocabulary holds some of its mass
     s["teacher_lse"] = torch.logsumexp(values / tau, 1) + 0.1 * torch.rand(T, device="cuda", generator=g) \
         if case["full"] else None
+    if case["mode"] == "backward":
+        s["lse"] = torch.where(weight != 0, torch.logsumexp(s["logits"].float() / tau, 1), 0.0)
     return s
 
 
@@ -154,8 +159,9 @@ def _prepare_own(case, s):
     T, f32, e = case["T"], torch.float32, lambda *a, **k: torch.empty(*a, device="cuda", **k)
     if case["op"] == "distill":
         s["ctx"] = G.Context(1, 1, workspace_bytes=1 << 20)
-        s["loss"], s["lse"] = e(T, dtype=f32), e(T, dtype=f32)
-        s["dlogits"] = torch.empty_like(s["logits"]) if case["backward"] else None
+        if case["mode"] != "backward":
+            s["loss"], s["lse"] = e(T, dtype=f32), e(T, dtype=f32)
+        s["dlogits"] = torch.empty_like(s["logits"]) if case["mode"] != "loss" else None
         return
     m, d, bits, R, n = (case[k] for k in ("m", "d", "bits", "rank", "n"))
     dt = DTYPES[case["x"]]
@@ -187,12 +193,15 @@ def _run_own(case, s):
                              s["scales"], s["zeros"], s["adapter"], s["A"], s["B"], s["scaling"], s["U"],
                              dX=s["dX"], dA=s["dA"], dB=s["dB"])
         return {"dX": s["dX"], "dA": s["dA"], "dB": s["dB"]}
-    G.gptq_distill_topk(s["ctx"], s["logits"], s["values"], s["indices"], case["tau"], s["loss"], s["lse"],
-                        weight=s["weight"], teacher_lse=s["teacher_lse"])
-    if case["backward"]:
+    if case["mode"] == "backward":
         G.gptq_distill_topk_backward(s["ctx"], s["logits"], s["values"], s["indices"], case["tau"], s["lse"],
                                      s["dloss"], s["dlogits"], weight=s["weight"],
                                      teacher_lse=s["teacher_lse"])
+        return {"dlogits": s["dlogits"]}
+    step = case["mode"] == "step"
+    G.gptq_distill_topk(s["ctx"], s["logits"], s["values"], s["indices"], case["tau"], s["loss"], s["lse"],
+                        weight=s["weight"], teacher_lse=s["teacher_lse"], dloss=s["dloss"] if step else None,
+                        dlogits=s["dlogits"])
     return {"loss": s["loss"], "lse": s["lse"], "dlogits": s["dlogits"]}
 
 
@@ -242,10 +251,8 @@ def _backward(case, s):
 
 
 def _distill(case, s):
-    tau, idx, w = case["tau"], s["indices"].long(), s["weight"]
+    tau, idx, w, mode = case["tau"], s["indices"].long(), s["weight"], case["mode"]
     y = s["logits"].float() / tau
-    top = y.max(1, keepdim=True).values
-    lse = (top + (y - top).exp().sum(1, keepdim=True).log())
     v = torch.where(idx >= 0, s["values"] / tau, -math.inf)
     if case["full"]:
         logp = v - s["teacher_lse"][:, None]
@@ -253,11 +260,16 @@ def _distill(case, s):
         most = v.max(1, keepdim=True).values
         logp = v - most - (v - most).exp().sum(1, keepdim=True).log()
     p, at = logp.exp(), idx.clamp(min=0)
-    logq = y.gather(1, at) - lse
-    loss = w * tau * tau * torch.where(p > 0, p * (logp - logq), 0.0).sum(1)
-    live = w != 0
-    out = {"loss": torch.where(live, loss, 0.0), "lse": torch.where(live, lse[:, 0], 0.0), "dlogits": None}
-    if case["backward"]:
+    out = {}
+    if mode == "backward":
+        lse = s["lse"][:, None]
+    else:
+        top = y.max(1, keepdim=True).values
+        lse = top + (y - top).exp().sum(1, keepdim=True).log()
+        kl = torch.where(p > 0, p * (logp - (y.gather(1, at) - lse)), 0.0).sum(1)
+        out = {"loss": torch.where(w != 0, w * tau * tau * kl, 0.0),
+               "lse": torch.where(w != 0, lse[:, 0], 0.0), "dlogits": None}
+    if mode != "loss":
         dz = (y - lse).exp() * p.sum(1, keepdim=True)
         dz.scatter_add_(1, at, -p)
         dz *= (s["dloss"] * w * tau)[:, None]
@@ -271,7 +283,7 @@ def work(case):
     T, size = case["T"], {"bf16": 2, "f16": 2, "f32": 4}
     if case["op"] == "distill":
         V, K, e = case["V"], case["K"], size[case["x"]]
-        passes = 2 if case["backward"] else 1          # logits read once; gradients written once
+        passes = 1 if case["mode"] == "loss" else 2    # logits read once; gradients written once
         return {"bytes": T * V * e * passes + 8.0 * T * K + 16.0 * T, "flops": 4.0 * T * V * passes}
     m, d, R, n, e = case["m"], case["d"], case["rank"], case["n"], size[case["x"]]
     ng = 1 if case["group"] == -1 else -(-d // case["group"])
@@ -325,10 +337,10 @@ def _exact_proj(case, s):
 
 
 def _exact_distill(case, s):
-    """Token by token where the lists differ in length, in blocks of tokens, in fp64."""
+    """The teacher as a dense distribution over the vocabulary, in blocks of tokens, in fp64."""
     T, V, tau, f64 = case["T"], case["V"], case["tau"], torch.float64
     loss, lse = torch.zeros(T, dtype=f64, device="cuda"), torch.zeros(T, dtype=f64, device="cuda")
-    grad = torch.zeros(T, V, dtype=f64, device="cuda") if case["backward"] else None
+    grad = None if case["mode"] == "loss" else torch.zeros(T, V, dtype=f64, device="cuda")
     for t0 in range(0, T, 256):
         sl = slice(t0, t0 + 256)
         w, idx = s["weight"][sl].to(f64), s["indices"][sl].long()
@@ -338,7 +350,6 @@ def _exact_distill(case, s):
         total = s["teacher_lse"][sl].to(f64) if case["full"] else torch.logsumexp(v, 1)
         p = torch.exp(v - total[:, None])
         have = idx >= 0
-        # the teacher as a dense distribution over the vocabulary
         dense = torch.zeros_like(logq)
         row = torch.arange(idx.shape[0], device="cuda")[:, None].expand_as(idx)
         dense[row[have], idx[have]] = p[have]
@@ -347,4 +358,4 @@ def _exact_distill(case, s):
         if grad is not None:
             step = (s["dloss"][sl].to(f64) * w * tau)[:, None]
             grad[sl] = step * (p.sum(1, keepdim=True) * logq.exp() - dense)
-    return {"loss": loss, "lse": lse, "dlogits": grad}
+    return {"dlogits": grad} if case["mode"] == "backward" else {"loss": loss, "lse": lse, "dlogits": grad}
