@@ -85,13 +85,15 @@ int gptq_set_wait_budget(gptq_ctx* ctx, int64_t cycles);
  * a-numbers are the steps of the hot path: a1 Hessian, a2 preconditioning, a3 factorization
  * (base blocks, recursion GEMMs, copies), a4 grid fit, a5 column loop (working copy, column
  * blocks), a6 lazy trailing updates, a7 outputs in original order, a8 packing; then the W4A16
- * product and two-sided rounding. */
+ * product, two-sided rounding, the packed layer with low-rank adapters and the distillation
+ * loss. */
 enum {
   GPTQ_STAGE_HESSIAN = 0, GPTQ_STAGE_PREPARE = 1, GPTQ_STAGE_FACTOR_BASE = 2,
   GPTQ_STAGE_FACTOR_GEMM = 3, GPTQ_STAGE_FACTOR_COPY = 4, GPTQ_STAGE_GRID = 5,
   GPTQ_STAGE_COLUMN = 6, GPTQ_STAGE_UPDATE = 7, GPTQ_STAGE_OUTPUT = 8, GPTQ_STAGE_PACK = 9,
   GPTQ_STAGE_DEQUANT = 10, GPTQ_STAGE_TWOSIDED = 11, GPTQ_STAGE_OTHER = 12,
-  GPTQ_NUM_STAGES = 13
+  GPTQ_STAGE_LORA = 13, GPTQ_STAGE_DISTILL = 14,
+  GPTQ_NUM_STAGES = 15
 };
 
 /* Per-stage kernel timing, for measurement.  on != 0: from now on every kernel this context
@@ -273,6 +275,96 @@ int gptq_retile_codes(gptq_ctx* ctx, const uint32_t* packed, int64_t m, int64_t 
 int gptq_dequant_matmul_tiled(gptq_ctx* ctx, const void* X, int x_dtype, int64_t T, int64_t d,
                               const uint32_t* tiled, int64_t m, int group, int64_t n_g,
                               const float* scales, const int32_t* zeros, float* Y);
+
+/* The packed layer with low-rank adapters of many requests.  The pages deploy one packed layer
+ * for everybody ([T] §1.2, [A] "how it works"); the adapters are the usual way to specialise it
+ * per request, and to win back what the rounding lost, without touching the codes.  Token t uses
+ * adapter a = adapter[t] (-1: none):
+ *   U[t]  = scaling[a] A[a] X[t]         (0 for a token without an adapter)
+ *   Y[t]  = Ŵ X[t] + B[a]ᵀ U[t]          (Ŵ as in gptq_dequant_matmul)
+ *   X        [T, d] of type x_dtype, device.  0 <= T <= 524280 (T = 0: nothing is done).
+ *   packed, bits, group, group_id, n_g, scales, zeros   the layer, as for gptq_dequant_matmul;
+ *            m, d <= 2^24.
+ *   adapter  [T] int32 device; the tokens of an adapter may stand anywhere in the batch.
+ *   A        [n_adapters, rank, d] and B [n_adapters, rank, m] of type x_dtype, device: both
+ *            rank-major (the usual up-projection [m, rank] of an adapter is stored transposed).
+ *            An adapter of a lower rank has zeros behind it.  n_adapters <= 65535, rank <= 1024.
+ *   scaling  [n_adapters] fp32 device.
+ *   Y        [T, m] out, of type y_dtype: GPTQ_F32 or x_dtype (rounded once, from fp32).
+ *   U        [T, rank] fp32 out, device, or NULL (then it stays in the workspace); a later
+ *            gptq_lora_backward takes it.
+ * Ŵ, U and every sum are kept in fp32 or better.  A token's result depends on its own row of X and
+ * its own adapter only: non-finite values in other rows or adapters do not reach it.
+ * 16-bit X with 1- to 4-bit codes, group -1 or a multiple of 128 and no group_id runs on the
+ * tensor cores (the zeros must then lie in 0..15); every other format on CUDA cores.
+ * Workspace: gptq_lora_workspace_bytes covers this call and gptq_lora_backward.  Asynchronous.  Errors: ARG (also an adapter id outside
+ * [-1, n_adapters), which then counts as -1, a group_id entry outside [0, n_g) or a zero outside
+ * 0..15 on the tensor cores, via gptq_sync_status), NOMEM, CUDA, TIMEOUT via gptq_sync_status. */
+size_t gptq_lora_workspace_bytes(int64_t T, int64_t m, int64_t d, int bits, int64_t n_adapters,
+                                 int64_t rank, int x_dtype);
+int gptq_lora_matmul(gptq_ctx* ctx, const void* X, int x_dtype, int64_t T, int64_t d,
+                     const uint32_t* packed, int64_t m, int bits, int group,
+                     const int32_t* group_id, int64_t n_g, const float* scales,
+                     const int32_t* zeros, const int32_t* adapter, int64_t n_adapters,
+                     int64_t rank, const void* A, const void* B, const float* scaling, void* Y,
+                     int y_dtype, float* U);
+
+/* The backward pass of gptq_lora_matmul for training the adapters; the codes and their grid are
+ * constants.  With G[t] = scaling[a] B[a] dY[t]:
+ *   dX[t]  = Ŵᵀ dY[t] + A[a]ᵀ G[t]
+ *   dA[a]  = Σ_{t: adapter[t] = a} G[t] X[t]ᵀ,   dB[a] = Σ_{t: adapter[t] = a} U[t] dY[t]ᵀ
+ *   dY       [T, m] of type x_dtype, device.
+ *   X, U     the forward call's input and its U (X may be NULL without dA, U without dB).
+ *   dX       [T, d] of type x_dtype out; dA [n_adapters, rank, d] and dB [n_adapters, rank, m]
+ *            fp32 out.  Any of the three may be NULL, not all.
+ *   accumulate  0: dA and dB are overwritten (adapters without tokens get 0); 1: they are added to.
+ * On the tensor cores dX is formed from Ŵ rounded to x_dtype (its products and sums in fp32); for
+ * GPTQ_F16 that asks for |Ŵ| < 255, else ARG via gptq_sync_status.  dA and dB are sums over tokens
+ * in a fixed order: two calls on the same inputs give the same bits.  Non-finite values of a token
+ * reach its own row of dX and its own adapter's gradients only.  T = 0 clears dA and dB (or leaves
+ * them, with accumulate).  Errors as for gptq_lora_matmul. */
+int gptq_lora_backward(gptq_ctx* ctx, const void* dY, const void* X, int x_dtype, int64_t T,
+                       int64_t d, const uint32_t* packed, int64_t m, int bits, int group,
+                       const int32_t* group_id, int64_t n_g, const float* scales,
+                       const int32_t* zeros, const int32_t* adapter, int64_t n_adapters,
+                       int64_t rank, const void* A, const void* B, const float* scaling,
+                       const float* U, void* dX, float* dA, float* dB, int accumulate);
+
+/* Distillation of the quantized model from the full-precision one's stored top logits: the loss
+ * that trains the adapters above back to the teacher.  Per token, with y = logits / tau,
+ * lse = log Σ_j exp y_j, and p_k = exp(values_k / tau - L) over the token's K stored entries:
+ *   loss   = weight tau² Σ_k p_k (log p_k - (y_{i_k} - lse))
+ *   dlogits_i = dloss weight tau (M exp(y_i - lse) - Σ_{k: i_k = i} p_k),      M = Σ_k p_k
+ *   logits   [T, V] of type dtype with a row stride of ld >= V elements, device.
+ *   values   [T, K] fp32 and indices [T, K] int32 in [0, V), device: the teacher's logits and where
+ *            they belong, in any order; index -1: no entry (a short list).  An index that occurs
+ *            twice counts with the sum of its entries' p_k in dlogits, and entry by entry in the
+ *            loss.  K <= 2048.  A value of -inf has p_k = 0; a token without entries has loss and
+ *            gradient 0.
+ *   tau      temperature, in [1e-6, 1e6].
+ *   weight   [T] fp32 or NULL (all 1); a token of weight 0 is not read: its loss, lse and gradient
+ *            are 0.
+ *   teacher_lse  [T] fp32 or NULL: L, the teacher's own log Σ exp(logit / tau) over its whole
+ *            vocabulary, so that M < 1; NULL: L is taken over the K entries, so that M = 1.
+ *   loss, lse    [T] fp32 out.
+ *   dloss, dlogits  [T] fp32 and [T, V] of type dtype (row stride ld_grad >= V) out, or both NULL:
+ *            with them the gradient is formed in the same pass.  dlogits may be logits itself
+ *            (then ld_grad == ld); what lies behind a row's V entries is left alone.
+ * A student logit of -inf has q = 0: listed with p_k > 0 it makes the loss +inf.  A row that is all
+ * -inf, or holds NaN or +inf, gives NaN.  Sums are kept in fp32.  No workspace.  Asynchronous.
+ * Errors: ARG (also an index outside [-1, V), which then counts as -1, via gptq_sync_status),
+ * CUDA. */
+int gptq_distill_topk(gptq_ctx* ctx, const void* logits, int dtype, int64_t T, int64_t V,
+                      int64_t ld, const float* values, const int32_t* indices, int64_t K,
+                      float tau, const float* weight, const float* teacher_lse, float* loss,
+                      float* lse, const float* dloss, void* dlogits, int64_t ld_grad);
+
+/* The gradient afterwards, from the lse that gptq_distill_topk wrote. */
+int gptq_distill_topk_backward(gptq_ctx* ctx, const void* logits, int dtype, int64_t T, int64_t V,
+                               int64_t ld, const float* values, const int32_t* indices, int64_t K,
+                               float tau, const float* weight, const float* teacher_lse,
+                               const float* lse, const float* dloss, void* dlogits,
+                               int64_t ld_grad);
 
 /* Two-sided rounding (GPTQ-2D, [D] "GPTQ-2D：把一个"四次方"难题压回"三次方"的故事"): X [m, n] is
  * rounded to an integer matrix Z for the metric ||A (Z - X) B||^2, given the metric factors

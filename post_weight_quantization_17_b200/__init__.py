@@ -29,7 +29,7 @@ _DTYPE_CODE = {torch.bfloat16: GPTQ_BF16, torch.float16: GPTQ_F16, torch.float32
 
 # stages of gptq_timing_read, in the order of the GPTQ_STAGE_* constants
 STAGES = ("hessian", "prepare", "factor_base", "factor_gemm", "factor_copy", "grid", "column",
-          "update", "output", "pack", "dequant", "twosided", "other")
+          "update", "output", "pack", "dequant", "twosided", "other", "lora", "distill")
 
 
 class GPTQError(RuntimeError):
@@ -69,6 +69,16 @@ _SIGS = {
     "gptq_retile_codes": (_i32, [_vp, _vp, _i64, _i64, _vp]),
     "gptq_dequant_matmul_tiled": (_i32, [_vp, _vp, _i32, _i64, _i64, _vp, _i64, _i32, _i64, _vp,
                                          _vp, _vp]),
+    "gptq_lora_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i64, _i64, _i32]),
+    "gptq_lora_matmul": (_i32, [_vp, _vp, _i32, _i64, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _vp,
+                                _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _vp]),
+    "gptq_lora_backward": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _vp, _i64, _i32, _i32, _vp,
+                                  _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _vp, _i32]),
+    "gptq_distill_topk": (_i32, [_vp, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _i64,
+                                 ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _i64]),
+    "gptq_distill_topk_backward": (_i32, [_vp, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _i64,
+                                          ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _i64]),
     "gptq_twosided_factor": (_i32, [_vp, _vp, _i64]),
     "gptq_twosided_round": (_i32, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
 }
@@ -98,13 +108,17 @@ def _dev(t: torch.Tensor, dtype=None, name="tensor"):
 
 class Context:
     """A library context: the CUDA stream the calls are enqueued on and a device workspace
-    (a torch uint8 tensor) sized for layers up to (m_max, d_max)."""
+    (a torch uint8 tensor) sized for layers up to (m_max, d_max), and of at least
+    `workspace_bytes` bytes (see gptq_lora_workspace_bytes)."""
 
     def __init__(self, m_max: int, d_max: int, act_order: bool = True, stream=None,
-                 device=None):
+                 device=None, workspace_bytes: int = 0):
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
-        nbytes = int(_lib.gptq_workspace_bytes(m_max, d_max, 1 if act_order else 0))
+        nbytes = max(int(_lib.gptq_workspace_bytes(m_max, d_max, 1 if act_order else 0)),
+                     int(workspace_bytes))
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         h = ctypes.c_void_p()
         with torch.cuda.device(self.device):
@@ -280,6 +294,127 @@ def gptq_dequant_matmul_tiled(ctx: Context, X, tiled, m: int, group: int, scales
                                              _ptr(tiled), m, group, scales.shape[1],
                                              _ptr(scales), _ptr(zeros), _ptr(Y)),
               "gptq_dequant_matmul_tiled")
+
+
+def gptq_lora_workspace_bytes(T: int, m: int, d: int, bits: int, n_adapters: int, rank: int,
+                              dtype=torch.bfloat16) -> int:
+    """Workspace of gptq_lora_matmul and gptq_lora_backward at these sizes (for Context)."""
+    return int(_lib.gptq_lora_workspace_bytes(T, m, d, bits, n_adapters, rank, _DTYPE_CODE[dtype]))
+
+
+def _shaped(ctx: Context, t: torch.Tensor, shape, dtypes, name):
+    """A contiguous tensor of this shape, one of these dtypes, on the context's device."""
+    if not t.is_cuda or not t.is_contiguous() or t.shape != shape or t.dtype not in dtypes or \
+            t.device != ctx.device:
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of "
+                         f"{' or '.join(map(str, dtypes))} on {ctx.device}, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+_F32, _I32 = (torch.float32,), (torch.int32,)
+
+
+def _lora_layer(ctx, T, packed, d, bits, group, group_id, scales, zeros, adapter, A, B, scaling,
+                dtype):
+    """The checked arguments that the two adapter calls share, in the C order."""
+    m, (n, R) = packed.shape[0], A.shape[:2]
+    grid = (m, scales.shape[1])
+    own = (dtype,)
+    return (T, d, _shaped(ctx, packed, (m, words_per_row(d, bits)), _I32, "packed"), m, bits, group,
+            None if group_id is None else _shaped(ctx, group_id, (d,), _I32, "group_id"), grid[1],
+            _shaped(ctx, scales, grid, _F32, "scales"), _shaped(ctx, zeros, grid, _I32, "zeros"),
+            _shaped(ctx, adapter, (T,), _I32, "adapter"), n, R,
+            _shaped(ctx, A, (n, R, d), own, "A"), _shaped(ctx, B, (n, R, m), own, "B"),
+            _shaped(ctx, scaling, (n,), _F32, "scaling"))
+
+
+def gptq_lora_matmul(ctx: Context, X, packed, d: int, bits: int, group: int, scales, zeros, adapter,
+                     A, B, scaling, Y, group_id=None, U=None):
+    """Y [T, m] = X Ŵᵀ + U B[adapter] with U [T, rank] = scaling[adapter] X A[adapter]ᵀ: the packed
+    layer with a low-rank adapter per token (adapter [T] int32, -1: none; A [n, rank, d] and
+    B [n, rank, m] of X's dtype; Y fp32 or X's dtype; U fp32, kept for gptq_lora_backward, or
+    None).  See include/gptq.h."""
+    T = X.shape[0]
+    layer = _lora_layer(ctx, T, packed, d, bits, group, group_id, scales, zeros, adapter, A, B,
+                        scaling, X.dtype)
+    rc = _lib.gptq_lora_matmul(
+        ctx.handle, _shaped(ctx, X, (T, d), _DTYPE_CODE, "X"), _DTYPE_CODE[X.dtype], *layer,
+        _shaped(ctx, Y, (T, layer[3]), (X.dtype, torch.float32), "Y"), _DTYPE_CODE[Y.dtype],
+        None if U is None else _shaped(ctx, U, (T, layer[12]), _F32, "U"))
+    if rc:
+        ctx.check(rc, "gptq_lora_matmul")
+
+
+def gptq_lora_backward(ctx: Context, dY, X, packed, d: int, bits: int, group: int, scales, zeros,
+                       adapter, A, B, scaling, U, dX=None, dA=None, dB=None, group_id=None,
+                       accumulate: bool = False):
+    """The gradients of gptq_lora_matmul: dX [T, d] (dY's dtype), dA [n, rank, d] and
+    dB [n, rank, m] (fp32; added to with accumulate), each where it is given.  X may be None
+    without dA, U without dB.  See include/gptq.h."""
+    T = dY.shape[0]
+    layer = _lora_layer(ctx, T, packed, d, bits, group, group_id, scales, zeros, adapter, A, B,
+                        scaling, dY.dtype)
+    m, n, R = layer[3], layer[11], layer[12]
+    own = (dY.dtype,)
+
+    def opt(t, shape, dtypes, name):
+        return None if t is None else _shaped(ctx, t, shape, dtypes, name)
+
+    rc = _lib.gptq_lora_backward(
+        ctx.handle, _shaped(ctx, dY, (T, m), _DTYPE_CODE, "dY"), opt(X, (T, d), own, "X"),
+        _DTYPE_CODE[dY.dtype], *layer, opt(U, (T, R), _F32, "U"), opt(dX, (T, d), own, "dX"),
+        opt(dA, (n, R, d), _F32, "dA"), opt(dB, (n, R, m), _F32, "dB"), 1 if accumulate else 0)
+    if rc:
+        ctx.check(rc, "gptq_lora_backward")
+
+
+def _rows(ctx: Context, t, shape, dtypes, name):
+    """As _shaped, but the rows may lie further apart than they are long; also that distance."""
+    if not t.is_cuda or t.shape != shape or t.dtype not in dtypes or t.device != ctx.device or \
+            (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be a {tuple(shape)} tensor with contiguous rows of "
+                         f"{' or '.join(map(str, dtypes))} on {ctx.device}, got {tuple(t.shape)} "
+                         f"{t.dtype} with strides {t.stride()} on {t.device}")
+    return t.data_ptr(), max(t.stride(0), shape[1])
+
+
+def gptq_distill_topk(ctx: Context, logits, values, indices, tau: float, loss, lse, weight=None,
+                      teacher_lse=None, dloss=None, dlogits=None):
+    """The distillation loss [T] of logits [T, V] against the teacher's top logits (values [T, K]
+    fp32 at indices [T, K] int32, -1: no entry) and the student's log-sum-exp lse [T]; with dloss
+    [T] and dlogits [T, V] also the gradient, in the same pass.  See include/gptq.h."""
+    T, V = logits.shape
+    K = values.shape[1]
+    if (dloss is None) != (dlogits is None):
+        raise ValueError("dloss and dlogits go together")
+    z, ld = _rows(ctx, logits, (T, V), _DTYPE_CODE, "logits")
+    dz, ld_grad = (None, 0) if dlogits is None else _rows(ctx, dlogits, (T, V), (logits.dtype,), "dlogits")
+    opt = lambda t, name: None if t is None else _shaped(ctx, t, (T,), _F32, name)  # noqa: E731
+    rc = _lib.gptq_distill_topk(
+        ctx.handle, z, _DTYPE_CODE[logits.dtype], T, V, ld,
+        _shaped(ctx, values, (T, K), _F32, "values"), _shaped(ctx, indices, (T, K), _I32, "indices"),
+        K, tau, opt(weight, "weight"), opt(teacher_lse, "teacher_lse"), opt(loss, "loss"),
+        opt(lse, "lse"), opt(dloss, "dloss"), dz, ld_grad)
+    if rc:
+        ctx.check(rc, "gptq_distill_topk")
+
+
+def gptq_distill_topk_backward(ctx: Context, logits, values, indices, tau: float, lse, dloss,
+                               dlogits, weight=None, teacher_lse=None):
+    """The gradient of gptq_distill_topk from the lse [T] it wrote (dlogits may be logits)."""
+    T, V = logits.shape
+    K = values.shape[1]
+    z, ld = _rows(ctx, logits, (T, V), _DTYPE_CODE, "logits")
+    dz, ld_grad = _rows(ctx, dlogits, (T, V), (logits.dtype,), "dlogits")
+    opt = lambda t, name: None if t is None else _shaped(ctx, t, (T,), _F32, name)  # noqa: E731
+    rc = _lib.gptq_distill_topk_backward(
+        ctx.handle, z, _DTYPE_CODE[logits.dtype], T, V, ld,
+        _shaped(ctx, values, (T, K), _F32, "values"), _shaped(ctx, indices, (T, K), _I32, "indices"),
+        K, tau, opt(weight, "weight"), opt(teacher_lse, "teacher_lse"), opt(lse, "lse"),
+        opt(dloss, "dloss"), dz, ld_grad)
+    if rc:
+        ctx.check(rc, "gptq_distill_topk_backward")
 
 
 def gptq_twosided_factor(ctx: Context, G):

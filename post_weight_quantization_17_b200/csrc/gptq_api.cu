@@ -1,5 +1,6 @@
 // C ABI of the library (declared and documented in include/gptq.h).
 #include <algorithm>
+#include <initializer_list>
 #include <new>
 
 #include "kernels.h"
@@ -52,6 +53,63 @@ int read_status(Ctx* c, gptq::DeviceStatus* out) {
 int clear_status(Ctx* c) {
   GPTQ_CUDA_CHECK(c, cudaMemsetAsync(c->status, 0, 2 * sizeof(int), c->stream));
   return GPTQ_OK;
+}
+
+// The adapter and distillation calls run on the context's device whichever one is current.
+struct DeviceScope {
+  int saved = -1;
+  bool ok = false;
+  explicit DeviceScope(const Ctx* c) {
+    if (cudaGetDevice(&saved) != cudaSuccess) return;
+    ok = saved == c->device || cudaSetDevice(c->device) == cudaSuccess;
+    if (saved == c->device) saved = -1;
+  }
+  ~DeviceScope() {
+    if (saved >= 0) cudaSetDevice(saved);
+  }
+};
+
+// Element alignment of a pointer (null passes: the caller tests for that).
+bool aligned_to(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == GPTQ_F32 ? 3 : 1)) == 0;
+}
+
+constexpr int64_t kLoraMaxRank = 1024, kLoraMaxAdapters = 65535;
+
+bool lora_sizes_ok(int64_t T, int64_t m, int64_t d, int bits, int64_t n, int64_t rank) {
+  return T >= 0 && T <= 65535LL * 8 && m >= 1 && m <= (1 << 24) && d >= 1 && d <= (1 << 24) &&
+         bits >= 1 && bits <= 8 && n >= 1 && n <= kLoraMaxAdapters && rank >= 1 &&
+         rank <= kLoraMaxRank;
+}
+
+bool make_lora_layer(gptq::LoraLayer* l, int64_t T, int64_t m, int64_t d, int bits, int group,
+                     int64_t n_g, const uint32_t* packed, const int32_t* group_id,
+                     const float* scales, const int32_t* zeros, int dtype, int64_t n,
+                     int64_t rank, const int32_t* adapter, const void* A, const void* B,
+                     const float* scaling) {
+  if (!lora_sizes_ok(T, m, d, bits, n, rank) || !valid_dtype(dtype) || !packed || !scales ||
+      !zeros || (T && !adapter) || !A || !B || !scaling || !(group == -1 || group > 0) || n_g < 1 ||
+      n_g > INT32_MAX || (!group_id && n_g < (group == -1 ? 1 : (d + group - 1) / group)))
+    return false;
+  for (const void* p : {(const void*)packed, (const void*)group_id, (const void*)scales,
+                        (const void*)zeros, (const void*)adapter, (const void*)scaling})
+    if (!aligned_to(p, GPTQ_F32)) return false;
+  if (!aligned_to(A, dtype) || !aligned_to(B, dtype)) return false;
+  *l = {(int)T, (int)m, (int)d, bits, group, (int)n_g, packed, group_id, scales, zeros, dtype,
+        (int)n, (int)rank, adapter, A, B, scaling};
+  return true;
+}
+
+constexpr int64_t kDistillMaxK = 2048;
+
+bool distill_ok(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                const float* values, const int32_t* indices, int64_t K, float tau,
+                const float* weight, const float* teacher_lse) {
+  return (T == 0 || (logits && values && indices)) && valid_dtype(dtype) && T >= 0 && T <= INT32_MAX && V >= 1 &&
+         V <= (1 << 24) && ld >= V && ld <= (1LL << 32) && K >= 1 && K <= kDistillMaxK &&
+         tau >= 1e-6f && tau <= 1e6f && aligned_to(logits, dtype) && aligned_to(values, GPTQ_F32) &&
+         aligned_to(indices, GPTQ_F32) && aligned_to(weight, GPTQ_F32) &&
+         aligned_to(teacher_lse, GPTQ_F32);
 }
 
 }  // namespace
@@ -410,6 +468,113 @@ int gptq_dequant_matmul_tiled(gptq_ctx* h, const void* X, int x_dtype, int64_t T
   gptq::StageScope stage(c, GPTQ_STAGE_DEQUANT);
   return gptq::dequant_matmul_tiled(c, X, x_dtype, (int)T, (int)d, tiled, (int)m, group,
                                     (int)n_g, scales, zeros, Y, part, avail);
+}
+
+size_t gptq_lora_workspace_bytes(int64_t T, int64_t m, int64_t d, int bits, int64_t n_adapters,
+                                 int64_t rank, int dtype) {
+  if (!lora_sizes_ok(T, m, d, bits, n_adapters, rank) || !valid_dtype(dtype))
+    return gptq::kStatusBytes;
+  gptq::LoraLayer l{};
+  l.T = (int)T; l.m = (int)m; l.d = (int)d; l.bits = bits;
+  l.n = (int)n_adapters; l.R = (int)rank;
+  l.dtype = dtype;
+  return gptq::lora_workspace_bytes(l);
+}
+
+int gptq_lora_matmul(gptq_ctx* h, const void* X, int x_dtype, int64_t T, int64_t d,
+                     const uint32_t* packed, int64_t m, int bits, int group,
+                     const int32_t* group_id, int64_t n_g, const float* scales,
+                     const int32_t* zeros, const int32_t* adapter, int64_t n_adapters,
+                     int64_t rank, const void* A, const void* B, const float* scaling, void* Y,
+                     int y_dtype, float* U) {
+  if (!h) return GPTQ_ERR_ARG;
+  Ctx* c = &h->c;
+  gptq::LoraLayer l{};
+  if (!make_lora_layer(&l, T, m, d, bits, group, n_g, packed, group_id, scales, zeros, x_dtype,
+                       n_adapters, rank, adapter, A, B, scaling) ||
+      (T && (!X || !Y)) || !aligned_to(X, x_dtype) || !aligned_to(Y, y_dtype) || !aligned_to(U, GPTQ_F32) ||
+      !(y_dtype == GPTQ_F32 || y_dtype == x_dtype))
+    GPTQ_SET_ERR(c, GPTQ_ERR_ARG, "lora_matmul: bad argument (T=%lld d=%lld m=%lld bits=%d group=%d n_g=%lld adapters=%lld rank=%lld)",
+                 (long long)T, (long long)d, (long long)m, bits, group, (long long)n_g,
+                 (long long)n_adapters, (long long)rank);
+  if (T == 0) return GPTQ_OK;
+  DeviceScope dev(c);
+  if (!dev.ok) GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "lora_matmul: the context's device is not usable");
+  gptq::StageScope stage(c, GPTQ_STAGE_LORA);
+  return gptq::lora_forward(c, l, X, Y, y_dtype == GPTQ_F32, U);
+}
+
+int gptq_lora_backward(gptq_ctx* h, const void* dY, const void* X, int x_dtype, int64_t T,
+                       int64_t d, const uint32_t* packed, int64_t m, int bits, int group,
+                       const int32_t* group_id, int64_t n_g, const float* scales,
+                       const int32_t* zeros, const int32_t* adapter, int64_t n_adapters,
+                       int64_t rank, const void* A, const void* B, const float* scaling,
+                       const float* U, void* dX, float* dA, float* dB, int accumulate) {
+  if (!h) return GPTQ_ERR_ARG;
+  Ctx* c = &h->c;
+  gptq::LoraLayer l{};
+  if (!make_lora_layer(&l, T, m, d, bits, group, n_g, packed, group_id, scales, zeros, x_dtype,
+                       n_adapters, rank, adapter, A, B, scaling) ||
+      !aligned_to(dY, x_dtype) || !aligned_to(X, x_dtype) || !aligned_to(U, GPTQ_F32) ||
+      !aligned_to(dX, x_dtype) || !aligned_to(dA, GPTQ_F32) || !aligned_to(dB, GPTQ_F32) ||
+      (T && (!dY || (!dX && !dA && !dB) || (dA && !X) || (dB && !U))))
+    GPTQ_SET_ERR(c, GPTQ_ERR_ARG, "lora_backward: bad argument (T=%lld d=%lld m=%lld bits=%d group=%d n_g=%lld adapters=%lld rank=%lld)",
+                 (long long)T, (long long)d, (long long)m, bits, group, (long long)n_g,
+                 (long long)n_adapters, (long long)rank);
+  DeviceScope dev(c);
+  if (!dev.ok) GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "lora_backward: the context's device is not usable");
+  gptq::StageScope stage(c, GPTQ_STAGE_LORA);
+  if (T == 0) {
+    const size_t n = (size_t)n_adapters * rank * sizeof(float);
+    if (dA && !accumulate) GPTQ_CUDA_CHECK(c, cudaMemsetAsync(dA, 0, n * d, c->stream));
+    if (dB && !accumulate) GPTQ_CUDA_CHECK(c, cudaMemsetAsync(dB, 0, n * m, c->stream));
+    return GPTQ_OK;
+  }
+  return gptq::lora_backward(c, l, dY, X, U, dX, dA, dB, accumulate);
+}
+
+int gptq_distill_topk(gptq_ctx* h, const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                      const float* values, const int32_t* indices, int64_t K, float tau,
+                      const float* weight, const float* teacher_lse, float* loss, float* lse,
+                      const float* dloss, void* dlogits, int64_t ld_grad) {
+  if (!h) return GPTQ_ERR_ARG;
+  Ctx* c = &h->c;
+  if (!distill_ok(logits, dtype, T, V, ld, values, indices, K, tau, weight, teacher_lse) ||
+      (T && (!loss || !lse)) || !aligned_to(loss, GPTQ_F32) || !aligned_to(lse, GPTQ_F32) ||
+      (T && dlogits && (!dloss || ld_grad < V || !aligned_to(dloss, GPTQ_F32) ||
+                   !aligned_to(dlogits, dtype) || (dlogits == logits && ld_grad != ld))))
+    GPTQ_SET_ERR(c, GPTQ_ERR_ARG, "distill_topk: bad argument (T=%lld V=%lld K=%lld tau=%g)",
+                 (long long)T, (long long)V, (long long)K, tau);
+  if (T == 0) return GPTQ_OK;
+  DeviceScope dev(c);
+  if (!dev.ok) GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "distill_topk: the context's device is not usable");
+  gptq::StageScope stage(c, GPTQ_STAGE_DISTILL);
+  gptq::DistillArgs p{logits, dtype, (int)T, (int)V, (int)K, ld, values, indices, tau, weight,
+                      teacher_lse, loss, lse, nullptr, dlogits ? dloss : nullptr, dlogits, ld_grad};
+  return gptq::distill(c, p);
+}
+
+int gptq_distill_topk_backward(gptq_ctx* h, const void* logits, int dtype, int64_t T, int64_t V,
+                               int64_t ld, const float* values, const int32_t* indices, int64_t K,
+                               float tau, const float* weight, const float* teacher_lse,
+                               const float* lse, const float* dloss, void* dlogits,
+                               int64_t ld_grad) {
+  if (!h) return GPTQ_ERR_ARG;
+  Ctx* c = &h->c;
+  if (!distill_ok(logits, dtype, T, V, ld, values, indices, K, tau, weight, teacher_lse) ||
+      (T && (!lse || !dloss || !dlogits)) || ld_grad < V || !aligned_to(lse, GPTQ_F32) ||
+      !aligned_to(dloss, GPTQ_F32) || !aligned_to(dlogits, dtype) ||
+      (T && dlogits == logits && ld_grad != ld))
+    GPTQ_SET_ERR(c, GPTQ_ERR_ARG, "distill_topk_backward: bad argument (T=%lld V=%lld K=%lld tau=%g)",
+                 (long long)T, (long long)V, (long long)K, tau);
+  if (T == 0) return GPTQ_OK;
+  DeviceScope dev(c);
+  if (!dev.ok)
+    GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "distill_topk_backward: the context's device is not usable");
+  gptq::StageScope stage(c, GPTQ_STAGE_DISTILL);
+  gptq::DistillArgs p{logits, dtype, (int)T, (int)V, (int)K, ld, values, indices, tau, weight,
+                      teacher_lse, nullptr, nullptr, lse, dloss, dlogits, ld_grad};
+  return gptq::distill(c, p);
 }
 
 int gptq_twosided_factor(gptq_ctx* h, float* G, int64_t k) {

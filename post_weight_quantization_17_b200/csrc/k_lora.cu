@@ -1,0 +1,288 @@
+// The packed layer with low-rank adapters of many requests: token t of a batch belongs to a request
+// that uses adapter a_t (or none), and every request shares the one packed projection,
+//   U[t]  = s[a_t] A[a_t] X[t]                       (A [n, R, d], s [n])
+//   Y[t]  = Ŵ X[t] + B[a_t]ᵀ U[t]                    (B [n, R, m])
+// and, for training the adapters on the frozen codes,
+//   G[t]  = s[a_t] B[a_t] dY[t]
+//   dX[t] = Ŵᵀ dY[t] + A[a_t]ᵀ G[t],   dA[a] = Σ_{t: a_t = a} G[t] X[t]ᵀ,   dB[a] = Σ U[t] dY[t]ᵀ.
+// A and B are both rank-major, so the four adapter products are two kinds: a contraction over the
+// features (A X, B dY) and a sum over tokens (dA, dB).
+//
+// The kernels of this file take every format (any code width, group, per-column group ids, fp32
+// activations) and run on CUDA cores, all sums in fp32 in a fixed order.
+#include "kernels.h"
+
+#include <algorithm>
+
+namespace gptq {
+
+template <class T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// The adapter of token t; an id outside [-1, n) is reported and counts as none.
+__device__ __forceinline__ int adapter_of(const int32_t* adapter, int t, int n, DeviceStatus* st) {
+  const int a = adapter[t];
+  if (a < -1 || a >= n) {
+    raise_error(st, GPTQ_ERR_ARG, t);
+    return -1;
+  }
+  return a;
+}
+
+// out[t, j] = s[a] Σ_f x[t, f] w[a, j, f]: one warp per (token, rank index).
+template <class TX>
+__global__ void __launch_bounds__(256)
+    k_lora_shrink_any(const TX* __restrict__ x, int T, int F, const TX* __restrict__ w, int n,
+                      int R, const int32_t* __restrict__ adapter, const float* __restrict__ scaling,
+                      float* __restrict__ out, DeviceStatus* st) {
+  pdl_wait();
+  pdl_release();
+  const int lane = threadIdx.x & 31;
+  const long long e = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (e >= (long long)T * R) return;
+  const int t = (int)(e / R), j = (int)(e % R);
+  const int a = adapter_of(adapter, t, n, st);
+  float s = 0.f;
+  if (a >= 0) {
+    const TX* xr = x + (long long)t * F;
+    const TX* wr = w + ((long long)a * R + j) * F;
+    for (int f = lane; f < F; f += 32) s = fmaf(to_f32<TX>(xr[f]), to_f32<TX>(wr[f]), s);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    s *= scaling[a];
+  }
+  if (lane == 0) out[e] = s;
+}
+
+struct AnyCodes {
+  const uint32_t* packed;
+  int wpr, bits, group, ng;
+  const int32_t* group_id;
+  const float* scales;
+  const int32_t* zeros;
+};
+
+// Ŵ[r, k] as the quantizer defines it, Δ (c - z) in fp32; *bad: a grid index outside [0, n_g).
+__device__ __forceinline__ float any_weight(const AnyCodes& q, long long r, int k, bool* bad) {
+  const long long bit = (long long)k * q.bits;
+  const uint32_t* row = q.packed + r * q.wpr;
+  const int w = (int)(bit >> 5), sh = (int)(bit & 31);
+  uint32_t c = row[w] >> sh;
+  if (sh + q.bits > 32) c |= row[w + 1] << (32 - sh);
+  c &= (1u << q.bits) - 1u;
+  int g = q.group_id ? q.group_id[k] : (q.group == -1 ? 0 : k / q.group);
+  if (g < 0 || g >= q.ng) {
+    *bad = true;
+    g = 0;
+  }
+  return __fmul_rn(q.scales[r * q.ng + g], (float)((int)c - q.zeros[r * q.ng + g]));
+}
+
+// Y: 128 rows x 8 tokens per CTA, one row per thread; the token's activations pass through shared
+// memory in runs of 32 columns.
+template <class TX, class TY>
+__global__ void __launch_bounds__(128)
+    k_lora_fwd_any(const TX* __restrict__ X, int T, int d, AnyCodes q, int m, int n, int R,
+                   const int32_t* __restrict__ adapter, const TX* __restrict__ B,
+                   const float* __restrict__ U, TY* __restrict__ Y, DeviceStatus* st) {
+  pdl_wait();
+  pdl_release();
+  __shared__ float xs[32][8];
+  const int r = blockIdx.x * 128 + threadIdx.x, t0 = blockIdx.y * 8;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  bool bad = false;
+  for (int k0 = 0; k0 < d; k0 += 32) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < 256; e += 128) {
+      const int t = t0 + (e >> 5), k = k0 + (e & 31);
+      xs[e & 31][e >> 5] = (t < T && k < d) ? to_f32<TX>(X[(long long)t * d + k]) : 0.f;
+    }
+    __syncthreads();
+    if (r >= m) continue;
+    const int nk = min(32, d - k0);
+    for (int k = 0; k < nk; ++k) {
+      const float w = any_weight(q, r, k0 + k, &bad);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) acc[t] = fmaf(xs[k][t], w, acc[t]);
+    }
+  }
+  if (bad) raise_error(st, GPTQ_ERR_ARG, r);
+  if (r >= m) return;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    if (t0 + t >= T) break;
+    const int a = adapter[t0 + t];
+    if (a >= 0 && a < n) {
+      const TX* b = B + (long long)a * R * m + r;
+      const float* u = U + (long long)(t0 + t) * R;
+      float s = 0.f;
+      for (int j = 0; j < R; ++j) s = fmaf(u[j], to_f32<TX>(b[(long long)j * m]), s);
+      acc[t] += s;
+    }
+    Y[(long long)(t0 + t) * m + r] = from_f32<TY>(acc[t]);
+  }
+}
+
+// dX: 128 columns x 8 tokens per CTA, one column per thread.
+template <class TX>
+__global__ void __launch_bounds__(128)
+    k_lora_dx_any(const TX* __restrict__ dY, int T, int d, AnyCodes q, int m, int n, int R,
+                  const int32_t* __restrict__ adapter, const TX* __restrict__ A,
+                  const float* __restrict__ G, TX* __restrict__ dX, DeviceStatus* st) {
+  pdl_wait();
+  pdl_release();
+  __shared__ float ys[32][8];
+  const int k = blockIdx.x * 128 + threadIdx.x, t0 = blockIdx.y * 8;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  bool bad = false;
+  for (int r0 = 0; r0 < m; r0 += 32) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < 256; e += 128) {
+      const int t = t0 + (e >> 5), r = r0 + (e & 31);
+      ys[e & 31][e >> 5] = (t < T && r < m) ? to_f32<TX>(dY[(long long)t * m + r]) : 0.f;
+    }
+    __syncthreads();
+    if (k >= d) continue;
+    const int nr = min(32, m - r0);
+    for (int r = 0; r < nr; ++r) {
+      const float w = any_weight(q, r0 + r, k, &bad);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) acc[t] = fmaf(ys[r][t], w, acc[t]);
+    }
+  }
+  if (bad) raise_error(st, GPTQ_ERR_ARG, k);
+  if (k >= d) return;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    if (t0 + t >= T) break;
+    const int a = adapter[t0 + t];
+    if (a >= 0 && a < n) {
+      const TX* w = A + (long long)a * R * d + k;
+      const float* g = G + (long long)(t0 + t) * R;
+      float s = 0.f;
+      for (int j = 0; j < R; ++j) s = fmaf(g[j], to_f32<TX>(w[(long long)j * d]), s);
+      acc[t] += s;
+    }
+    dX[(long long)(t0 + t) * d + k] = from_f32<TX>(acc[t]);
+  }
+}
+
+// out[a, j, f] (+)= Σ_{t: a_t = a} u[t, j] x[t, f] for 8 rank indices: one feature per thread.
+// A token of another adapter is skipped, not multiplied by zero, so its non-finite values stay out.
+template <class TX>
+__global__ void __launch_bounds__(128)
+    k_lora_outer_any(const float* __restrict__ u, const TX* __restrict__ x, int T, int F, int R,
+                     const int32_t* __restrict__ adapter, int accumulate, float* __restrict__ out) {
+  pdl_wait();
+  pdl_release();
+  const int f = blockIdx.x * 128 + threadIdx.x, j0 = blockIdx.y * 8, a = blockIdx.z;
+  if (f >= F) return;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < T; ++t) {
+    if (adapter[t] != a) continue;
+    const float v = to_f32<TX>(x[(long long)t * F + f]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < R) acc[j] = fmaf(u[(long long)t * R + j0 + j], v, acc[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j0 + j >= R) break;
+    float* o = out + ((long long)a * R + j0 + j) * F + f;
+    *o = accumulate ? *o + acc[j] : acc[j];
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+namespace {
+
+AnyCodes any_codes(const LoraLayer& l) {
+  return {l.packed, (int)(((long long)l.d * l.bits + 31) / 32), l.bits, l.group, l.ng, l.group_id,
+          l.scales, l.zeros};
+}
+
+template <class TX>
+int shrink_any(Ctx* c, const LoraLayer& l, const TX* x, int F, const TX* w, float* out) {
+  const long long warps = (long long)l.T * l.R;
+  GPTQ_LAUNCH(c, k_lora_shrink_any<TX>, (unsigned)((warps + 7) / 8), 256, 0, x, l.T, F, w, l.n, l.R,
+              l.adapter, l.scaling, out, c->status);
+  return GPTQ_OK;
+}
+
+template <class TX>
+int outer_any(Ctx* c, const LoraLayer& l, const float* u, const TX* x, int F, int accumulate,
+              float* out) {
+  GPTQ_LAUNCH(c, k_lora_outer_any<TX>, dim3((F + 127) / 128, (l.R + 7) / 8, l.n), 128, 0, u, x, l.T,
+              F, l.R, l.adapter, accumulate, out);
+  return GPTQ_OK;
+}
+
+template <class TX>
+int forward_any(Ctx* c, const LoraLayer& l, const TX* X, void* Y, bool y_f32, float* U) {
+  int rc = shrink_any<TX>(c, l, X, l.d, (const TX*)l.A, U);
+  if (rc) return rc;
+  const dim3 grid((l.m + 127) / 128, (l.T + 7) / 8);
+  if (y_f32)
+    GPTQ_LAUNCH(c, k_lora_fwd_any<TX, float>, grid, 128, 0, X, l.T, l.d, any_codes(l), l.m, l.n,
+                l.R, l.adapter, (const TX*)l.B, (const float*)U, (float*)Y, c->status);
+  else
+    GPTQ_LAUNCH(c, k_lora_fwd_any<TX, TX>, grid, 128, 0, X, l.T, l.d, any_codes(l), l.m, l.n, l.R,
+                l.adapter, (const TX*)l.B, (const float*)U, (TX*)Y, c->status);
+  return GPTQ_OK;
+}
+
+template <class TX>
+int backward_any(Ctx* c, const LoraLayer& l, const TX* dY, const TX* X, const float* U, TX* dX,
+                 float* dA, float* dB, int accumulate, float* G) {
+  int rc;
+  if ((dX || dA) && (rc = shrink_any<TX>(c, l, dY, l.m, (const TX*)l.B, G))) return rc;
+  if (dX)
+    GPTQ_LAUNCH(c, k_lora_dx_any<TX>, dim3((l.d + 127) / 128, (l.T + 7) / 8), 128, 0, dY, l.T, l.d,
+                any_codes(l), l.m, l.n, l.R, l.adapter, (const TX*)l.A, (const float*)G, dX,
+                c->status);
+  if (dA && (rc = outer_any<TX>(c, l, G, X, l.d, accumulate, dA))) return rc;
+  if (dB && (rc = outer_any<TX>(c, l, U, dY, l.m, accumulate, dB))) return rc;
+  return GPTQ_OK;
+}
+
+}  // namespace
+
+size_t lora_workspace_bytes(const LoraLayer& l) {
+  return kStatusBytes + 256 * 2 + (size_t)l.T * l.R * sizeof(float);
+}
+
+int lora_forward(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool y_f32, float* U) {
+  Carver cv(c);
+  float* ws_U = cv.take<float>((size_t)l.T * l.R);
+  if (!U) {
+    if (!cv.ok())
+      GPTQ_SET_ERR(c, GPTQ_ERR_NOMEM, "lora_matmul: workspace %zu < %zu bytes", c->ws_bytes, cv.off);
+    U = ws_U;
+  }
+  if (l.dtype == GPTQ_BF16)
+    return forward_any<__nv_bfloat16>(c, l, (const __nv_bfloat16*)X, Y, y_f32, U);
+  if (l.dtype == GPTQ_F16) return forward_any<__half>(c, l, (const __half*)X, Y, y_f32, U);
+  return forward_any<float>(c, l, (const float*)X, Y, true, U);
+}
+
+int lora_backward(Ctx* c, const LoraLayer& l, const void* dY, const void* X, const float* U,
+                  void* dX, float* dA, float* dB, int accumulate) {
+  Carver cv(c);
+  float* G = cv.take<float>((size_t)l.T * l.R);
+  if (!cv.ok())
+    GPTQ_SET_ERR(c, GPTQ_ERR_NOMEM, "lora_backward: workspace %zu < %zu bytes", c->ws_bytes, cv.off);
+  if (l.dtype == GPTQ_BF16)
+    return backward_any<__nv_bfloat16>(c, l, (const __nv_bfloat16*)dY, (const __nv_bfloat16*)X, U,
+                                       (__nv_bfloat16*)dX, dA, dB, accumulate, G);
+  if (l.dtype == GPTQ_F16)
+    return backward_any<__half>(c, l, (const __half*)dY, (const __half*)X, U, (__half*)dX, dA, dB,
+                                accumulate, G);
+  return backward_any<float>(c, l, (const float*)dY, (const float*)X, U, (float*)dX, dA, dB,
+                             accumulate, G);
+}
+
+}  // namespace gptq

@@ -97,6 +97,40 @@ int dequant_matmul_tiled(Ctx* c, const void* X, int x_dtype, int T, int d,
                          const uint32_t* tiled, int m, int group, int ng, const float* scales,
                          const int32_t* zeros, float* Y, float* part_ws, size_t part_floats);
 
+// ---- the packed layer with low-rank adapters (k_lora.cu)
+struct LoraLayer {
+  int T, m, d, bits, group, ng;
+  const uint32_t* packed;
+  const int32_t* group_id;
+  const float* scales;
+  const int32_t* zeros;
+  int dtype;               // of X, A, B, dY, dX
+  int n, R;
+  const int32_t* adapter;  // [T]
+  const void *A, *B;       // [n, R, d], [n, R, m]
+  const float* scaling;    // [n]
+};
+size_t lora_workspace_bytes(const LoraLayer& l);   // sizes and types only
+int lora_forward(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool y_f32, float* U);
+int lora_backward(Ctx* c, const LoraLayer& l, const void* dY, const void* X, const float* U,
+                  void* dX, float* dA, float* dB, int accumulate);
+
+// ---- distillation from a teacher's top logits (k_distill.cu)
+struct DistillArgs {
+  const void* logits;
+  int dtype, T, V, K;
+  long long ld;
+  const float* values;
+  const int32_t* indices;
+  float tau;
+  const float *weight, *teacher_lse;  // may be null
+  float *loss, *lse_out;              // null in the backward form, which takes lse_in
+  const float *lse_in, *dloss;
+  void* dlogits;
+  long long ld_grad;
+};
+int distill(Ctx* c, const DistillArgs& p);
+
 // ---- two-sided rounding (GPTQ-2D, k_twosided.cu); workspace: Y, C, etas (m n floats each) and
 // RAT (m m floats)
 int twosided_round(Ctx* c, const float* X, int m, int n, const float* RA, const float* RB,
