@@ -111,19 +111,26 @@ __device__ __forceinline__ void pdl_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// cluster_x > 1: CTAs per cluster along x (for kernels without a compile-time cluster size).
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(Ctx* c, void (*kernel)(KArgs...), dim3 grid, dim3 block,
-                              size_t smem, Args&&... args) {
+inline cudaError_t launch_pdl_cluster(Ctx* c, int cluster_x, void (*kernel)(KArgs...), dim3 grid,
+                                      dim3 block, size_t smem, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c->stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cluster_x > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster_x;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
   ++c->launches;
   if (!c->timing) return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
   // timed launch: the events serialize this kernel with its neighbours on the stream
@@ -135,6 +142,12 @@ inline cudaError_t launch_pdl(Ctx* c, void (*kernel)(KArgs...), dim3 grid, dim3 
   if (r == cudaSuccess) r = cudaEventRecord(t.stop, c->stream);
   if (r == cudaSuccess) c->timed.push_back(t);
   return r;
+}
+
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(Ctx* c, void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                              size_t smem, Args&&... args) {
+  return launch_pdl_cluster(c, 1, kernel, grid, block, smem, std::forward<Args>(args)...);
 }
 
 template <class T> __device__ __forceinline__ float to_f32(T v);

@@ -4,11 +4,26 @@
 //   loss = w τ² Σ_k p_k (log p_k - (y_{i_k} - lse)),          lse = log Σ_j exp y_j
 //   dz_i = g w τ (M q_i - Σ_{k: i_k = i} p_k),                M = Σ_k p_k
 // (g: the token's upstream gradient).
+//
+// Bound by HBM: the logits are read once and the gradients written once.  A row is split over a
+// cluster of CTAs so that each CTA's piece (about 64 KB, three CTAs to an SM) stays in shared
+// memory: all of it is requested at once with bulk copies, the running maximum and sum are formed
+// as the pieces land, the cluster joins them through distributed shared memory, and the gradient
+// is formed from the same shared memory.  Several CTAs per SM let one load while another computes.
+// Rows too long for 8 CTAs' shared memory take k_distill_long, which reads them again instead.
+#include <algorithm>
+
 #include "kernels.h"
+#include "tc_util.cuh"
 
 namespace gptq {
 
 constexpr int DS_THREADS = 256;
+constexpr int DS_WARPS = DS_THREADS / 32;
+constexpr int DS_PIECES = 8;                     // bulk copies (and barriers) of a CTA's part
+constexpr int DS_PART = 64 * 1024;               // a CTA's part of a row, where rows allow it
+constexpr int DS_PART_MAX = 160 * 1024;
+constexpr float DS_LOG2E = 1.4426950408889634f, DS_LN2 = 0.6931471805599453f;
 
 template <class T> __device__ __forceinline__ T ds_round(float v);
 template <> __device__ __forceinline__ float ds_round<float>(float v) { return v; }
@@ -41,16 +56,340 @@ __device__ __forceinline__ float ds_block(float v, bool is_max, float* red) {
   return red[32];
 }
 
-// One CTA per token.
+// 2^x, within 2 units in the last place and 0 below 2^-126.
+__device__ __forceinline__ float ds_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <class T> struct DsVec { static constexpr int N = 16 / sizeof(T); };
+
 template <class T>
-__global__ void __launch_bounds__(DS_THREADS) k_distill(DistillArgs p, DeviceStatus* st) {
+__device__ __forceinline__ void ds_unpack(const uint4& v, float (&x)[DsVec<T>::N]);
+template <> __device__ __forceinline__ void ds_unpack<float>(const uint4& v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x);
+  x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z);
+  x[3] = __uint_as_float(v.w);
+}
+template <> __device__ __forceinline__ void ds_unpack<__half>(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <> __device__ __forceinline__ void ds_unpack<__nv_bfloat16>(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+template <class T>
+__device__ __forceinline__ uint4 ds_pack(const float (&x)[DsVec<T>::N]);
+template <> __device__ __forceinline__ uint4 ds_pack<float>(const float (&x)[4]) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                    __float_as_uint(x[3]));
+}
+template <> __device__ __forceinline__ uint4 ds_pack<__half>(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <> __device__ __forceinline__ uint4 ds_pack<__nv_bfloat16>(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A running maximum and the sum of 2^(k x - k max): joins (m2, s2) into (m, s).
+__device__ __forceinline__ void ds_join(float& m, float& s, float m2, float s2, float k) {
+  const float mm = fmaxf(m, m2);
+  // an empty side (maximum -inf) has the sum 0; -inf - (-inf) must not become a factor
+  const float a = m == mm ? 1.f : ds_exp2((m - mm) * k), b = m2 == mm ? 1.f : ds_exp2((m2 - mm) * k);
+  s = s * a + s2 * b;
+  m = mm;
+}
+
+// The teacher's list of one row in shared memory, and what follows from it.
+struct DsList {
+  float *pk, *zk;
+  int32_t* ik;
+  float mass, cm, c;   // M, g w tau M, g w tau
+};
+
+// Reads the list (indices, the student's scaled logits there, the teacher's), and turns the
+// teacher's logits into probabilities.  Returns L; every thread of the CTA.
+template <class T>
+__device__ __forceinline__ float ds_read_list(const DistillArgs& p, int t, const T* z, float it,
+                                              DsList& l, float* red, DeviceStatus* st) {
+  float most = -INFINITY;
+  bool bad = false;
+  for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
+    int i = p.indices[(long long)t * p.K + k];
+    if (i < -1 || i >= p.V) {
+      bad = true;
+      i = -1;
+    }
+    l.ik[k] = i;
+    l.pk[k] = i < 0 ? -INFINITY : p.values[(long long)t * p.K + k] * it;
+    l.zk[k] = i < 0 ? 0.f : to_f32<T>(z[i]) * it;
+    most = fmaxf(most, l.pk[k]);
+  }
+  if (bad) raise_error(st, GPTQ_ERR_ARG, t);
+  float L;
+  if (p.teacher_lse) {
+    L = p.teacher_lse[t];
+  } else {
+    most = ds_block(most, true, red);
+    float s = 0.f;
+    for (int k = threadIdx.x; k < p.K; k += DS_THREADS)
+      s += l.pk[k] == -INFINITY ? 0.f : ds_exp2((l.pk[k] - most) * DS_LOG2E);
+    L = most + logf(ds_block(s, false, red));
+  }
+  return L;
+}
+
+// log p - log q summed over the list into *kl where asked for, the probabilities into l.pk and
+// their sum into l.mass.
+__device__ __forceinline__ void ds_finish_list(const DistillArgs& p, float L, float lse, DsList& l,
+                                               float* kl_out, float* red) {
+  float kl = 0.f, mass = 0.f;
+  for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
+    const float lp = l.pk[k] - L;
+    const float q = l.pk[k] == -INFINITY ? 0.f : ds_exp2(lp * DS_LOG2E);
+    l.pk[k] = q;
+    mass += q;
+    if (q != 0.f) kl += q * (lp - (l.zk[k] - lse));
+  }
+  l.mass = ds_block(mass, false, red);
+  if (kl_out) *kl_out = ds_block(kl, false, red);
+}
+
+// The gradient at the listed entries inside [lo, hi), over what the dense pass wrote there: the
+// first listing of an index writes the sum of all its listings, rounded once.  After a
+// __syncthreads that follows the dense pass.
+template <class T>
+__device__ __forceinline__ void ds_listed(const DistillArgs& p, T* dz, const DsList& l, float lse,
+                                          long long lo, long long hi) {
+  for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
+    const int i = l.ik[k];
+    if (i < lo || i >= hi) continue;
+    bool first = true;
+    float sum = 0.f;
+    for (int j = 0; j < p.K; ++j)
+      if (l.ik[j] == i) {
+        first = first && j >= k;
+        sum += l.pk[j];
+      }
+    if (first) dz[i] = ds_round<T>(fmaf(l.cm, ds_exp2((l.zk[k] - lse) * DS_LOG2E), -l.c * sum));
+  }
+}
+
+__device__ __forceinline__ void ds_store_remote(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// One cluster per token; `part`: 16-byte vectors of the row per CTA.  LOSS: the loss and lse are
+// formed (else lse is given); GRAD: the gradient is written.
+template <class T, bool LOSS, bool GRAD>
+__global__ void __launch_bounds__(DS_THREADS)
+    k_distill(DistillArgs p, int part, DeviceStatus* st, long long budget) {
+  constexpr int N = DsVec<T>::N;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bar[DS_PIECES];
+  __shared__ float red[33], joined[2 * 8];
+  uint4* row = reinterpret_cast<uint4*>(smem);
+  DsList l;
+  l.pk = reinterpret_cast<float*>(smem + (size_t)part * 16);
+  l.zk = l.pk + p.K;
+  l.ik = reinterpret_cast<int32_t*>(l.zk + p.K);
+  const int C = (int)(gridDim.x / p.T);
+  const int t = blockIdx.x / C, rank = blockIdx.x % C;
+  const T* z = (const T*)p.logits + (long long)t * p.ld;
+  T* dz = GRAD ? (T*)p.dlogits + (long long)t * p.ld_grad : nullptr;
+  // the row as `head` scalars, nvec aligned vectors and `tail` scalars
+  const int head = min(p.V, (int)((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / (int)sizeof(T));
+  const int nvec = (p.V - head) / N, tail0 = head + nvec * N;
+  const int v0 = min(nvec, rank * part), nv = min(nvec, v0 + part) - v0;
+  const int per = (nv + DS_PIECES - 1) / DS_PIECES;
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < DS_PIECES; ++b) tc::mbar_init(&bar[b], 1);
+    tc::mbar_fence_init();
+  }
+  if (LOSS && C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
   pdl_release();
-  extern __shared__ char smem[];
-  float* pk = reinterpret_cast<float*>(smem);               // teacher's probabilities [K]
-  float* zk = pk + p.K;                                     // the student's logits there
-  int32_t* ik = reinterpret_cast<int32_t*>(zk + p.K);       // and where (-1: no entry)
+  const float w = p.weight ? p.weight[t] : 1.f;
+  if (w == 0.f) {   // the whole cluster takes this branch
+    if (LOSS && rank == 0 && threadIdx.x == 0) {
+      p.loss[t] = 0.f;
+      p.lse_out[t] = 0.f;
+    }
+    if (GRAD) {
+      const int lo = rank ? head + v0 * N : 0, hi = rank == C - 1 ? p.V : head + (v0 + nv) * N;
+      for (int i = lo + threadIdx.x; i < hi; i += DS_THREADS) dz[i] = ds_round<T>(0.f);
+    }
+    if (LOSS && C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    return;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint4* src = reinterpret_cast<const uint4*>(z + head) + v0;
+    for (int b = 0; b < DS_PIECES; ++b) {
+      const int i = b * per, n = min(per, nv - i);
+      if (n <= 0) break;
+      tc::mbar_expect_tx(&bar[b], n * 16);
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+          ::"r"(tc::smem_u32(row + i)), "l"(src + i), "r"(n * 16), "r"(tc::smem_u32(&bar[b]))
+          : "memory");
+    }
+  }
+  // while the row is on its way: the scalars at its ends (rank 0's), and the list
+  const float it = 1.f / p.tau, k2 = it * DS_LOG2E;
+  int edge = -1;
+  if (rank == 0 && (int)threadIdx.x < 32) {
+    if ((int)threadIdx.x < head) edge = threadIdx.x;
+    if ((int)threadIdx.x >= 16 && tail0 + (int)threadIdx.x - 16 < p.V)
+      edge = tail0 + threadIdx.x - 16;
+  }
+  const float edge_z = edge >= 0 ? to_f32<T>(z[edge]) : -INFINITY;
+  const float L = ds_read_list<T>(p, t, z, it, l, red, st);
+  float lse;
+  if (LOSS) {
+    float m = edge_z, s = edge_z == -INFINITY ? 0.f : 1.f;
+    if (edge_z != edge_z) s = edge_z;   // NaN: fmaxf drops it from the maximum, not from the sum
+    for (int b = 0; b < DS_PIECES; ++b) {
+      const int i0 = b * per, i1 = min(nv, i0 + per);
+      if (i0 >= i1) break;
+      if (!tc::mbar_wait(&bar[b], 0, budget)) {
+        raise_error(st, GPTQ_ERR_TIMEOUT, 61);
+        tc::mbar_wait(&bar[b], 0, kDrainCycles);
+      }
+      for (int i = i0 + threadIdx.x; i < i1; i += 2 * DS_THREADS) {
+        float x[2][N];
+        ds_unpack<T>(row[i], x[0]);
+        const bool two = i + DS_THREADS < i1;
+        if (two) ds_unpack<T>(row[i + DS_THREADS], x[1]);
+        float mx = m;
+#pragma unroll
+        for (int e = 0; e < N; ++e) mx = fmaxf(mx, x[0][e]);
+        if (two) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) mx = fmaxf(mx, x[1][e]);
+        }
+        const float mk = mx == -INFINITY ? 0.f : mx * k2;
+        s *= m == mx ? 1.f : ds_exp2((m - mx) * k2);
+        m = mx;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) s0 += ds_exp2(fmaf(x[0][e], k2, -mk));
+        if (two) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) s1 += ds_exp2(fmaf(x[1][e], k2, -mk));
+        }
+        s += s0 + s1;
+      }
+    }
+    // join the threads, then the cluster, both in a fixed order
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      ds_join(m, s, m2, s2, k2);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) {
+      red[2 * (threadIdx.x >> 5)] = m;
+      red[2 * (threadIdx.x >> 5) + 1] = s;
+    }
+    __syncthreads();
+    m = red[0];
+    s = red[1];
+#pragma unroll
+    for (int i = 1; i < DS_WARPS; ++i) ds_join(m, s, red[2 * i], red[2 * i + 1], k2);
+    if (C > 1) {
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every CTA has started
+      if ((int)threadIdx.x < C) {
+        ds_store_remote(tc::map_to_rank(&joined[2 * rank], threadIdx.x), m);
+        ds_store_remote(tc::map_to_rank(&joined[2 * rank + 1], threadIdx.x), s);
+      }
+      tc::cluster_sync();   // also: every listed logit was read before any gradient is written
+      m = joined[0];
+      s = joined[1];
+      for (int i = 1; i < C; ++i) ds_join(m, s, joined[2 * i], joined[2 * i + 1], k2);
+    }
+    lse = fmaf(m, it, logf(s));
+  } else {
+    lse = p.lse_in[t];
+  }
+  float kl;
+  ds_finish_list(p, L, lse, l, LOSS ? &kl : nullptr, red);
+  if (LOSS && rank == 0 && threadIdx.x == 0) {
+    p.loss[t] = w * p.tau * p.tau * kl;
+    p.lse_out[t] = lse;
+  }
+  if (!GRAD) return;
+  l.c = p.dloss[t] * w * p.tau;
+  l.cm = l.c * l.mass;
+  const float lse2 = lse * DS_LOG2E;
+  if (edge >= 0) dz[edge] = ds_round<T>(l.cm * ds_exp2(fmaf(edge_z, k2, -lse2)));
+  T* out = dz + head + (long long)v0 * N;
+  const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+  for (int b = 0; b < DS_PIECES; ++b) {
+    const int i0 = b * per, i1 = min(nv, i0 + per);
+    if (i0 >= i1) break;
+    if (!LOSS && !tc::mbar_wait(&bar[b], 0, budget)) {
+      raise_error(st, GPTQ_ERR_TIMEOUT, 62);
+      tc::mbar_wait(&bar[b], 0, kDrainCycles);
+    }
+    for (int i = i0 + threadIdx.x; i < i1; i += DS_THREADS) {
+      float x[N];
+      ds_unpack<T>(row[i], x);
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[e] = l.cm * ds_exp2(fmaf(x[e], k2, -lse2));
+      if (wide) {
+        __stcs(reinterpret_cast<uint4*>(out) + i, ds_pack<T>(x));
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) out[(long long)i * N + e] = ds_round<T>(x[e]);
+      }
+    }
+  }
+  __syncthreads();
+  // this CTA's own elements only (rank 0 also has the row's ends)
+  const int lo = head + v0 * N, hi = lo + nv * N;
+  ds_listed<T>(p, dz, l, lse, lo, hi);
+  if (rank == 0) {
+    ds_listed<T>(p, dz, l, lse, 0, head);
+    ds_listed<T>(p, dz, l, lse, tail0, p.V);
+  }
+}
+
+// Rows that do not fit a cluster's shared memory: one CTA per token, which reads them again.
+template <class T>
+__global__ void __launch_bounds__(DS_THREADS) k_distill_long(DistillArgs p, DeviceStatus* st) {
+  pdl_wait();
+  pdl_release();
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[33];
+  DsList l;
+  l.pk = reinterpret_cast<float*>(smem);
+  l.zk = l.pk + p.K;
+  l.ik = reinterpret_cast<int32_t*>(l.zk + p.K);
   const int t = blockIdx.x;
   const T* z = (const T*)p.logits + (long long)t * p.ld;
   const float w = p.weight ? p.weight[t] : 1.f;
@@ -64,85 +403,73 @@ __global__ void __launch_bounds__(DS_THREADS) k_distill(DistillArgs p, DeviceSta
       for (int i = threadIdx.x; i < p.V; i += DS_THREADS) dz[i] = ds_round<T>(0.f);
     return;
   }
-  const float it = 1.f / p.tau;
-  float most = -INFINITY;
-  bool bad = false;
-  for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
-    int i = p.indices[(long long)t * p.K + k];
-    if (i < -1 || i >= p.V) {
-      bad = true;
-      i = -1;
-    }
-    ik[k] = i;
-    pk[k] = i < 0 ? -INFINITY : p.values[(long long)t * p.K + k] * it;
-    zk[k] = i < 0 ? 0.f : to_f32<T>(z[i]) * it;
-    most = fmaxf(most, pk[k]);
-  }
-  if (bad) raise_error(st, GPTQ_ERR_ARG, t);
-  float L;
-  if (p.teacher_lse) {
-    L = p.teacher_lse[t];
-  } else {
-    most = ds_block(most, true, red);
-    float s = 0.f;
-    for (int k = threadIdx.x; k < p.K; k += DS_THREADS)
-      s += pk[k] == -INFINITY ? 0.f : expf(pk[k] - most);
-    L = most + logf(ds_block(s, false, red));
-  }
+  const float it = 1.f / p.tau, k2 = it * DS_LOG2E;
+  const float L = ds_read_list<T>(p, t, z, it, l, red, st);
   float lse;
   if (p.lse_in) {
     lse = p.lse_in[t];
   } else {
     float mx = -INFINITY;
     for (int i = threadIdx.x; i < p.V; i += DS_THREADS) mx = fmaxf(mx, to_f32<T>(z[i]));
-    mx = ds_block(mx, true, red) * it;
+    mx = ds_block(mx, true, red);
     float s = 0.f;
-    for (int i = threadIdx.x; i < p.V; i += DS_THREADS) s += expf(fmaf(to_f32<T>(z[i]), it, -mx));
-    lse = mx + logf(ds_block(s, false, red));
+    for (int i = threadIdx.x; i < p.V; i += DS_THREADS)
+      s += ds_exp2(fmaf(to_f32<T>(z[i]), k2, -mx * k2));
+    lse = fmaf(mx, it, logf(ds_block(s, false, red)));
   }
-  float kl = 0.f, mass = 0.f;
-  for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
-    const float lp = pk[k] - L, q = pk[k] == -INFINITY ? 0.f : expf(lp);
-    pk[k] = q;
-    mass += q;
-    if (q != 0.f) kl += q * (lp - (zk[k] - lse));
-  }
-  mass = ds_block(mass, false, red);
-  if (p.loss) {
-    kl = ds_block(kl, false, red);
-    if (threadIdx.x == 0) {
-      p.loss[t] = w * p.tau * p.tau * kl;
-      p.lse_out[t] = lse;
-    }
+  float kl;
+  ds_finish_list(p, L, lse, l, &kl, red);
+  if (p.loss && threadIdx.x == 0) {
+    p.loss[t] = w * p.tau * p.tau * kl;
+    p.lse_out[t] = lse;
   }
   if (!dz) return;
-  const float c = p.dloss[t] * w * p.tau, cm = c * mass;
+  l.c = p.dloss[t] * w * p.tau;
+  l.cm = l.c * l.mass;
   for (int i = threadIdx.x; i < p.V; i += DS_THREADS)
-    dz[i] = ds_round<T>(cm * expf(fmaf(to_f32<T>(z[i]), it, -lse)));
+    dz[i] = ds_round<T>(l.cm * ds_exp2(fmaf(to_f32<T>(z[i]), k2, -lse * DS_LOG2E)));
   __syncthreads();
-  // the listed entries: the first listing of an index writes the sum of all its listings
-  for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
-    if (ik[k] < 0) continue;
-    bool first = true;
-    float sum = 0.f;
-    for (int j = 0; j < p.K; ++j)
-      if (ik[j] == ik[k]) {
-        if (j < k) first = false;
-        sum += pk[j];
-      }
-    if (first) dz[ik[k]] = ds_round<T>(fmaf(cm, expf(zk[k] - lse), -c * sum));
-  }
+  ds_listed<T>(p, dz, l, lse, 0, p.V);
 }
 
-int distill(Ctx* c, const DistillArgs& p) {
-  const size_t smem = (size_t)p.K * 12;
-  if (p.dtype == GPTQ_BF16)
-    GPTQ_LAUNCH(c, k_distill<__nv_bfloat16>, p.T, DS_THREADS, smem, p, c->status);
-  else if (p.dtype == GPTQ_F16)
-    GPTQ_LAUNCH(c, k_distill<__half>, p.T, DS_THREADS, smem, p, c->status);
-  else
-    GPTQ_LAUNCH(c, k_distill<float>, p.T, DS_THREADS, smem, p, c->status);
+namespace {
+
+template <class T, bool LOSS, bool GRAD>
+int launch_distill(Ctx* c, const DistillArgs& p, int C, int part, size_t smem) {
+  GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(k_distill<T, LOSS, GRAD>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, LOSS ? C : 1, k_distill<T, LOSS, GRAD>,
+                                        dim3((unsigned)(p.T * C)), dim3(DS_THREADS), smem, p, part,
+                                        c->status, c->timeout_cycles));
   return GPTQ_OK;
+}
+
+template <class T>
+int distill_as(Ctx* c, const DistillArgs& p) {
+  const size_t list = (size_t)p.K * 12;
+  const long long nvec = std::max<long long>(1, (long long)p.V / DsVec<T>::N);
+  // CTAs per row: parts of at most DS_PART bytes; with few rows more, down to 8 KB parts, so that
+  // the SMs share the work (the loss of 5 rows of 32000 fp32 logits: {SMALL}).
+  int C = 1;
+  while (C < 8 && nvec * 16 > (long long)C * DS_PART) C *= 2;
+  while (C < 8 && (long long)p.T * C * 2 <= c->num_sms && nvec * 16 > (long long)C * 8192) C *= 2;
+  const long long part = (nvec + C - 1) / C;
+  if (part * 16 > DS_PART_MAX || (long long)p.T * C > INT32_MAX) {
+    GPTQ_LAUNCH(c, k_distill_long<T>, p.T, DS_THREADS, list, p, c->status);
+    return GPTQ_OK;
+  }
+  const size_t smem = (size_t)part * 16 + list;
+  if (!p.loss) return launch_distill<T, false, true>(c, p, C, (int)part, smem);
+  if (!p.dlogits) return launch_distill<T, true, false>(c, p, C, (int)part, smem);
+  return launch_distill<T, true, true>(c, p, C, (int)part, smem);
+}
+
+}  // namespace
+
+int distill(Ctx* c, const DistillArgs& p) {
+  if (p.dtype == GPTQ_BF16) return distill_as<__nv_bfloat16>(c, p);
+  if (p.dtype == GPTQ_F16) return distill_as<__half>(c, p);
+  return distill_as<float>(c, p);
 }
 
 }  // namespace gptq
