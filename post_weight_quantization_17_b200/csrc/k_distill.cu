@@ -20,7 +20,7 @@ namespace gptq {
 
 constexpr int DS_THREADS = 256;
 constexpr int DS_WARPS = DS_THREADS / 32;
-constexpr int DS_PIECES = 8;                     // bulk copies (and barriers) of a CTA's part
+constexpr int DS_PIECES = 4;                     // bulk copies (and barriers) of a CTA's part
 constexpr int DS_PART = 64 * 1024;               // a CTA's part of a row, where rows allow it
 constexpr int DS_PART_MAX = 160 * 1024;
 constexpr float DS_LOG2E = 1.4426950408889634f, DS_LN2 = 0.6931471805599453f;
@@ -113,6 +113,57 @@ template <> __device__ __forceinline__ uint4 ds_pack<__nv_bfloat16>(const float 
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Two fp32 operations per instruction.
+__device__ __forceinline__ uint64_t ds_pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void ds_split(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t ds_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t ds_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t ds_mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// x[e] <- 2^(k x[e] + b) for a vector.
+template <int N>
+__device__ __forceinline__ void ds_exp2_all(float (&x)[N], uint64_t k, uint64_t b) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    ds_split(ds_fma2(ds_pair(x[e], x[e + 1]), k, b), x[e], x[e + 1]);
+    x[e] = ds_exp2(x[e]);
+    x[e + 1] = ds_exp2(x[e + 1]);
+  }
+}
+// The largest of a vector's values (NaN is passed over).
+template <class T> __device__ __forceinline__ float ds_max(const uint4& v);
+template <> __device__ __forceinline__ float ds_max<float>(const uint4& v) {
+  return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+               fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+template <> __device__ __forceinline__ float ds_max<__half>(const uint4& v) {
+  const __half2* h = reinterpret_cast<const __half2*>(&v);
+  const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+template <> __device__ __forceinline__ float ds_max<__nv_bfloat16>(const uint4& v) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+  const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  return fmaxf(__low2float(m), __high2float(m));
 }
 
 // A running maximum and the sum of 2^(k x - k max): joins (m2, s2) into (m, s).
@@ -281,27 +332,27 @@ __global__ void __launch_bounds__(DS_THREADS)
         tc::mbar_wait(&bar[b], 0, kDrainCycles);
       }
       for (int i = i0 + threadIdx.x; i < i1; i += 2 * DS_THREADS) {
-        float x[2][N];
-        ds_unpack<T>(row[i], x[0]);
+        const uint4 v0 = row[i];
         const bool two = i + DS_THREADS < i1;
-        if (two) ds_unpack<T>(row[i + DS_THREADS], x[1]);
-        float mx = m;
-#pragma unroll
-        for (int e = 0; e < N; ++e) mx = fmaxf(mx, x[0][e]);
-        if (two) {
-#pragma unroll
-          for (int e = 0; e < N; ++e) mx = fmaxf(mx, x[1][e]);
-        }
+        const uint4 v1 = two ? row[i + DS_THREADS] : v0;
+        const float mx = fmaxf(m, fmaxf(ds_max<T>(v0), ds_max<T>(v1)));
         const float mk = mx == -INFINITY ? 0.f : mx * k2;
-        s *= m == mx ? 1.f : ds_exp2((m - mx) * k2);
+        if (m != mx) s *= ds_exp2((m - mx) * k2);
         m = mx;
-        float s0 = 0.f, s1 = 0.f;
+        float x[N];
+        ds_unpack<T>(v0, x);
+        ds_exp2_all<N>(x, ds_pair(k2, k2), ds_pair(-mk, -mk));
+        uint64_t sum = ds_pair(x[0], x[1]);
 #pragma unroll
-        for (int e = 0; e < N; ++e) s0 += ds_exp2(fmaf(x[0][e], k2, -mk));
+        for (int e = 2; e < N; e += 2) sum = ds_add2(sum, ds_pair(x[e], x[e + 1]));
         if (two) {
+          ds_unpack<T>(v1, x);
+          ds_exp2_all<N>(x, ds_pair(k2, k2), ds_pair(-mk, -mk));
 #pragma unroll
-          for (int e = 0; e < N; ++e) s1 += ds_exp2(fmaf(x[1][e], k2, -mk));
+          for (int e = 0; e < N; e += 2) sum = ds_add2(sum, ds_pair(x[e], x[e + 1]));
         }
+        float s0, s1;
+        ds_split(sum, s0, s1);
         s += s0 + s1;
       }
     }
@@ -349,18 +400,22 @@ __global__ void __launch_bounds__(DS_THREADS)
   if (edge >= 0) dz[edge] = ds_round<T>(l.cm * ds_exp2(fmaf(edge_z, k2, -lse2)));
   T* out = dz + head + (long long)v0 * N;
   const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-  for (int b = 0; b < DS_PIECES; ++b) {
-    const int i0 = b * per, i1 = min(nv, i0 + per);
+  const uint64_t kk = ds_pair(k2, k2), off = ds_pair(-lse2, -lse2), cc = ds_pair(l.cm, l.cm);
+  // with the loss formed all pieces have landed, else they are waited for one by one
+  for (int b = 0; b < (LOSS ? 1 : DS_PIECES); ++b) {
+    const int i0 = LOSS ? 0 : b * per, i1 = LOSS ? nv : min(nv, i0 + per);
     if (i0 >= i1) break;
     if (!LOSS && !tc::mbar_wait(&bar[b], 0, budget)) {
       raise_error(st, GPTQ_ERR_TIMEOUT, 62);
       tc::mbar_wait(&bar[b], 0, kDrainCycles);
     }
+#pragma unroll 2
     for (int i = i0 + threadIdx.x; i < i1; i += DS_THREADS) {
       float x[N];
       ds_unpack<T>(row[i], x);
+      ds_exp2_all<N>(x, kk, off);
 #pragma unroll
-      for (int e = 0; e < N; ++e) x[e] = l.cm * ds_exp2(fmaf(x[e], k2, -lse2));
+      for (int e = 0; e < N; e += 2) ds_split(ds_mul2(ds_pair(x[e], x[e + 1]), cc), x[e], x[e + 1]);
       if (wide) {
         __stcs(reinterpret_cast<uint4*>(out) + i, ds_pack<T>(x));
       } else {
@@ -369,11 +424,37 @@ __global__ void __launch_bounds__(DS_THREADS)
       }
     }
   }
+  // The listed entries of this CTA's own part, over what was just written there.  Their slots in
+  // the row's shared memory, no longer needed, find indices that are listed twice: every listing
+  // leaves its number, one of each index's listings finds its own again and writes the sum over
+  // all of them (in list order, whichever listing it is).
   __syncthreads();
-  // this CTA's own elements only (rank 0 also has the row's ends)
   const int lo = head + v0 * N, hi = lo + nv * N;
-  ds_listed<T>(p, dz, l, lse, lo, hi);
-  if (rank == 0) {
+  uint16_t* tag = reinterpret_cast<uint16_t*>(row);
+  constexpr int TS = sizeof(T) / 2;
+  for (int k = threadIdx.x; k < p.K; k += DS_THREADS)
+    if (l.ik[k] >= lo && l.ik[k] < hi) tag[(l.ik[k] - lo) * TS] = (uint16_t)k;
+  __syncthreads();
+  constexpr int kTwice = 1 << 30;
+  for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
+    const int i = l.ik[k] & ~kTwice;
+    if (l.ik[k] < 0 || i < lo || i >= hi) continue;
+    const int winner = tag[(i - lo) * TS];
+    if (winner != k) atomicOr(&l.ik[winner], kTwice);
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
+    const int i = l.ik[k] & ~kTwice;
+    if (l.ik[k] < 0 || i < lo || i >= hi || tag[(i - lo) * TS] != k) continue;
+    float sum = l.pk[k];
+    if (l.ik[k] & kTwice) {
+      sum = 0.f;
+      for (int j = 0; j < p.K; ++j)
+        if (l.ik[j] >= 0 && (l.ik[j] & ~kTwice) == i) sum += l.pk[j];
+    }
+    dz[i] = ds_round<T>(fmaf(l.cm, ds_exp2((l.zk[k] - lse) * DS_LOG2E), -l.c * sum));
+  }
+  if (rank == 0) {   // the row's ends
     ds_listed<T>(p, dz, l, lse, 0, head);
     ds_listed<T>(p, dz, l, lse, tail0, p.V);
   }
