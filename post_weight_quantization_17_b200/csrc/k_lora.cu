@@ -10,28 +10,11 @@
 //
 // The kernels of this file take every format (any code width, group, per-column group ids, fp32
 // activations) and run on CUDA cores, all sums in fp32 in a fixed order.
-#include "kernels.h"
-
 #include <algorithm>
 
+#include "lora_util.cuh"
+
 namespace gptq {
-
-template <class T> __device__ __forceinline__ T from_f32(float v);
-template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
-  return __float2bfloat16_rn(v);
-}
-
-// The adapter of token t; an id outside [-1, n) is reported and counts as none.
-__device__ __forceinline__ int adapter_of(const int32_t* adapter, int t, int n, DeviceStatus* st) {
-  const int a = adapter[t];
-  if (a < -1 || a >= n) {
-    raise_error(st, GPTQ_ERR_ARG, t);
-    return -1;
-  }
-  return a;
-}
 
 // out[t, j] = s[a] Σ_f x[t, f] w[a, j, f]: one warp per (token, rank index).
 template <class TX>
@@ -251,12 +234,25 @@ int backward_any(Ctx* c, const LoraLayer& l, const TX* dY, const TX* X, const fl
 
 }  // namespace
 
+// The formats that run on tensor cores: 16-bit activations, codes of 1 to 4 bits, one grid per row
+// or per multiple of 128 columns.
+static bool lora_tensor_format(const LoraLayer& l) {
+  return l.dtype != GPTQ_F32 && l.bits <= 4 && !l.group_id && (l.group == -1 || l.group % 128 == 0);
+}
+
 size_t lora_workspace_bytes(const LoraLayer& l) {
-  return kStatusBytes + 256 * 2 + (size_t)l.T * l.R * sizeof(float);
+  size_t floats = (size_t)l.T * l.R;
+  if (l.T <= kLoraSmallTokens) floats = std::max(floats, lora_small_floats(l));
+  return kStatusBytes + 256 * 2 + floats * sizeof(float);
 }
 
 int lora_forward(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool y_f32, float* U) {
   Carver cv(c);
+  if (lora_tensor_format(l) && lora_small_applies(l, X)) {
+    float* ws = cv.take<float>(0);
+    const size_t floats = cv.ok() ? (c->ws_bytes - cv.off) / sizeof(float) : 0;
+    return lora_forward_small(c, l, X, Y, y_f32, U, ws, floats);
+  }
   float* ws_U = cv.take<float>((size_t)l.T * l.R);
   if (!U) {
     if (!cv.ok())

@@ -115,6 +115,16 @@ int lora_forward(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool y_f32,
 int lora_backward(Ctx* c, const LoraLayer& l, const void* dY, const void* X, const float* U,
                   void* dX, float* dA, float* dB, int accumulate);
 
+// up to kLoraSmallTokens tokens (k_lora_small.cu): X and A 16-byte aligned, d % 8 == 0
+constexpr int kLoraSmallTokens = 32;
+bool lora_small_applies(const LoraLayer& l, const void* X);
+size_t lora_small_floats(const LoraLayer& l);
+int lora_forward_small(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool y_f32, float* U,
+                       float* ws, size_t ws_floats);
+// out [T, F] = Σ_splits part [splits, T, F] + U w[adapter], U = scaling Σ_chunks upart
+int lora_join(Ctx* c, const LoraLayer& l, const float* part, int splits, int F, const float* upart,
+              int chunks, const void* w, void* out, bool out_f32, float* U);
+
 // ---- distillation from a teacher's top logits (k_distill.cu)
 struct DistillArgs {
   const void* logits;

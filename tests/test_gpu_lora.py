@@ -193,7 +193,7 @@ def test_empty_batch(ctx):
     assert (dA == 0).all() and (dB == 0).all()
 
 
-def test_bad_ids_are_reported(ctx):
+def test_bad_ids_and_zeros_are_reported(ctx):
     c = Case(8, 64, 256, 4, 128, 8, 2, BF, "mixed", 9)
     good = c.adapter.clone()
     for bad in (2, -2, 2 ** 31 - 1, -2 ** 31):
@@ -206,6 +206,12 @@ def test_bad_ids_are_reported(ctx):
         with pytest.raises(G.GPTQError) as e:
             G.gptq_sync_status(ctx)
         assert e.value.code == G.GPTQ_ERR_ARG and torch.equal(Y, want)
+    c.adapter.copy_(good)
+    c.zeros[5, 1] = 16
+    G.gptq_lora_matmul(ctx, c.X, *c.layer(), Y)
+    with pytest.raises(G.GPTQError) as e:
+        G.gptq_sync_status(ctx)
+    assert e.value.code == G.GPTQ_ERR_ARG
 
 
 def test_refusals(ctx):
