@@ -219,6 +219,15 @@ int forward_any(Ctx* c, const LoraLayer& l, const TX* X, void* Y, bool y_f32, fl
 }
 
 template <class TX>
+int outers(Ctx* c, const LoraLayer& l, const TX* dY, const TX* X, const float* U, float* dA,
+           float* dB, int accumulate, const float* G) {
+  int rc;
+  if (dA && (rc = outer_any<TX>(c, l, G, X, l.d, accumulate, dA))) return rc;
+  if (dB && (rc = outer_any<TX>(c, l, U, dY, l.m, accumulate, dB))) return rc;
+  return GPTQ_OK;
+}
+
+template <class TX>
 int backward_any(Ctx* c, const LoraLayer& l, const TX* dY, const TX* X, const float* U, TX* dX,
                  float* dA, float* dB, int accumulate, float* G) {
   int rc;
@@ -227,12 +236,17 @@ int backward_any(Ctx* c, const LoraLayer& l, const TX* dY, const TX* X, const fl
     GPTQ_LAUNCH(c, k_lora_dx_any<TX>, dim3((l.d + 127) / 128, (l.T + 7) / 8), 128, 0, dY, l.T, l.d,
                 any_codes(l), l.m, l.n, l.R, l.adapter, (const TX*)l.A, (const float*)G, dX,
                 c->status);
-  if (dA && (rc = outer_any<TX>(c, l, G, X, l.d, accumulate, dA))) return rc;
-  if (dB && (rc = outer_any<TX>(c, l, U, dY, l.m, accumulate, dB))) return rc;
-  return GPTQ_OK;
+  return outers<TX>(c, l, dY, X, U, dA, dB, accumulate, G);
 }
 
 }  // namespace
+
+int lora_shrink_any(Ctx* c, const LoraLayer& l, const void* x, int F, const void* w, float* out) {
+  if (l.dtype == GPTQ_BF16)
+    return shrink_any<__nv_bfloat16>(c, l, (const __nv_bfloat16*)x, F, (const __nv_bfloat16*)w, out);
+  if (l.dtype == GPTQ_F16) return shrink_any<__half>(c, l, (const __half*)x, F, (const __half*)w, out);
+  return shrink_any<float>(c, l, (const float*)x, F, (const float*)w, out);
+}
 
 // The formats that run on tensor cores: 16-bit activations, codes of 1 to 4 bits, one grid per row
 // or per multiple of 128 columns.
@@ -243,7 +257,10 @@ static bool lora_tensor_format(const LoraLayer& l) {
 size_t lora_workspace_bytes(const LoraLayer& l) {
   size_t floats = (size_t)l.T * l.R;
   if (l.T <= kLoraSmallTokens) floats = std::max(floats, lora_small_floats(l));
-  return kStatusBytes + 256 * 2 + floats * sizeof(float);
+  size_t b = 256 * 2 + floats * sizeof(float);
+  if (l.dtype != GPTQ_F32 && l.bits <= 4)   // the backward pass keeps G in front
+    b = std::max(b, 256 + (size_t)l.T * l.R * sizeof(float) + lora_tc_bytes(l));
+  return kStatusBytes + b;
 }
 
 int lora_forward(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool y_f32, float* U) {
@@ -253,6 +270,7 @@ int lora_forward(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool y_f32,
     const size_t floats = cv.ok() ? (c->ws_bytes - cv.off) / sizeof(float) : 0;
     return lora_forward_small(c, l, X, Y, y_f32, U, ws, floats);
   }
+  if (lora_tensor_format(l)) return lora_tc(c, l, true, X, Y, y_f32, U, kStatusBytes);
   float* ws_U = cv.take<float>((size_t)l.T * l.R);
   if (!U) {
     if (!cv.ok())
@@ -271,6 +289,14 @@ int lora_backward(Ctx* c, const LoraLayer& l, const void* dY, const void* X, con
   float* G = cv.take<float>((size_t)l.T * l.R);
   if (!cv.ok())
     GPTQ_SET_ERR(c, GPTQ_ERR_NOMEM, "lora_backward: workspace %zu < %zu bytes", c->ws_bytes, cv.off);
+  if (lora_tensor_format(l)) {
+    int rc;
+    if ((dX || dA) && (rc = lora_tc(c, l, false, dY, dX, false, G, cv.off))) return rc;
+    if (l.dtype == GPTQ_BF16)
+      return outers<__nv_bfloat16>(c, l, (const __nv_bfloat16*)dY, (const __nv_bfloat16*)X, U, dA,
+                                   dB, accumulate, G);
+    return outers<__half>(c, l, (const __half*)dY, (const __half*)X, U, dA, dB, accumulate, G);
+  }
   if (l.dtype == GPTQ_BF16)
     return backward_any<__nv_bfloat16>(c, l, (const __nv_bfloat16*)dY, (const __nv_bfloat16*)X, U,
                                        (__nv_bfloat16*)dX, dA, dB, accumulate, G);

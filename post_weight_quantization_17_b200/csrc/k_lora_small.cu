@@ -21,7 +21,7 @@ namespace gptq {
 constexpr int LS_THREADS = 256;
 // 16-row tiles per warp: two halve the reads of X per code; at 32 tokens the registers of their
 // sums leave room for one (two spilled).
-constexpr int ls_row_tiles(int token_tiles) { return token_tiles == 4 ? 1 : 2; }
+inline constexpr int ls_row_tiles(int token_tiles) { return token_tiles == 4 ? 1 : 2; }
 // rows per CTA: 4 row warps x 2 column warps
 constexpr int ls_rows(int token_tiles) { return 64 * ls_row_tiles(token_tiles); }
 constexpr int LS_KC = 4096;                    // columns per warp of A X
@@ -115,12 +115,12 @@ __global__ void __launch_bounds__(LS_THREADS, 2) k_lora_small(SmallParams p, Dev
     small_shrink<BF16>(p, st);
     return;
   }
-  constexpr int LS_MT = ls_row_tiles(NT);
+  constexpr int LS_MT = NT == 4 ? 1 : 2;
   __shared__ float joined[4][32][LS_MT * NT * 4 + 1];
   const int bid = blockIdx.x - p.shrink_ctas;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wr = warp & 3, wk = warp >> 2, g = lane >> 2, t4 = lane & 3;
-  const int row0 = (bid % p.row_ctas) * ls_rows(NT) + wr * (LS_MT * 16) + g, split = bid / p.row_ctas;
+  const int row0 = (bid % p.row_ctas) * (64 * LS_MT) + wr * (LS_MT * 16) + g, split = bid / p.row_ctas;
   const int n = min(p.steps, (split + 1) * p.per) - split * p.per;
   const int s0 = split * p.per + (wk ? (n + 1) / 2 : 0), s1 = split * p.per + (wk ? n : (n + 1) / 2);
   float acc[LS_MT][NT][4] = {};
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(LJ_THREADS)
 #pragma unroll
   for (int j = 0; j < LJ_AHEAD; ++j)
     if (a >= 0 && j < R) first[j] = wr[(long long)j * F];
-  const float s = a >= 0 ? scaling[a] : 0.f;
+  const float s = a >= 0 && scaling ? scaling[a] : 1.f;
   pdl_wait();
   pdl_release();
   for (int j = threadIdx.x; j < R; j += LJ_THREADS) {
@@ -265,12 +265,12 @@ __global__ void __launch_bounds__(LJ_THREADS)
 }
 
 int lora_join(Ctx* c, const LoraLayer& l, const float* part, int splits, int F, const float* upart,
-              int chunks, const void* w, void* out, bool out_f32, float* U) {
+              int chunks, const float* scaling, const void* w, void* out, bool out_f32, float* U) {
   const dim3 grid((F + LJ_THREADS - 1) / LJ_THREADS, l.T);
   const size_t smem = l.R * sizeof(float);
 #define GPTQ_JOIN(TX, TY)                                                                       \
   GPTQ_LAUNCH(c, k_lora_join<TX, TY>, grid, LJ_THREADS, smem, part, splits, l.T, F, upart, chunks, \
-              l.n, l.R, l.adapter, l.scaling, (const TX*)w, (TY*)out, U)
+              l.n, l.R, l.adapter, scaling, (const TX*)w, (TY*)out, U)
   if (l.dtype == GPTQ_BF16) {
     if (out_f32) GPTQ_JOIN(__nv_bfloat16, float);
     else GPTQ_JOIN(__nv_bfloat16, __nv_bfloat16);
@@ -374,7 +374,7 @@ int lora_forward_small(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool 
     default: rc = launch_small<4>(c, p, grid, bf); break;
   }
   if (rc) return rc;
-  return lora_join(c, l, p.part, splits, l.m, p.upart, p.chunks, l.B, Y, y_f32, U);
+  return lora_join(c, l, p.part, splits, l.m, p.upart, p.chunks, l.scaling, l.B, Y, y_f32, U);
 }
 
 }  // namespace gptq

@@ -1,0 +1,936 @@
+// The packed layer with adapters for many tokens, on tcgen05: both directions of
+//   forward   out[t, r] = Σ_k X[t, k] Ŵ[r, k]  + Σ_j U[t, j] B[a_t, j, r]
+//   backward  out[t, k] = Σ_r dY[t, r] Ŵ[r, k] + Σ_j G[t, j] A[a_t, j, k]
+// as D[feature, token] tiles of 128 x BN.  The weight operand is made from the codes on the way into
+// shared memory; the stage's image is the same in both directions (row = weight row, 128 bytes = 64
+// columns, 128-byte swizzle), read K-major forward (the contraction runs along the row) and MN-major
+// backward (it runs down the rows), so one kernel serves both.
+//
+//   Forward: the stage holds (c - z), exact in 16 bits; the group's Δ multiplies each 128-column
+//   partial sum in fp32 as it is taken out of TMEM, so Ŵ is never rounded.
+//   Backward: Δ differs along the contraction, so it has to be in the operand: Δ (c - z) is rounded
+//   once to the 16-bit type, as (c - z) Δ_hi + (c - z) Δ_lo with Δ split in two 16-bit parts.  Its
+//   error is that of a 16-bit weight, half a step, the same size as the rounding of dX itself.  (fp16
+//   operands carry a factor of 256, taken out at the end, so that small Δ stay normal numbers.)
+//   Adapters: each adapter that occurs among the tile's tokens ("slot") adds one more partial sum,
+//   whose operands are the adapter's 16-bit rows and U in two tf32 parts (22 bits), both fp32 in
+//   shared memory (kind::tf32); the epilogue adds it to that adapter's tokens only, so one request's
+//   non-finite values never reach another's.
+//
+// Roles (one CTA per SM, persistent over tiles):
+//   warp 0        TMA producer of the tokens' operand (BN rows x 128 bytes per stage)
+//   warp 1        MMA issuer, owner of TMEM (two partial-sum buffers of BN columns)
+//   warps 4-7     the weight operand: codes global -> registers (several stages ahead) -> shared
+//   warps 8-15    epilogue: TMEM -> fp32 sums in registers -> out, or a split's partial
+// Few tokens: the contraction is split over CTAs and k_lora_join adds the splits and the adapter.
+#include <algorithm>
+#include <cstring>
+
+#include "lora_util.cuh"
+#include "tc_util.cuh"
+
+namespace gptq {
+
+constexpr int LT_THREADS = 512;
+constexpr int LT_A_BYTES = 128 * 128;      // weight operand of a stage
+constexpr int LT_AHEAD = 4;                // stages whose codes are in flight
+constexpr float LT_F16_SCALE = 256.f;
+
+template <int BN>
+struct LtCfg {
+  static constexpr int X_BYTES = BN * 128;
+  static constexpr int STAGE = LT_A_BYTES + X_BYTES;
+  static constexpr int NS = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
+  static constexpr int SMEM = NS * STAGE + 1024 + 256;
+  static constexpr int EBN = BN / 2;       // tokens per epilogue thread
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct LtParams {
+  int M, K;                 // features out, contraction length
+  int T, m, ng, wpr;
+  int group_steps;          // groups in 128-column steps; 0: one grid per row
+  const uint32_t* packed;   // 4-bit codes, rows of wpr words (a multiple of 4), 16-byte aligned
+  const float* scales;
+  const int32_t* zeros;
+  int mtiles, ttiles, splits;
+  int units, per;           // the contraction in 128-column steps (forward) or 64-row stages
+                            // (backward): in all and per split
+  int T_rows;               // rows of one part of the split U
+  int rank_chunks;          // 32-rank chunks; 0: no adapter partials (split contraction)
+  int R, n;
+  const int32_t* adapter;
+  const void* w;            // [n, R, M] 16-bit
+  const int32_t* slots;     // per token tile: count, then the adapters that occur in it
+  void* out;                // [T, M]
+  int out_f32;
+  float* part;              // [splits, T, M] or null
+  uint32_t idesc, idesc_tf32;
+};
+
+__device__ __forceinline__ bool lt_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+// Waits for a phase, suspended in hardware between tries; false after `budget` cycles.
+__device__ __forceinline__ bool lt_wait(uint64_t* bar, uint32_t parity, long long budget) {
+  if (lt_try(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!lt_try(bar, parity))
+    if (clock64() - t0 > budget) return false;
+  return true;
+}
+__device__ __forceinline__ bool lt_wait_warp(uint64_t* bar, uint32_t parity, long long budget) {
+  return __all_sync(0xffffffffu, lt_wait(bar, parity, budget));
+}
+
+// A position in a ring of N stages or buffers.
+template <int N> struct LtRing {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// One work item: a tile of features x tokens and a range of the contraction.
+struct LtTile {
+  int f0, t0, nt, split, u0, u1;
+  __device__ __forceinline__ LtTile(const LtParams& p, int i, int BN) {
+    const int mt = i % p.mtiles, r = i / p.mtiles;
+    nt = r % p.ttiles;
+    split = r / p.ttiles;
+    f0 = mt * 128;
+    t0 = nt * BN;
+    u0 = split * p.per;
+    u1 = min(p.units, u0 + p.per);
+  }
+};
+
+template <bool FWD, int BN, bool BF16>
+__global__ void __launch_bounds__(LT_THREADS, 1)
+    k_lora_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
+              const __grid_constant__ LtParams p, DeviceStatus* st, long long budget) {
+  using Cfg = LtCfg<BN>;
+  constexpr int NS = Cfg::NS, EBN = Cfg::EBN, ND = 2;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full_x = reinterpret_cast<uint64_t*>(smem + NS * Cfg::STAGE);
+  uint64_t* full_a = full_x + NS;
+  uint64_t* empty = full_a + NS;
+  uint64_t* d_full = empty + NS;
+  uint64_t* d_empty = d_full + ND;
+  uint64_t* drain = d_empty + ND;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int items = p.mtiles * p.ttiles * p.splits;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      tc::mbar_init(&full_x[s], 1);
+      tc::mbar_init(&full_a[s], 4);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < ND; ++b) {
+      tc::mbar_init(&d_full[b], 1);
+      tc::mbar_init(&d_empty[b], 8);
+    }
+    tc::mbar_init(drain, 1);
+    *abort_flag = 0;
+    tc::mbar_fence_init();
+    tc::prefetch_tmap(&tmX);
+    tc::prefetch_tmap(&tmU);
+  }
+  if (warp == 1) tc::tmem_alloc(tmem_slot, ND * BN);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  // The kernel right before (A X or B dY of this call) has itself waited for everything earlier, so
+  // the layer, X and dY may be read now; only its own results (slots, the split U) wait for it.
+  pdl_release();
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------------- tokens' operand
+      LtRing<NS> ring;
+      int issued = 0;
+      bool ok = true, waited = false;
+      auto stage = [&](const CUtensorMap* map, int x, int y) {
+        if (!ok) return;
+        if (!lt_wait(&empty[ring.i], ring.phase ^ 1u, budget)) {
+          raise_error(st, GPTQ_ERR_TIMEOUT, 71);
+          *abort_flag = 1;
+          ok = false;
+          return;
+        }
+        tc::mbar_expect_tx(&full_x[ring.i], Cfg::X_BYTES);
+        tc::tma_load_2d(smem + ring.i * Cfg::STAGE + LT_A_BYTES, map, &full_x[ring.i], x, y);
+        ring.next();
+        ++issued;
+      };
+      for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
+        const LtTile t(p, i, BN);
+        const int k1 = FWD ? 2 * t.u1 : t.u1;
+        for (int k = FWD ? 2 * t.u0 : t.u0; k < k1 && ok; ++k) stage(&tmX, k * 64, t.t0);
+        if (!p.rank_chunks) continue;
+        if (!waited) pdl_wait();
+        waited = true;
+        const int count = p.slots[t.nt * (BN + 1)];
+        for (int s = 0; s < count && ok; ++s)
+          for (int c = 0; c < 2 * p.rank_chunks && ok; ++c)
+            stage(&tmU, (c >> 1) * 32, (c & 1) * p.T_rows + t.t0);
+      }
+      // every copy this thread issued has landed before the CTA may exit
+      const int left = min(issued, NS);
+      for (int s = 0; s < left; ++s) {
+        const int j = issued - left + s;
+        if (!lt_wait(&full_x[j % NS], (uint32_t)(j / NS) & 1u, kDrainCycles))
+          raise_error(st, GPTQ_ERR_TIMEOUT, 72);
+      }
+    } else if (warp == 1 && lane == 0) {
+      // -------------------------------------------------------------- MMA issuer
+      LtRing<NS> ring;
+      LtRing<ND> dr;
+      bool ok = true, any = false, waited = false;
+      // one partial sum of `stages` stages
+      auto partial = [&](int stages, bool tf32) {
+        if (!ok) return;
+        if (!lt_wait(&d_empty[dr.i], dr.phase ^ 1u, budget)) {
+          raise_error(st, GPTQ_ERR_TIMEOUT, 73);
+          *abort_flag = 1;
+          ok = false;
+          return;
+        }
+        tc::fence_after_sync();
+        const uint32_t d = tmem + dr.i * BN;
+        for (int s = 0; s < stages; ++s) {
+          if (!lt_wait(&full_x[ring.i], ring.phase, budget) ||
+              !lt_wait(&full_a[ring.i], ring.phase, budget)) {
+            raise_error(st, GPTQ_ERR_TIMEOUT, 74);
+            *abort_flag = 1;
+            ok = false;
+            return;
+          }
+          tc::fence_after_sync();
+          const uint32_t a = tc::smem_u32(smem + ring.i * Cfg::STAGE), b = a + LT_A_BYTES;
+          if (tf32) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_tf32(d, tc::sdesc_sw128(a + kk * 32, 16, 1024),
+                           tc::sdesc_sw128(b + kk * 32, 16, 1024), p.idesc_tf32,
+                           (s | kk) ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_f16(d,
+                          FWD ? tc::sdesc_sw128(a + kk * 32, 16, 1024)
+                              : tc::sdesc_sw128(a + kk * 2048, 8192, 1024),
+                          tc::sdesc_sw128(b + kk * 32, 16, 1024), p.idesc, (s | kk) ? 1u : 0u);
+          }
+          any = true;
+          tc::mma_commit(&empty[ring.i]);
+          ring.next();
+        }
+        tc::mma_commit(&d_full[dr.i]);
+        dr.next();
+      };
+      for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
+        const LtTile t(p, i, BN);
+        if (FWD)
+          for (int u = t.u0; u < t.u1 && ok; ++u) partial(2, false);
+        else
+          partial(t.u1 - t.u0, false);
+        if (!p.rank_chunks) continue;
+        if (!waited) pdl_wait();
+        waited = true;
+        const int count = p.slots[t.nt * (BN + 1)];
+        for (int s = 0; s < count && ok; ++s) partial(2 * p.rank_chunks, true);
+      }
+      // every MMA has completed before TMEM is freed
+      if (any) {
+        tc::mma_commit(drain);
+        if (!lt_wait(drain, 0, kDrainCycles)) raise_error(st, GPTQ_ERR_TIMEOUT, 75);
+      }
+    }
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    // ---------------------------------------------------------------- weight operand
+    const int tid = threadIdx.x - 128;
+    LtRing<NS> ring;
+    bool ok = true, waited = false, bad = false;
+    // Forward: thread = weight row, two 16-byte pieces (64 codes) per stage.  Backward: 64 rows x
+    // four pieces (128 columns) per stage, two per thread; eight threads with the same piece of eight
+    // rows store to eight different 16-byte columns of the swizzled image.
+    const int q = (tid >> 3) & 3, brow = (tid & 7) + 8 * (tid >> 5);
+    uint4 code[LT_AHEAD][2];
+    float delta[LT_AHEAD][2];
+    int zero[LT_AHEAD][2];
+    for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
+      const LtTile t(p, i, BN);
+      const int k0 = FWD ? 2 * t.u0 : t.u0, k1 = FWD ? 2 * t.u1 : t.u1;
+      const int bgi = p.group_steps ? (t.f0 / 128) / p.group_steps : 0;
+      auto fetch = [&](int k, uint4 (&cd)[2], float (&dl)[2], int (&zr)[2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = FWD ? t.f0 + tid : 64 * k + brow + 32 * h;
+          const int word = FWD ? 8 * k + 4 * h : t.f0 / 8 + 4 * q;
+          const bool in = row < p.m && word < p.wpr && k < k1;
+          cd[h] = in ? *reinterpret_cast<const uint4*>(p.packed + (long long)row * p.wpr + word)
+                     : make_uint4(0, 0, 0, 0);
+          if (FWD && h) continue;   // one grid column per stage
+          const int gi = FWD ? (p.group_steps ? (k / 2) / p.group_steps : 0) : bgi;
+          const long long at = (long long)row * p.ng + gi;
+          zr[h] = in ? p.zeros[at] : 0;
+          if (!FWD) dl[h] = in ? p.scales[at] : 0.f;
+        }
+      };
+#pragma unroll
+      for (int u = 0; u < LT_AHEAD; ++u) fetch(k0 + u, code[u], delta[u], zero[u]);
+      for (int kb = k0; kb < k1 && ok; kb += LT_AHEAD) {
+#pragma unroll
+        for (int u = 0; u < LT_AHEAD; ++u) {
+          const int k = kb + u;
+          if (k >= k1 || !ok) break;
+          if (!lt_wait_warp(&empty[ring.i], ring.phase ^ 1u, budget)) {
+            raise_error(st, GPTQ_ERR_TIMEOUT, 76);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          uint8_t* dst = smem + ring.i * Cfg::STAGE;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            int z = zero[u][FWD ? 0 : h];
+            if (z < 0 || z > 15) {
+              bad = true;
+              z = 0;
+            }
+            const uint32_t zz = zero_pair<BF16>(z);
+            const uint32_t words[4] = {code[u][h].x, code[u][h].y, code[u][h].z, code[u][h].w};
+            uint32_t hi2 = 0, lo2 = 0;
+            if (!FWD) {
+              if (BF16) {
+                const __nv_bfloat16 hi = __float2bfloat16_rn(delta[u][h]);
+                const __nv_bfloat16 lo = __float2bfloat16_rn(delta[u][h] - __bfloat162float(hi));
+                const __nv_bfloat162 a = __halves2bfloat162(hi, hi), b = __halves2bfloat162(lo, lo);
+                hi2 = *reinterpret_cast<const uint32_t*>(&a);
+                lo2 = *reinterpret_cast<const uint32_t*>(&b);
+              } else {
+                if (!(fabsf(delta[u][h]) < 17.f)) bad = true;
+                const float ds = delta[u][h] * LT_F16_SCALE;
+                const __half hi = __float2half_rn(ds);
+                const __half lo = __float2half_rn(ds - __half2float(hi));
+                const __half2 a = __halves2half2(hi, hi), b = __halves2half2(lo, lo);
+                hi2 = *reinterpret_cast<const uint32_t*>(&a);
+                lo2 = *reinterpret_cast<const uint32_t*>(&b);
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              uint32_t v[4];
+              centered8<BF16>(words[w], zz, v);
+              if (!FWD) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (BF16) {
+                    const __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&v[e]);
+                    const __nv_bfloat162 r =
+                        __hfma2(c, *reinterpret_cast<const __nv_bfloat162*>(&hi2),
+                                __hmul2(c, *reinterpret_cast<const __nv_bfloat162*>(&lo2)));
+                    v[e] = *reinterpret_cast<const uint32_t*>(&r);
+                  } else {
+                    const __half2 c = *reinterpret_cast<const __half2*>(&v[e]);
+                    const __half2 r = __hfma2(c, *reinterpret_cast<const __half2*>(&hi2),
+                                              __hmul2(c, *reinterpret_cast<const __half2*>(&lo2)));
+                    v[e] = *reinterpret_cast<const uint32_t*>(&r);
+                  }
+                }
+              }
+              const int row = FWD ? tid : brow + 32 * h;
+              const int chunk = FWD ? 4 * h + w : 4 * (q & 1) + w;
+              *reinterpret_cast<uint4*>(dst + (FWD ? 0 : (q >> 1) * 8192) + row * 128 +
+                                        ((chunk ^ (row & 7)) << 4)) =
+                  make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&full_a[ring.i]);
+          ring.next();
+          fetch(k + LT_AHEAD, code[u], delta[u], zero[u]);
+        }
+      }
+      if (!p.rank_chunks || !ok) continue;
+      if (!waited) pdl_wait();
+      waited = true;
+      const int32_t* slots = p.slots + t.nt * (BN + 1);
+      const int count = slots[0], f = t.f0 + tid;
+      for (int s = 0; s < count && ok; ++s) {
+        const uint16_t* w = (const uint16_t*)p.w + (long long)slots[1 + s] * p.R * p.M + f;
+        for (int c = 0; c < p.rank_chunks && ok; ++c) {
+          uint32_t v[16];   // 32 ranks of this feature, two to a word
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const uint32_t e = (f < p.M && 32 * c + j < p.R) ? w[(long long)(32 * c + j) * p.M] : 0u;
+            if (j & 1) v[j / 2] |= e << 16;
+            else v[j / 2] = e;
+          }
+          for (int half = 0; half < 2; ++half) {   // against U's high and low parts
+            if (!lt_wait_warp(&empty[ring.i], ring.phase ^ 1u, budget)) {
+              raise_error(st, GPTQ_ERR_TIMEOUT, 77);
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+            uint8_t* dst = smem + ring.i * Cfg::STAGE + tid * 128;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 a = pair_f32<BF16>(v[2 * e]), b = pair_f32<BF16>(v[2 * e + 1]);
+              *reinterpret_cast<float4*>(dst + ((e ^ (tid & 7)) << 4)) =
+                  make_float4(a.x, a.y, b.x, b.y);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&full_a[ring.i]);
+            ring.next();
+          }
+        }
+      }
+    }
+    if (bad) raise_error(st, GPTQ_ERR_ARG, tid);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    // ---------------------------------------------------------------- epilogue
+    const int half = (warp - 8) >> 2, r = 32 * (warp & 3) + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * EBN;
+    LtRing<ND> dr;
+    bool ok = true, waited = false;
+    for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
+      const LtTile t(p, i, BN);
+      const int f = t.f0 + r, tok = t.t0 + half * EBN;
+      const float* srow = p.scales + (long long)min(f, p.m - 1) * p.ng;   // forward: f is a weight row
+      float acc[EBN];
+#pragma unroll
+      for (int e = 0; e < EBN; ++e) acc[e] = 0.f;
+      auto take = [&](float factor, const uint32_t* mask) {
+        if (!ok) return;
+        if (!lt_wait_warp(&d_full[dr.i], dr.phase, budget)) {
+          raise_error(st, GPTQ_ERR_TIMEOUT, 78);
+          *abort_flag = 1;
+          ok = false;
+          return;
+        }
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < EBN / 32; ++c) {
+          uint32_t v[32];
+          tc::tmem_ld32(lane_base + dr.i * BN + c * 32, v);
+          if (mask) {   // an adapter's partial: its own tokens only
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((mask[c] >> e) & 1u) acc[c * 32 + e] += __uint_as_float(v[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              acc[c * 32 + e] = fmaf(factor, __uint_as_float(v[e]), acc[c * 32 + e]);
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&d_empty[dr.i]);
+        dr.next();
+      };
+      if (FWD) {
+        float next = srow[p.group_steps ? t.u0 / p.group_steps : 0];
+        for (int u = t.u0; u < t.u1 && ok; ++u) {
+          const float delta = next;
+          if (u + 1 < t.u1) next = srow[p.group_steps ? (u + 1) / p.group_steps : 0];
+          take(delta, nullptr);
+        }
+      } else {
+        take(BF16 ? 1.f : 1.f / LT_F16_SCALE, nullptr);
+      }
+      if (p.rank_chunks && ok) {
+        if (!waited) pdl_wait();
+        waited = true;
+        const int32_t* slots = p.slots + t.nt * (BN + 1);
+        const int count = slots[0];
+        for (int s = 0; s < count && ok; ++s) {
+          const int a = slots[1 + s];
+          uint32_t mask[EBN / 32];
+#pragma unroll
+          for (int c = 0; c < EBN / 32; ++c) {
+            const int tt = tok + 32 * c + lane;
+            mask[c] = __ballot_sync(0xffffffffu, tt < p.T && p.adapter[tt] == a);
+          }
+          take(1.f, mask);
+        }
+      }
+      if (!ok || f >= p.M) continue;
+      if (p.part) {
+        float* o = p.part + ((long long)t.split * p.T + tok) * p.M + f;
+#pragma unroll
+        for (int e = 0; e < EBN; ++e)
+          if (tok + e < p.T) o[(long long)e * p.M] = acc[e];
+      } else if (p.out_f32) {
+        float* o = (float*)p.out + (long long)tok * p.M + f;
+#pragma unroll
+        for (int e = 0; e < EBN; ++e)
+          if (tok + e < p.T) o[(long long)e * p.M] = acc[e];
+      } else {
+        using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+        T16* o = (T16*)p.out + (long long)tok * p.M + f;
+#pragma unroll
+        for (int e = 0; e < EBN; ++e)
+          if (tok + e < p.T) o[(long long)e * p.M] = from_f32<T16>(acc[e]);
+      }
+    }
+  }
+  // whoever follows may rely on the kernel before this one being done, too
+  pdl_wait();
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, ND * BN);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// U = s A X (or G = s B dY): 32 tokens per CTA, the features over its 8 warps and over a cluster's
+// CTAs, on mma.sync straight from global memory (16 bytes a lane; tokens and adapter rows share the
+// tensor instruction's free column order).  Every adapter among the 32 tokens takes a pass over the
+// tile's features; a token keeps its own adapter's.  Writes U [T, R], its two tf32 parts
+// [2, T_rows, Rp] (zero behind R), and the lists of adapters per tile of BN tokens.
+constexpr int LU_THREADS = 256;
+
+struct ShrinkParams {
+  const void *x, *w;     // [T, F], [n, R, F]
+  int T, F, n, R, Rp, T_rows;
+  const int32_t* adapter;
+  const float* scaling;
+  float* U;              // or null
+  float* parts;          // or null
+  int32_t* slots;        // or null
+  int BN, ttiles;
+  int shrink_ctas, cluster;
+};
+
+__device__ __forceinline__ void write_low_rank(const ShrinkParams& p, int t, int j, float u) {
+  if (p.U && j < p.R) p.U[(long long)t * p.R + j] = u;
+  if (p.parts) {
+    const float hi = tc::tf32_rna(u);
+    // a non-finite or huge value has no low part
+    const float lo = fabsf(hi) <= 3.0e38f ? u - hi : 0.f;
+    p.parts[(long long)t * p.Rp + j] = fabsf(u) <= 3.0e38f ? hi : u;
+    p.parts[((long long)p.T_rows + t) * p.Rp + j] = lo;
+  }
+}
+
+// The adapters that occur among the BN tokens of tile `nt`, in order of their first token.
+__device__ __forceinline__ void list_slots(const ShrinkParams& p, int nt) {
+  __shared__ int ids[256];
+  __shared__ int counts[8];
+  const int tid = threadIdx.x, t = nt * p.BN + tid;
+  int a = (tid < p.BN && t < p.T) ? p.adapter[t] : -1;
+  if (a < 0 || a >= p.n) a = -1;
+  ids[tid] = a;
+  __syncthreads();
+  bool first = a >= 0;
+  for (int i = 0; i < tid && first; ++i) first = ids[i] != a;
+  const uint32_t b = __ballot_sync(0xffffffffu, first);
+  if ((tid & 31) == 0) counts[tid >> 5] = __popc(b);
+  __syncthreads();
+  int at = __popc(b & ((1u << (tid & 31)) - 1u)), total = 0;
+  for (int i = 0; i < 8; ++i) {
+    if (i < (tid >> 5)) at += counts[i];
+    total += counts[i];
+  }
+  int32_t* out = p.slots + nt * (p.BN + 1);
+  if (first) out[1 + at] = a;
+  if (tid == 0) out[0] = total;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(LU_THREADS) k_lora_shrink(ShrinkParams p, DeviceStatus* st) {
+  pdl_wait();
+  pdl_release();
+  __shared__ float sums[8][32][64 / 4 + 1];   // a quarter of the ranks at a time, per warp
+  __shared__ float total[32 * 64];
+  const int cl = p.cluster, rank = blockIdx.x % cl;
+  if ((int)blockIdx.x >= p.shrink_ctas) {
+    if ((int)blockIdx.x - p.shrink_ctas < p.ttiles) list_slots(p, blockIdx.x - p.shrink_ctas);
+    return;   // whole clusters of list CTAs: no cluster barrier
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int t0 = (int)(blockIdx.x / cl) * 32;
+  int id = t0 + lane < p.T ? adapter_of(p.adapter, t0 + lane, p.n, st) : -1;
+  // features in steps of 64, spread over the cluster's CTAs and their warps in contiguous runs
+  const int steps = (p.F + 63) / 64, lanes = cl * 8, per = (steps + lanes - 1) / lanes;
+  const int s0 = min(steps, (rank * 8 + warp) * per), s1 = min(steps, s0 + per);
+  // tokens without an adapter
+  if (rank == 0)
+    for (int e = threadIdx.x; e < 32 * p.Rp; e += LU_THREADS) {
+      const int t = t0 + e / p.Rp;
+      if (t < p.T) {
+        const int a = p.adapter[t];
+        if (a < 0 || a >= p.n) write_low_rank(p, t, e % p.Rp, 0.f);
+      }
+    }
+  uint32_t todo = __ballot_sync(0xffffffffu, id >= 0);
+  while (todo) {
+    const int a = __shfl_sync(0xffffffffu, id, __ffs(todo) - 1);
+    const uint32_t mine = __ballot_sync(0xffffffffu, id == a);
+    todo &= ~mine;
+    for (int j0 = 0; j0 < p.Rp; j0 += 64) {
+      const int ntile = min(8, (p.R - j0 + 7) / 8);   // <= 0 behind R cannot occur: Rp - R < 32
+      float acc[2][8][4] = {};
+      const uint16_t* xb = (const uint16_t*)p.x + (long long)t0 * p.F;
+      const uint16_t* wb = (const uint16_t*)p.w + ((long long)a * p.R + j0) * p.F;
+      for (int s = s0; s < s1; ++s) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int k = s * 64 + hh * 32 + t4 * 8;
+          const bool in = k < p.F;
+          uint4 xv[2][2];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int row = 16 * mt + 8 * h + g;
+              xv[mt][h] = (in && t0 + row < p.T)
+                              ? *reinterpret_cast<const uint4*>(xb + (long long)row * p.F + k)
+                              : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+          for (int nt = 0; nt < 8; ++nt) {
+            if (nt >= ntile) break;
+            const int j = 8 * nt + g;
+            const uint4 wv = (in && j0 + j < p.R)
+                                 ? *reinterpret_cast<const uint4*>(wb + (long long)j * p.F + k)
+                                 : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              mma16816<BF16>(acc[mt][nt], xv[mt][0].x, xv[mt][1].x, xv[mt][0].y, xv[mt][1].y, wv.x,
+                             wv.y);
+              mma16816<BF16>(acc[mt][nt], xv[mt][0].z, xv[mt][1].z, xv[mt][0].w, xv[mt][1].w, wv.z,
+                             wv.w);
+            }
+          }
+        }
+      }
+      // join the warps (fixed order), 16 ranks at a time
+#pragma unroll
+      for (int quarter = 0; quarter < 4; ++quarter) {
+        __syncthreads();
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int n2 = 0; n2 < 2; ++n2)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sums[warp][16 * mt + 8 * (i >> 1) + g][8 * n2 + 2 * t4 + (i & 1)] =
+                  acc[mt][2 * quarter + n2][i];
+        __syncthreads();
+        for (int e = threadIdx.x; e < 32 * 16; e += LU_THREADS) {
+          float v = 0.f;
+#pragma unroll
+          for (int w = 0; w < 8; ++w) v += sums[w][e >> 4][e & 15];
+          total[(e >> 4) * 64 + 16 * quarter + (e & 15)] = v;
+        }
+      }
+      if (cl > 1) tc::cluster_sync();
+      else __syncthreads();
+      if (rank == 0) {
+        const float scale = p.scaling[a];
+        for (int e = threadIdx.x; e < 32 * 64; e += LU_THREADS) {
+          const int row = e >> 6, j = j0 + (e & 63);
+          if (j >= p.Rp || !((mine >> row) & 1u)) continue;
+          float v = total[e];
+          for (int c = 1; c < cl; ++c) {
+            float u;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                         : "=f"(u)
+                         : "r"(tc::map_to_rank(&total[e], c))
+                         : "memory");
+            v += u;
+          }
+          write_low_rank(p, t0 + row, j, j < p.R ? v * scale : 0.f);
+        }
+      }
+      if (cl > 1) tc::cluster_sync();   // the other CTAs' sums are read before they are reused
+      else __syncthreads();
+    }
+  }
+}
+
+// The two parts and the lists from a U that another kernel has formed.
+__global__ void __launch_bounds__(256) k_lora_parts(ShrinkParams p, const float* __restrict__ U) {
+  pdl_wait();
+  pdl_release();
+  if ((int)blockIdx.x >= p.shrink_ctas) {
+    list_slots(p, blockIdx.x - p.shrink_ctas);
+    return;
+  }
+  const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int t = (int)(e / p.Rp), j = (int)(e % p.Rp);
+  if (t < p.T) write_low_rank(p, t, j, j < p.R ? U[(long long)t * p.R + j] : 0.f);
+}
+
+// Codes of BITS bits -> 4-bit codes in rows of `wpr4` words (zeros behind d): eight codes a thread.
+template <int BITS>
+__global__ void __launch_bounds__(256)
+    k_lora_widen(const uint32_t* __restrict__ packed, int m, int wpr, int wpr4,
+                 uint32_t* __restrict__ out) {
+  pdl_wait();
+  pdl_release();
+  const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (e >= (long long)m * wpr4) return;
+  const long long row = e / wpr4;
+  const int i = (int)(e % wpr4);
+  const long long bit = (long long)i * 8 * BITS;
+  const int w = (int)(bit >> 5), s = (int)(bit & 31);
+  uint32_t v = 0;
+  if (w < wpr) {
+    v = packed[row * wpr + w] >> s;
+    if (s + 8 * BITS > 32 && w + 1 < wpr) v |= packed[row * wpr + w + 1] << (32 - s);
+    v = expand8<BITS>(v);
+  }
+  out[e] = v;
+}
+
+// Rows of `cols` 16-bit values -> rows of `ld` (zeros behind), so that they start on 16 bytes.
+__global__ void __launch_bounds__(256)
+    k_lora_pad(const uint16_t* __restrict__ x, int rows, int cols, int ld, uint16_t* __restrict__ out) {
+  pdl_wait();
+  pdl_release();
+  const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (e >= (long long)rows * ld) return;
+  const long long r = e / ld;
+  const int k = (int)(e % ld);
+  out[e] = k < cols ? x[r * cols + k] : (uint16_t)0;
+}
+
+// ------------------------------------------------------------------------------------------
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 lt_encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* ptr = nullptr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    return (PFN_cuTensorMapEncodeTiled_v12000) nullptr;
+  }();
+  return fn;
+}
+
+bool lt_map(CUtensorMap* map, CUtensorMapDataType dt, int esize, const void* base, long long cols,
+            long long rows, int box_rows) {
+  auto enc = lt_encode();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(cols * esize)};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / esize), (cuuint32_t)box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return enc(map, dt, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+long long round_up(long long x, long long a) { return (x + a - 1) / a * a; }
+
+// Tile width and splits of the contraction: the smallest waves x (stages of an item x the cycles of
+// a stage + what an item costs besides).  A stage of 256 tokens is bound by the MMAs (about 512
+// cycles), narrower ones by making the weight operand (about 330); an item costs about 2000 cycles,
+// a split's sums their traffic.
+struct LtPlan { int BN, splits, per; };
+LtPlan lt_plan(int M, int T, int units, int stages_per_unit, int num_sms, size_t part_floats) {
+  LtPlan best{0, 1, units};
+  double best_cost = 0;
+  for (int BN : {64, 128, 256}) {
+    if (BN < 256 && T > 4 * BN) continue;
+    const long long tiles = ((M + 127) / 128) * (long long)((T + BN - 1) / BN);
+    const double stage = BN == 256 ? 512 : 330;
+    for (int s = 1; s <= 32 && s <= units; ++s) {
+      const int per = (units + s - 1) / s, splits = (units + per - 1) / per;
+      if (splits > 1 && (T > 1024 || (size_t)splits * T * M > part_floats)) break;
+      const long long waves = (tiles * splits + num_sms - 1) / num_sms;
+      const double cost = waves * ((double)per * stages_per_unit * stage + 2000) +
+                          (splits > 1 ? 4000 + splits * (double)T * M * 8 / 3000 : 0);
+      if (!best.BN || cost < best_cost) {
+        best = {BN, splits, per};
+        best_cost = cost;
+      }
+    }
+  }
+  return best;
+}
+
+template <bool FWD, int BN, bool BF16>
+int launch_tc(Ctx* c, const CUtensorMap& mx, const CUtensorMap& mu, const LtParams& p) {
+  GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(k_lora_tc<FWD, BN, BF16>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          LtCfg<BN>::SMEM));
+  const int grid = std::min(c->num_sms, p.mtiles * p.ttiles * p.splits);
+  GPTQ_LAUNCH(c, (k_lora_tc<FWD, BN, BF16>), grid, LT_THREADS, LtCfg<BN>::SMEM, mx, mu, p, c->status,
+              c->timeout_cycles);
+  return GPTQ_OK;
+}
+
+template <bool FWD>
+int launch_tc_any(Ctx* c, int BN, bool bf, const CUtensorMap& mx, const CUtensorMap& mu,
+                  const LtParams& p) {
+  if (BN == 64) return bf ? launch_tc<FWD, 64, true>(c, mx, mu, p) : launch_tc<FWD, 64, false>(c, mx, mu, p);
+  if (BN == 128) return bf ? launch_tc<FWD, 128, true>(c, mx, mu, p) : launch_tc<FWD, 128, false>(c, mx, mu, p);
+  return bf ? launch_tc<FWD, 256, true>(c, mx, mu, p) : launch_tc<FWD, 256, false>(c, mx, mu, p);
+}
+
+constexpr size_t kMaxParts = 8;   // splits' partial sums that the asked-for workspace holds
+
+}  // namespace
+
+// Workspace in bytes: U, its parts, the lists, rows that have to be padded, widened codes, splits.
+size_t lora_tc_bytes(const LoraLayer& l) {
+  const size_t Rp = (size_t)round_up(l.R, 32), T = l.T, F = std::max(l.m, l.d);
+  size_t b = 256 * 8;
+  b += T * l.R * 4 + 2 * T * Rp * 4;
+  b += (T / 64 + 1) * 65 * 4 + (T / 256 + 1) * 257 * 4;
+  b += T * round_up(F, 8) * 2;                                  // a padded X or dY
+  b += (size_t)l.m * round_up((l.d + 7) / 8, 4) * 4;            // widened codes
+  if (T <= 1024) b += kMaxParts * T * F * 4;
+  return b;
+}
+
+// forward: x = X, out = Y, low (may be null) = U;  backward: x = dY, out = dX (or null: only G),
+// low = where G goes (not null).
+int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, bool out_f32,
+            float* low, size_t ws_offset) {
+  const int K = forward ? l.d : l.m, M = forward ? l.m : l.d;
+  const bool bf = l.dtype == GPTQ_BF16;
+  const void* w1 = forward ? l.A : l.B;   // contracted with x
+  const void* w2 = forward ? l.B : l.A;   // multiplies the low-rank values
+  const int Rp = (int)round_up(l.R, 32);
+  Carver cv(c);
+  cv.off = ws_offset;
+  // rows on 16-byte boundaries
+  const int ld = (int)round_up(K, 8);
+  const bool pad = K % 8 != 0 || !aligned16(x);
+  uint16_t* xp = pad ? cv.take<uint16_t>((size_t)l.T * ld) : nullptr;
+  const int wpr = (int)(((long long)l.d * l.bits + 31) / 32), wpr4 = (int)round_up((l.d + 7) / 8, 4);
+  const bool widen = out && (l.bits != 4 || wpr != wpr4 || !aligned16(l.packed));
+  uint32_t* codes = widen ? cv.take<uint32_t>((size_t)l.m * wpr4) : nullptr;
+  float* u_tmp = low ? low : cv.take<float>((size_t)l.T * l.R);
+  float* parts = cv.take<float>((size_t)2 * l.T * Rp);
+  int32_t* slots = cv.take<int32_t>((size_t)(l.T / 64 + 1) * 65 + (size_t)(l.T / 256 + 1) * 257);
+  if (!cv.ok())
+    GPTQ_SET_ERR(c, GPTQ_ERR_NOMEM, "lora: workspace %zu < %zu bytes", c->ws_bytes, cv.off);
+  float* part = cv.take<float>(0);
+  const size_t part_floats = cv.ok() ? (c->ws_bytes - cv.off) / sizeof(float) : 0;
+
+  if (widen) {
+    const unsigned grid = (unsigned)(((long long)l.m * wpr4 + 255) / 256);
+    switch (l.bits) {
+      case 1: GPTQ_LAUNCH(c, k_lora_widen<1>, grid, 256, 0, l.packed, l.m, wpr, wpr4, codes); break;
+      case 2: GPTQ_LAUNCH(c, k_lora_widen<2>, grid, 256, 0, l.packed, l.m, wpr, wpr4, codes); break;
+      case 3: GPTQ_LAUNCH(c, k_lora_widen<3>, grid, 256, 0, l.packed, l.m, wpr, wpr4, codes); break;
+      default: GPTQ_LAUNCH(c, k_lora_widen<4>, grid, 256, 0, l.packed, l.m, wpr, wpr4, codes); break;
+    }
+  }
+  if (pad)
+    GPTQ_LAUNCH(c, k_lora_pad, (unsigned)(((long long)l.T * ld + 255) / 256), 256, 0,
+                (const uint16_t*)x, l.T, K, ld, xp);
+  const void* xs = pad ? xp : x;
+
+  const int units = forward ? (K + 127) / 128 : (K + 63) / 64;
+  const LtPlan plan = lt_plan(M, l.T, units, forward ? 2 : 1, c->num_sms, part_floats);
+  const bool fused = plan.splits == 1;
+  const int ttiles = (l.T + plan.BN - 1) / plan.BN;
+
+  ShrinkParams s{};
+  s.x = xs;
+  s.w = w1;
+  s.T = l.T; s.F = K; s.n = l.n; s.R = l.R; s.Rp = Rp; s.T_rows = l.T;
+  s.adapter = l.adapter;
+  s.scaling = l.scaling;
+  s.parts = fused && out ? parts : nullptr;
+  s.slots = slots;
+  s.BN = plan.BN;
+  s.ttiles = fused && out ? ttiles : 0;
+  // the adapter's rows must be readable in 16-byte pieces; x's are (padded rows are longer than the
+  // adapter's, so those go the other way)
+  if (K % 8 == 0 && aligned16(w1)) {
+    s.U = (low || !fused) ? u_tmp : nullptr;
+    const int tiles = (l.T + 31) / 32;
+    s.cluster = 1;
+    while (s.cluster < 8 && 2 * tiles * s.cluster <= c->num_sms && (K + 63) / 64 > 16 * s.cluster)
+      s.cluster *= 2;
+    s.shrink_ctas = tiles * s.cluster;
+    const int grid = s.shrink_ctas + (int)round_up(s.ttiles, s.cluster);
+    if (bf)
+      GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, s.cluster, k_lora_shrink<true>, dim3(grid),
+                                            dim3(LU_THREADS), 0, s, c->status));
+    else
+      GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, s.cluster, k_lora_shrink<false>, dim3(grid),
+                                            dim3(LU_THREADS), 0, s, c->status));
+  } else {
+    const int rc = lora_shrink_any(c, l, x, K, w1, u_tmp);
+    if (rc) return rc;
+    s.shrink_ctas = s.parts ? (int)(((long long)l.T * Rp + 255) / 256) : 0;
+    if (s.shrink_ctas + s.ttiles)
+      GPTQ_LAUNCH(c, k_lora_parts, s.shrink_ctas + s.ttiles, 256, 0, s, (const float*)u_tmp);
+  }
+  if (!out) return GPTQ_OK;
+
+  CUtensorMap mx, mu;
+  if (!lt_map(&mx, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, xs,
+              ld, l.T, plan.BN) ||
+      !lt_map(&mu, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, parts, Rp, 2LL * l.T, plan.BN))
+    GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "lora: tensor map failed");
+  LtParams p{};
+  p.M = M; p.K = K;
+  p.T = l.T; p.m = l.m; p.ng = l.ng; p.wpr = wpr4;
+  p.group_steps = l.group == -1 ? 0 : l.group / 128;
+  p.packed = widen ? codes : l.packed;
+  p.scales = l.scales;
+  p.zeros = l.zeros;
+  p.mtiles = (M + 127) / 128;
+  p.ttiles = ttiles;
+  p.splits = plan.splits;
+  p.units = units;
+  p.per = plan.per;
+  p.T_rows = l.T;
+  p.rank_chunks = fused ? Rp / 32 : 0;
+  p.R = l.R; p.n = l.n;
+  p.adapter = l.adapter;
+  p.w = w2;
+  p.slots = slots;
+  p.out = out;
+  p.out_f32 = out_f32;
+  p.part = fused ? nullptr : part;
+  p.idesc = tc::idesc_f32acc(bf ? 1u : 0u, !forward, false, 128, plan.BN);
+  p.idesc_tf32 = tc::idesc_f32acc(2u, false, false, 128, plan.BN);
+  const int rc = forward ? launch_tc_any<true>(c, plan.BN, bf, mx, mu, p)
+                         : launch_tc_any<false>(c, plan.BN, bf, mx, mu, p);
+  if (rc || fused) return rc;
+  return lora_join(c, l, part, plan.splits, M, u_tmp, 1, nullptr, w2, out, out_f32, nullptr);
+}
+
+}  // namespace gptq

@@ -121,9 +121,16 @@ bool lora_small_applies(const LoraLayer& l, const void* X);
 size_t lora_small_floats(const LoraLayer& l);
 int lora_forward_small(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool y_f32, float* U,
                        float* ws, size_t ws_floats);
-// out [T, F] = Σ_splits part [splits, T, F] + U w[adapter], U = scaling Σ_chunks upart
+// out [T, F] = Σ_splits part [splits, T, F] + U w[adapter], U = scaling Σ_chunks upart (scaling null:
+// U = upart)
 int lora_join(Ctx* c, const LoraLayer& l, const float* part, int splits, int F, const float* upart,
-              int chunks, const void* w, void* out, bool out_f32, float* U);
+              int chunks, const float* scaling, const void* w, void* out, bool out_f32, float* U);
+// any format: out [T, R] = scaling x w[adapter]ᵀ (x [T, F], w [n, R, F]), zero without an adapter
+int lora_shrink_any(Ctx* c, const LoraLayer& l, const void* x, int F, const void* w, float* out);
+// many tokens, both directions (k_lora_tc.cu); its workspace starts at ws_offset
+size_t lora_tc_bytes(const LoraLayer& l);
+int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, bool out_f32,
+            float* low, size_t ws_offset);
 
 // ---- distillation from a teacher's top logits (k_distill.cu)
 struct DistillArgs {
