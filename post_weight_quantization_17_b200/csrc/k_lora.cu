@@ -154,11 +154,10 @@ __global__ void __launch_bounds__(128)
   }
 }
 
-// out[a, j, f] (+)= Σ_{t: a_t = a} u[t, j] x[t, f] for 8 rank indices: one feature per thread.
+// fp32 x: out[a, j, f] (+)= Σ_{t: a_t = a} u[t, j] x[t, f] for 8 rank indices: one feature per thread.
 // A token of another adapter is skipped, not multiplied by zero, so its non-finite values stay out.
-template <class TX>
 __global__ void __launch_bounds__(128)
-    k_lora_outer_any(const float* __restrict__ u, const TX* __restrict__ x, int T, int F, int R,
+    k_lora_outer_f32(const float* __restrict__ u, const float* __restrict__ x, int T, int F, int R,
                      const int32_t* __restrict__ adapter, int accumulate, float* __restrict__ out) {
   pdl_wait();
   pdl_release();
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(128)
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int t = 0; t < T; ++t) {
     if (adapter[t] != a) continue;
-    const float v = to_f32<TX>(x[(long long)t * F + f]);
+    const float v = x[(long long)t * F + f];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j0 + j < R) acc[j] = fmaf(u[(long long)t * R + j0 + j], v, acc[j]);
@@ -197,14 +196,6 @@ int shrink_any(Ctx* c, const LoraLayer& l, const TX* x, int F, const TX* w, floa
 }
 
 template <class TX>
-int outer_any(Ctx* c, const LoraLayer& l, const float* u, const TX* x, int F, int accumulate,
-              float* out) {
-  GPTQ_LAUNCH(c, k_lora_outer_any<TX>, dim3((F + 127) / 128, (l.R + 7) / 8, l.n), 128, 0, u, x, l.T,
-              F, l.R, l.adapter, accumulate, out);
-  return GPTQ_OK;
-}
-
-template <class TX>
 int forward_any(Ctx* c, const LoraLayer& l, const TX* X, void* Y, bool y_f32, float* U) {
   int rc = shrink_any<TX>(c, l, X, l.d, (const TX*)l.A, U);
   if (rc) return rc;
@@ -218,25 +209,21 @@ int forward_any(Ctx* c, const LoraLayer& l, const TX* X, void* Y, bool y_f32, fl
   return GPTQ_OK;
 }
 
-template <class TX>
-int outers(Ctx* c, const LoraLayer& l, const TX* dY, const TX* X, const float* U, float* dA,
-           float* dB, int accumulate, const float* G) {
-  int rc;
-  if (dA && (rc = outer_any<TX>(c, l, G, X, l.d, accumulate, dA))) return rc;
-  if (dB && (rc = outer_any<TX>(c, l, U, dY, l.m, accumulate, dB))) return rc;
+int outer(Ctx* c, const LoraLayer& l, const float* u, const void* x, int F, int accumulate,
+          float* out) {
+  if (l.dtype != GPTQ_F32) return lora_outer(c, l, u, x, F, accumulate, out);
+  GPTQ_LAUNCH(c, k_lora_outer_f32, dim3((F + 127) / 128, (l.R + 7) / 8, l.n), 128, 0, u,
+              (const float*)x, l.T, F, l.R, l.adapter, accumulate, out);
   return GPTQ_OK;
 }
 
 template <class TX>
-int backward_any(Ctx* c, const LoraLayer& l, const TX* dY, const TX* X, const float* U, TX* dX,
-                 float* dA, float* dB, int accumulate, float* G) {
-  int rc;
-  if ((dX || dA) && (rc = shrink_any<TX>(c, l, dY, l.m, (const TX*)l.B, G))) return rc;
-  if (dX)
-    GPTQ_LAUNCH(c, k_lora_dx_any<TX>, dim3((l.d + 127) / 128, (l.T + 7) / 8), 128, 0, dY, l.T, l.d,
-                any_codes(l), l.m, l.n, l.R, l.adapter, (const TX*)l.A, (const float*)G, dX,
-                c->status);
-  return outers<TX>(c, l, dY, X, U, dA, dB, accumulate, G);
+int dx_any(Ctx* c, const LoraLayer& l, const TX* dY, TX* dX, float* G) {
+  int rc = shrink_any<TX>(c, l, dY, l.m, (const TX*)l.B, G);
+  if (rc || !dX) return rc;
+  GPTQ_LAUNCH(c, k_lora_dx_any<TX>, dim3((l.d + 127) / 128, (l.T + 7) / 8), 128, 0, dY, l.T, l.d,
+              any_codes(l), l.m, l.n, l.R, l.adapter, (const TX*)l.A, (const float*)G, dX, c->status);
+  return GPTQ_OK;
 }
 
 }  // namespace
@@ -289,22 +276,17 @@ int lora_backward(Ctx* c, const LoraLayer& l, const void* dY, const void* X, con
   float* G = cv.take<float>((size_t)l.T * l.R);
   if (!cv.ok())
     GPTQ_SET_ERR(c, GPTQ_ERR_NOMEM, "lora_backward: workspace %zu < %zu bytes", c->ws_bytes, cv.off);
-  if (lora_tensor_format(l)) {
-    int rc;
-    if ((dX || dA) && (rc = lora_tc(c, l, false, dY, dX, false, G, cv.off))) return rc;
-    if (l.dtype == GPTQ_BF16)
-      return outers<__nv_bfloat16>(c, l, (const __nv_bfloat16*)dY, (const __nv_bfloat16*)X, U, dA,
-                                   dB, accumulate, G);
-    return outers<__half>(c, l, (const __half*)dY, (const __half*)X, U, dA, dB, accumulate, G);
+  int rc = GPTQ_OK;
+  if (dX || dA) {   // G, and dX where it is asked for
+    if (lora_tensor_format(l)) rc = lora_tc(c, l, false, dY, dX, false, G, cv.off);
+    else if (l.dtype == GPTQ_BF16)
+      rc = dx_any(c, l, (const __nv_bfloat16*)dY, (__nv_bfloat16*)dX, G);
+    else if (l.dtype == GPTQ_F16) rc = dx_any(c, l, (const __half*)dY, (__half*)dX, G);
+    else rc = dx_any(c, l, (const float*)dY, (float*)dX, G);
   }
-  if (l.dtype == GPTQ_BF16)
-    return backward_any<__nv_bfloat16>(c, l, (const __nv_bfloat16*)dY, (const __nv_bfloat16*)X, U,
-                                       (__nv_bfloat16*)dX, dA, dB, accumulate, G);
-  if (l.dtype == GPTQ_F16)
-    return backward_any<__half>(c, l, (const __half*)dY, (const __half*)X, U, (__half*)dX, dA, dB,
-                                accumulate, G);
-  return backward_any<float>(c, l, (const float*)dY, (const float*)X, U, (float*)dX, dA, dB,
-                             accumulate, G);
+  if (!rc && dA) rc = outer(c, l, G, X, l.d, accumulate, dA);
+  if (!rc && dB) rc = outer(c, l, U, dY, l.m, accumulate, dB);
+  return rc;
 }
 
 }  // namespace gptq
