@@ -18,10 +18,15 @@
 //   non-finite values never reach another's.
 //
 // Roles (one CTA per SM, persistent over tiles):
-//   warp 0        TMA producer of the tokens' operand (BN rows x 128 bytes per stage)
-//   warp 1        MMA issuer, owner of TMEM (two partial-sum buffers of BN columns)
-//   warps 4-7     the weight operand: codes global -> registers (several stages ahead) -> shared
+//   warps 0-7     the weight operand: codes and grid of a unit, shared -> registers -> shared
 //   warps 8-15    epilogue: TMEM -> fp32 sums in registers -> out, or a split's partial
+//   warp 16       TMA producer of the tokens' operand (BN rows x 128 bytes per stage)
+//   warp 17       MMA issuer, owner of TMEM (two partial-sum buffers of BN columns)
+//   warp 18       copies of the codes (TMA boxes) and of the grid, some units ahead; 19 idle
+// The grid is first turned column-major (k_lora_grid), so that the (Δ, z) of a unit's rows are one
+// contiguous copy: read in place they are 128 scattered words per step, and loads of codes and grid
+// into the weight warps' registers, though issued two to four stages ahead, took as long as the
+// whole stage (0.74 us of 256 tokens; without them 0.45).
 // Few tokens: the contraction is split over CTAs and k_lora_join adds the splits and the adapter.
 #include <algorithm>
 #include <cstring>
@@ -31,28 +36,30 @@
 
 namespace gptq {
 
-constexpr int LT_THREADS = 512;
+constexpr int LT_THREADS = 640;
 constexpr int LT_A_BYTES = 128 * 128;      // weight operand of a stage
-constexpr int LT_AHEAD = 4;                // stages whose codes are in flight
+constexpr int LT_DELTAS = 8;               // forward: partial sums whose Δ wait in shared memory
 constexpr float LT_F16_SCALE = 256.f;
 
-template <int BN>
+template <bool FWD, int BN>
 struct LtCfg {
   static constexpr int X_BYTES = BN * 128;
   static constexpr int STAGE = LT_A_BYTES + X_BYTES;
   static constexpr int NS = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
-  static constexpr int SMEM = NS * STAGE + 1024 + 256;
+  // a unit of codes and grid: 128 rows x 128 columns forward, 64 rows backward
+  static constexpr int C_BYTES = FWD ? 8192 : 4096, G_BYTES = FWD ? 1024 : 512;
+  static constexpr int NC = FWD ? 3 : 6;
+  static constexpr int SMEM = NS * STAGE + NC * (C_BYTES + G_BYTES) + LT_DELTAS * 128 * 4 + 1024 + 512;
   static constexpr int EBN = BN / 2;       // tokens per epilogue thread
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 struct LtParams {
   int M, K;                 // features out, contraction length
-  int T, m, ng, wpr;
+  int T;
   int group_steps;          // groups in 128-column steps; 0: one grid per row
-  const uint32_t* packed;   // 4-bit codes, rows of wpr words (a multiple of 4), 16-byte aligned
-  const float* scales;
-  const int32_t* zeros;
+  const float2* grid;       // [n_g, m_pad] (Δ, z), zero behind m
+  int m_pad;
   int mtiles, ttiles, splits;
   int units, per;           // the contraction in 128-column steps (forward) or 64-row stages
                             // (backward): in all and per split
@@ -87,8 +94,45 @@ __device__ __forceinline__ bool lt_wait(uint64_t* bar, uint32_t parity, long lon
     if (clock64() - t0 > budget) return false;
   return true;
 }
+// Two phases at once: both are tried before either is waited for.
+__device__ __forceinline__ bool lt_wait2(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1,
+                                         long long budget) {
+  const bool r0 = lt_try(b0, p0), r1 = lt_try(b1, p1);
+  return (r0 || lt_wait(b0, p0, budget)) && (r1 || lt_wait(b1, p1, budget));
+}
 __device__ __forceinline__ bool lt_wait_warp(uint64_t* bar, uint32_t parity, long long budget) {
   return __all_sync(0xffffffffu, lt_wait(bar, parity, budget));
+}
+
+// 8 TMEM columns of this warp's lanes; the registers may be read after lt_tmem_wait8 on them.
+__device__ __forceinline__ void lt_tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                 "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void lt_tmem_wait8(uint32_t (&v)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ uint64_t pack_f32x2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+// (a0, a1) += f · (v0, v1)
+__device__ __forceinline__ void fma_f32x2(float& a0, float& a1, uint64_t f, uint32_t v0,
+                                          uint32_t v1) {
+  asm("{\n\t.reg .b64 a, v;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 v, {%3, %4};\n\t"
+      "fma.rn.f32x2 a, %2, v, a;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "l"(f), "r"(v0), "r"(v1));
 }
 
 // A position in a ring of N stages or buffers.
@@ -120,18 +164,25 @@ struct LtTile {
 template <bool FWD, int BN, bool BF16>
 __global__ void __launch_bounds__(LT_THREADS, 1)
     k_lora_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
+              const __grid_constant__ CUtensorMap tmC,
               const __grid_constant__ LtParams p, DeviceStatus* st, long long budget) {
-  using Cfg = LtCfg<BN>;
+  using Cfg = LtCfg<FWD, BN>;
   constexpr int NS = Cfg::NS, EBN = Cfg::EBN, ND = 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full_x = reinterpret_cast<uint64_t*>(smem + NS * Cfg::STAGE);
+  constexpr int NC = Cfg::NC;
+  uint8_t* codes = smem + NS * Cfg::STAGE;               // NC units of codes, then of grid
+  float2* grids = reinterpret_cast<float2*>(codes + NC * Cfg::C_BYTES);
+  float* deltas = reinterpret_cast<float*>(codes + NC * (Cfg::C_BYTES + Cfg::G_BYTES));
+  uint64_t* full_x = reinterpret_cast<uint64_t*>(deltas + LT_DELTAS * 128);
   uint64_t* full_a = full_x + NS;
   uint64_t* empty = full_a + NS;
   uint64_t* d_full = empty + NS;
   uint64_t* d_empty = d_full + ND;
-  uint64_t* drain = d_empty + ND;
+  uint64_t* full_c = d_empty + ND;
+  uint64_t* empty_c = full_c + NC;
+  uint64_t* drain = empty_c + NC;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -140,20 +191,25 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       tc::mbar_init(&full_x[s], 1);
-      tc::mbar_init(&full_a[s], 4);
+      tc::mbar_init(&full_a[s], 8);
       tc::mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < ND; ++b) {
       tc::mbar_init(&d_full[b], 1);
       tc::mbar_init(&d_empty[b], 8);
     }
+    for (int b = 0; b < NC; ++b) {
+      tc::mbar_init(&full_c[b], 1);
+      tc::mbar_init(&empty_c[b], 8);
+    }
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
     tc::mbar_fence_init();
     tc::prefetch_tmap(&tmX);
     tc::prefetch_tmap(&tmU);
+    tc::prefetch_tmap(&tmC);
   }
-  if (warp == 1) tc::tmem_alloc(tmem_slot, ND * BN);
+  if (warp == 17) tc::tmem_alloc(tmem_slot, ND * BN);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -162,9 +218,10 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
   // the layer, X and dY may be read now; only its own results (slots, the split U) wait for it.
   pdl_release();
 
-  if (warp < 4) {
+  // registers: 640 threads start with 96 (61440); 128 x 40 + 256 x 64 + 256 x 152 = 60416
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 0 && lane == 0) {
+    if (warp == 16 && lane == 0) {
       // -------------------------------------------------------------- tokens' operand
       LtRing<NS> ring;
       int issued = 0;
@@ -201,11 +258,18 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
         if (!lt_wait(&full_x[j % NS], (uint32_t)(j / NS) & 1u, kDrainCycles))
           raise_error(st, GPTQ_ERR_TIMEOUT, 72);
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 17 && lane == 0) {
       // -------------------------------------------------------------- MMA issuer
       LtRing<NS> ring;
       LtRing<ND> dr;
-      bool ok = true, any = false, waited = false;
+      bool ok = true, any = false, waited = false, ready = false;
+      // The descriptors of stage 0; a stage or a k step on is an addition to the address field (in
+      // 16-byte units; shared memory ends below its 14 bits).  Little else may stand between the
+      // MMAs: this thread's own instructions are what would hold them up.
+      const uint32_t a0 = tc::smem_u32(smem), b0 = a0 + LT_A_BYTES;
+      const uint64_t da0 = FWD ? tc::sdesc_sw128(a0, 16, 1024) : tc::sdesc_sw128(a0, 8192, 1024);
+      const uint64_t dk0 = tc::sdesc_sw128(a0, 16, 1024), db0 = tc::sdesc_sw128(b0, 16, 1024);
+      constexpr uint32_t A_STEP = FWD ? 2 : 128;
       // one partial sum of `stages` stages
       auto partial = [&](int stages, bool tf32) {
         if (!ok) return;
@@ -215,35 +279,39 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
           ok = false;
           return;
         }
-        tc::fence_after_sync();
         const uint32_t d = tmem + dr.i * BN;
         for (int s = 0; s < stages; ++s) {
-          if (!lt_wait(&full_x[ring.i], ring.phase, budget) ||
-              !lt_wait(&full_a[ring.i], ring.phase, budget)) {
+          if (!ready && !lt_wait2(&full_x[ring.i], ring.phase, &full_a[ring.i], ring.phase, budget)) {
             raise_error(st, GPTQ_ERR_TIMEOUT, 74);
             *abort_flag = 1;
             ok = false;
             return;
           }
           tc::fence_after_sync();
-          const uint32_t a = tc::smem_u32(smem + ring.i * Cfg::STAGE), b = a + LT_A_BYTES;
+          const uint32_t at = ring.i * (Cfg::STAGE / 16);
+          const uint64_t db = db0 + at;
+          LtRing<NS> next = ring;
+          next.next();
           if (tf32) {
+            const uint64_t da = dk0 + at;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc::mma_tf32(d, tc::sdesc_sw128(a + kk * 32, 16, 1024),
-                           tc::sdesc_sw128(b + kk * 32, 16, 1024), p.idesc_tf32,
-                           (s | kk) ? 1u : 0u);
+              tc::mma_tf32(d, da + 2 * kk, db + 2 * kk, p.idesc_tf32, (s | kk) ? 1u : 0u);
+            ready = false;
           } else {
+            const uint64_t da = da0 + at;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_f16(d,
-                          FWD ? tc::sdesc_sw128(a + kk * 32, 16, 1024)
-                              : tc::sdesc_sw128(a + kk * 2048, 8192, 1024),
-                          tc::sdesc_sw128(b + kk * 32, 16, 1024), p.idesc, (s | kk) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              tc::mma_f16(d, da + A_STEP * kk, db + 2 * kk, p.idesc, (s | kk) ? 1u : 0u);
+              // the next stage's barriers, while MMAs are still queued behind this one
+              if (kk == 1)
+                ready = tc::mbar_try_wait(&full_x[next.i], next.phase) &&
+                        tc::mbar_try_wait(&full_a[next.i], next.phase);
+            }
           }
           any = true;
           tc::mma_commit(&empty[ring.i]);
-          ring.next();
+          ring = next;
         }
         tc::mma_commit(&d_full[dr.i]);
         dr.next();
@@ -265,127 +333,163 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
         tc::mma_commit(drain);
         if (!lt_wait(drain, 0, kDrainCycles)) raise_error(st, GPTQ_ERR_TIMEOUT, 75);
       }
-    }
-  } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    // ---------------------------------------------------------------- weight operand
-    const int tid = threadIdx.x - 128;
-    LtRing<NS> ring;
-    bool ok = true, waited = false, bad = false;
-    // Forward: thread = weight row, two 16-byte pieces (64 codes) per stage.  Backward: 64 rows x
-    // four pieces (128 columns) per stage, two per thread; eight threads with the same piece of eight
-    // rows store to eight different 16-byte columns of the swizzled image.
-    const int q = (tid >> 3) & 3, brow = (tid & 7) + 8 * (tid >> 5);
-    uint4 code[LT_AHEAD][2];
-    float delta[LT_AHEAD][2];
-    int zero[LT_AHEAD][2];
-    for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
-      const LtTile t(p, i, BN);
-      const int k0 = FWD ? 2 * t.u0 : t.u0, k1 = FWD ? 2 * t.u1 : t.u1;
-      const int bgi = p.group_steps ? (t.f0 / 128) / p.group_steps : 0;
-      auto fetch = [&](int k, uint4 (&cd)[2], float (&dl)[2], int (&zr)[2]) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = FWD ? t.f0 + tid : 64 * k + brow + 32 * h;
-          const int word = FWD ? 8 * k + 4 * h : t.f0 / 8 + 4 * q;
-          const bool in = row < p.m && word < p.wpr && k < k1;
-          cd[h] = in ? *reinterpret_cast<const uint4*>(p.packed + (long long)row * p.wpr + word)
-                     : make_uint4(0, 0, 0, 0);
-          if (FWD && h) continue;   // one grid column per stage
-          const int gi = FWD ? (p.group_steps ? (k / 2) / p.group_steps : 0) : bgi;
-          const long long at = (long long)row * p.ng + gi;
-          zr[h] = in ? p.zeros[at] : 0;
-          if (!FWD) dl[h] = in ? p.scales[at] : 0.f;
-        }
-      };
-#pragma unroll
-      for (int u = 0; u < LT_AHEAD; ++u) fetch(k0 + u, code[u], delta[u], zero[u]);
-      for (int kb = k0; kb < k1 && ok; kb += LT_AHEAD) {
-#pragma unroll
-        for (int u = 0; u < LT_AHEAD; ++u) {
-          const int k = kb + u;
-          if (k >= k1 || !ok) break;
-          if (!lt_wait_warp(&empty[ring.i], ring.phase ^ 1u, budget)) {
-            raise_error(st, GPTQ_ERR_TIMEOUT, 76);
+    } else if (warp == 18 && lane == 0) {
+      // -------------------------------------------------------------- codes and grid
+      LtRing<NC> ring;
+      int issued = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
+        const LtTile t(p, i, BN);
+        for (int u = t.u0; u < t.u1; ++u) {
+          if (!lt_wait(&empty_c[ring.i], ring.phase ^ 1u, budget)) {
+            raise_error(st, GPTQ_ERR_TIMEOUT, 79);
             *abort_flag = 1;
             ok = false;
             break;
           }
-          uint8_t* dst = smem + ring.i * Cfg::STAGE;
+          const int g = p.group_steps ? (FWD ? u : t.f0 / 128) / p.group_steps : 0;
+          const int row = FWD ? t.f0 : 64 * u;
+          tc::mbar_expect_tx(&full_c[ring.i], Cfg::C_BYTES + Cfg::G_BYTES);
+          tc::tma_load_2d(codes + ring.i * Cfg::C_BYTES, &tmC, &full_c[ring.i],
+                          FWD ? 16 * u : t.f0 / 8, row);
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+              "[%3];" ::"r"(tc::smem_u32(grids) + ring.i * Cfg::G_BYTES),
+              "l"(p.grid + (long long)g * p.m_pad + row), "r"(Cfg::G_BYTES),
+              "r"(tc::smem_u32(&full_c[ring.i]))
+              : "memory");
+          ring.next();
+          ++issued;
+        }
+      }
+      const int left = min(issued, NC);
+      for (int s = 0; s < left; ++s) {
+        const int j = issued - left + s;
+        if (!lt_wait(&full_c[j % NC], (uint32_t)(j / NC) & 1u, kDrainCycles))
+          raise_error(st, GPTQ_ERR_TIMEOUT, 80);
+      }
+    }
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // ---------------------------------------------------------------- weight operand
+    const int tid = threadIdx.x;
+    LtRing<NS> ring;
+    LtRing<NC> cring;
+    bool ok = true, waited = false;
+    // A thread's piece is 16 bytes (32 codes) of a row: eight lanes with the same piece of eight rows
+    // read eight different 16-byte columns of the 64-byte-swizzled codes, and store to eight
+    // different ones of the 128-byte-swizzled operand.  Forward: 128 rows x 128 columns at a time,
+    // two stages (pieces 0, 1 and 2, 3).  Backward: 64 rows x 128 columns, one stage.
+    const int q = (tid >> 3) & 3, brow = (tid & 7) + 8 * (tid >> 5);
+    constexpr int PIECES = FWD ? 2 : 1;
+    uint32_t pc = 0;   // partial sums so far
+    for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
+      const LtTile t(p, i, BN);
+      for (int k = t.u0; k < t.u1; ++k) {
+        LtRing<NS> second = ring;
+        second.next();
+        if (!__all_sync(0xffffffffu,
+                        lt_wait(&full_c[cring.i], cring.phase, budget) &&
+                            (FWD ? lt_wait2(&empty[ring.i], ring.phase ^ 1u, &empty[second.i],
+                                            second.phase ^ 1u, budget)
+                                 : lt_wait(&empty[ring.i], ring.phase ^ 1u, budget)))) {
+          raise_error(st, GPTQ_ERR_TIMEOUT, 76);
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        uint4 code[PIECES];
+        float2 dz[PIECES];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            int z = zero[u][FWD ? 0 : h];
-            if (z < 0 || z > 15) {
-              bad = true;
-              z = 0;
-            }
-            const uint32_t zz = zero_pair<BF16>(z);
-            const uint32_t words[4] = {code[u][h].x, code[u][h].y, code[u][h].z, code[u][h].w};
-            uint32_t hi2 = 0, lo2 = 0;
-            if (!FWD) {
-              if (BF16) {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(delta[u][h]);
-                const __nv_bfloat16 lo = __float2bfloat16_rn(delta[u][h] - __bfloat162float(hi));
-                const __nv_bfloat162 a = __halves2bfloat162(hi, hi), b = __halves2bfloat162(lo, lo);
-                hi2 = *reinterpret_cast<const uint32_t*>(&a);
-                lo2 = *reinterpret_cast<const uint32_t*>(&b);
-              } else {
-                if (!(fabsf(delta[u][h]) < 17.f)) bad = true;
-                const float ds = delta[u][h] * LT_F16_SCALE;
-                const __half hi = __float2half_rn(ds);
-                const __half lo = __float2half_rn(ds - __half2float(hi));
-                const __half2 a = __halves2half2(hi, hi), b = __halves2half2(lo, lo);
-                hi2 = *reinterpret_cast<const uint32_t*>(&a);
-                lo2 = *reinterpret_cast<const uint32_t*>(&b);
-              }
-            }
+        for (int h = 0; h < PIECES; ++h) {
+          const int row = brow + 64 * h;
+          code[h] = *reinterpret_cast<const uint4*>(codes + cring.i * Cfg::C_BYTES + row * 64 +
+                                                    ((q ^ ((row >> 1) & 3)) << 4));
+          dz[h] = grids[cring.i * (Cfg::G_BYTES / 8) + row];
+        }
+        uint8_t* dst = smem + (FWD && q >= 2 ? second.i : ring.i) * Cfg::STAGE;
+        // the partial that last used this slot of deltas has been taken out: its MMAs' successors,
+        // two partials on, have released the stages that were just waited for
+        if (FWD && q == 0) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              uint32_t v[4];
-              centered8<BF16>(words[w], zz, v);
-              if (!FWD) {
+          for (int h = 0; h < PIECES; ++h) deltas[(pc % LT_DELTAS) * 128 + brow + 64 * h] = dz[h].x;
+        }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if (BF16) {
-                    const __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&v[e]);
-                    const __nv_bfloat162 r =
-                        __hfma2(c, *reinterpret_cast<const __nv_bfloat162*>(&hi2),
-                                __hmul2(c, *reinterpret_cast<const __nv_bfloat162*>(&lo2)));
-                    v[e] = *reinterpret_cast<const uint32_t*>(&r);
-                  } else {
-                    const __half2 c = *reinterpret_cast<const __half2*>(&v[e]);
-                    const __half2 r = __hfma2(c, *reinterpret_cast<const __half2*>(&hi2),
-                                              __hmul2(c, *reinterpret_cast<const __half2*>(&lo2)));
-                    v[e] = *reinterpret_cast<const uint32_t*>(&r);
-                  }
-                }
-              }
-              const int row = FWD ? tid : brow + 32 * h;
-              const int chunk = FWD ? 4 * h + w : 4 * (q & 1) + w;
-              *reinterpret_cast<uint4*>(dst + (FWD ? 0 : (q >> 1) * 8192) + row * 128 +
-                                        ((chunk ^ (row & 7)) << 4)) =
-                  make_uint4(v[0], v[1], v[2], v[3]);
+        for (int h = 0; h < PIECES; ++h) {
+          const uint32_t zz = zero_pair<BF16>((int)dz[h].y);
+          const uint32_t words[4] = {code[h].x, code[h].y, code[h].z, code[h].w};
+          uint32_t hi2 = 0, lo2 = 0;
+          if (!FWD) {
+            if (BF16) {
+              const __nv_bfloat16 hi = __float2bfloat16_rn(dz[h].x);
+              const __nv_bfloat16 lo = __float2bfloat16_rn(dz[h].x - __bfloat162float(hi));
+              const __nv_bfloat162 a = __halves2bfloat162(hi, hi), b = __halves2bfloat162(lo, lo);
+              hi2 = *reinterpret_cast<const uint32_t*>(&a);
+              lo2 = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+              const float ds = dz[h].x * LT_F16_SCALE;
+              const __half hi = __float2half_rn(ds);
+              const __half lo = __float2half_rn(ds - __half2float(hi));
+              const __half2 a = __halves2half2(hi, hi), b = __halves2half2(lo, lo);
+              hi2 = *reinterpret_cast<const uint32_t*>(&a);
+              lo2 = *reinterpret_cast<const uint32_t*>(&b);
             }
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&full_a[ring.i]);
-          ring.next();
-          fetch(k + LT_AHEAD, code[u], delta[u], zero[u]);
+          const int row = brow + 64 * h;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t v[4];
+            centered8<BF16>(words[w], zz, v);
+            if (!FWD) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (BF16) {
+                  const __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&v[e]);
+                  const __nv_bfloat162 r =
+                      __hfma2(c, *reinterpret_cast<const __nv_bfloat162*>(&hi2),
+                              __hmul2(c, *reinterpret_cast<const __nv_bfloat162*>(&lo2)));
+                  v[e] = *reinterpret_cast<const uint32_t*>(&r);
+                } else {
+                  const __half2 c = *reinterpret_cast<const __half2*>(&v[e]);
+                  const __half2 r = __hfma2(c, *reinterpret_cast<const __half2*>(&hi2),
+                                            __hmul2(c, *reinterpret_cast<const __half2*>(&lo2)));
+                  v[e] = *reinterpret_cast<const uint32_t*>(&r);
+                }
+              }
+            }
+            const int chunk = 4 * (q & 1) + w;
+            *reinterpret_cast<uint4*>(dst + (FWD ? 0 : (q >> 1) * 8192) + row * 128 +
+                                      ((chunk ^ (row & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+          }
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&full_a[ring.i]);
+          if (FWD) tc::mbar_arrive(&full_a[second.i]);
+          tc::mbar_arrive(&empty_c[cring.i]);
+        }
+        ring.next();
+        if (FWD) ring.next();
+        cring.next();
+        ++pc;
       }
       if (!p.rank_chunks || !ok) continue;
       if (!waited) pdl_wait();
       waited = true;
       const int32_t* slots = p.slots + t.nt * (BN + 1);
-      const int count = slots[0], f = t.f0 + tid;
+      // thread = feature and half of a chunk's 32 ranks
+      const int count = slots[0], fr = tid & 127, jh = tid >> 7, f = t.f0 + fr;
       for (int s = 0; s < count && ok; ++s) {
         const uint16_t* w = (const uint16_t*)p.w + (long long)slots[1 + s] * p.R * p.M + f;
+        ++pc;
         for (int c = 0; c < p.rank_chunks && ok; ++c) {
-          uint32_t v[16];   // 32 ranks of this feature, two to a word
+          const int j0 = 32 * c + 16 * jh;
+          uint32_t v[8];   // 16 ranks of this feature, two to a word
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const uint32_t e = (f < p.M && 32 * c + j < p.R) ? w[(long long)(32 * c + j) * p.M] : 0u;
+          for (int j = 0; j < 16; ++j) {
+            const uint32_t e = (f < p.M && j0 + j < p.R) ? w[(long long)(j0 + j) * p.M] : 0u;
             if (j & 1) v[j / 2] |= e << 16;
             else v[j / 2] = e;
           }
@@ -396,11 +500,11 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
               ok = false;
               break;
             }
-            uint8_t* dst = smem + ring.i * Cfg::STAGE + tid * 128;
+            uint8_t* dst = smem + ring.i * Cfg::STAGE + fr * 128;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4; ++e) {
               const float2 a = pair_f32<BF16>(v[2 * e]), b = pair_f32<BF16>(v[2 * e + 1]);
-              *reinterpret_cast<float4*>(dst + ((e ^ (tid & 7)) << 4)) =
+              *reinterpret_cast<float4*>(dst + (((4 * jh + e) ^ (fr & 7)) << 4)) =
                   make_float4(a.x, a.y, b.x, b.y);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -411,22 +515,23 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
         }
       }
     }
-    if (bad) raise_error(st, GPTQ_ERR_ARG, tid);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     // ---------------------------------------------------------------- epilogue
     const int half = (warp - 8) >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * EBN;
     LtRing<ND> dr;
+    uint32_t pc = 0;
     bool ok = true, waited = false;
     for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
       const LtTile t(p, i, BN);
       const int f = t.f0 + r, tok = t.t0 + half * EBN;
-      const float* srow = p.scales + (long long)min(f, p.m - 1) * p.ng;   // forward: f is a weight row
       float acc[EBN];
 #pragma unroll
       for (int e = 0; e < EBN; ++e) acc[e] = 0.f;
-      auto take = [&](float factor, const uint32_t* mask) {
+      // acc += factor · the next partial sum; in a forward base partial the factor is the row's Δ.
+      // Eight columns are on their way from TMEM while eight are added.
+      auto take = [&](bool scaled, const uint32_t* mask) {
         if (!ok) return;
         if (!lt_wait_warp(&d_full[dr.i], dr.phase, budget)) {
           raise_error(st, GPTQ_ERR_TIMEOUT, 78);
@@ -435,35 +540,37 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
           return;
         }
         tc::fence_after_sync();
+        const float factor = scaled ? deltas[(pc % LT_DELTAS) * 128 + r]
+                                    : (FWD || BF16 || mask ? 1.f : 1.f / LT_F16_SCALE);
+        const uint64_t ff = pack_f32x2(factor, factor);
+        uint32_t v[2][8];
+        const uint32_t base = lane_base + dr.i * BN;
+        lt_tmem_ld8(base, v[0]);
 #pragma unroll
-        for (int c = 0; c < EBN / 32; ++c) {
-          uint32_t v[32];
-          tc::tmem_ld32(lane_base + dr.i * BN + c * 32, v);
+        for (int c = 0; c < EBN / 8; ++c) {
+          lt_tmem_wait8(v[c & 1]);
+          if (c + 1 < EBN / 8) lt_tmem_ld8(base + (c + 1) * 8, v[(c + 1) & 1]);
           if (mask) {   // an adapter's partial: its own tokens only
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if ((mask[c] >> e) & 1u) acc[c * 32 + e] += __uint_as_float(v[e]);
+            for (int e = 0; e < 8; ++e)
+              if ((mask[c >> 2] >> (8 * (c & 3) + e)) & 1u)
+                acc[c * 8 + e] += __uint_as_float(v[c & 1][e]);
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              acc[c * 32 + e] = fmaf(factor, __uint_as_float(v[e]), acc[c * 32 + e]);
+            for (int e = 0; e < 8; e += 2)
+              fma_f32x2(acc[c * 8 + e], acc[c * 8 + e + 1], ff, v[c & 1][e], v[c & 1][e + 1]);
           }
         }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&d_empty[dr.i]);
         dr.next();
+        ++pc;
       };
-      if (FWD) {
-        float next = srow[p.group_steps ? t.u0 / p.group_steps : 0];
-        for (int u = t.u0; u < t.u1 && ok; ++u) {
-          const float delta = next;
-          if (u + 1 < t.u1) next = srow[p.group_steps ? (u + 1) / p.group_steps : 0];
-          take(delta, nullptr);
-        }
-      } else {
-        take(BF16 ? 1.f : 1.f / LT_F16_SCALE, nullptr);
-      }
+      if (FWD)
+        for (int u = t.u0; u < t.u1 && ok; ++u) take(true, nullptr);
+      else
+        take(false, nullptr);
       if (p.rank_chunks && ok) {
         if (!waited) pdl_wait();
         waited = true;
@@ -477,7 +584,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
             const int tt = tok + 32 * c + lane;
             mask[c] = __ballot_sync(0xffffffffu, tt < p.T && p.adapter[tt] == a);
           }
-          take(1.f, mask);
+          take(false, mask);
         }
       }
       if (!ok || f >= p.M) continue;
@@ -505,7 +612,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 17) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, ND * BN);
   }
@@ -692,6 +799,35 @@ __global__ void __launch_bounds__(256) k_lora_parts(ShrinkParams p, const float*
   if (t < p.T) write_low_rank(p, t, j, j < p.R ? U[(long long)t * p.R + j] : 0.f);
 }
 
+// The grid column-major: out[g, r] = (Δ[r, g], z[r, g]), zero for r in [m, m_pad); limit > 0: |Δ| must be
+// below it.  32 x 32 tiles.
+__global__ void __launch_bounds__(256)
+    k_lora_grid(const float* __restrict__ scales, const int32_t* __restrict__ zeros, int m, int ng,
+                int used, int m_pad, float limit, float2* __restrict__ out, DeviceStatus* st) {
+  pdl_wait();
+  pdl_release();
+  __shared__ float2 tile[32][33];
+  const int g0 = blockIdx.x * 32, r0 = blockIdx.y * 32, x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  bool bad = false;
+#pragma unroll
+  for (int i = y; i < 32; i += 8) {
+    float2 v = make_float2(0.f, 0.f);
+    if (r0 + i < m && g0 + x < used) {
+      const long long at = (long long)(r0 + i) * ng + g0 + x;
+      const int z = zeros[at];
+      v = make_float2(scales[at], (float)z);
+      bad = bad || z < 0 || z > 15 || (limit > 0.f && !(fabsf(v.x) < limit));
+      if (z < 0 || z > 15) v.y = 0.f;
+    }
+    tile[i][x] = v;
+  }
+  if (bad) raise_error(st, GPTQ_ERR_ARG, r0);
+  __syncthreads();
+#pragma unroll
+  for (int i = y; i < 32; i += 8)
+    if (g0 + i < used && r0 + x < m_pad) out[(long long)(g0 + i) * m_pad + r0 + x] = tile[x][i];
+}
+
 // Codes of BITS bits -> 4-bit codes in rows of `wpr4` words (zeros behind d): eight codes a thread.
 template <int BITS>
 __global__ void __launch_bounds__(256)
@@ -741,16 +877,18 @@ PFN_cuTensorMapEncodeTiled_v12000 lt_encode() {
   return fn;
 }
 
+// Boxes of box_rows x (swizzle width) bytes.
 bool lt_map(CUtensorMap* map, CUtensorMapDataType dt, int esize, const void* base, long long cols,
-            long long rows, int box_rows) {
+            long long rows, int box_rows, int width = 128) {
   auto enc = lt_encode();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)(cols * esize)};
-  cuuint32_t box[2] = {(cuuint32_t)(128 / esize), (cuuint32_t)box_rows};
+  cuuint32_t box[2] = {(cuuint32_t)(width / esize), (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1, 1};
   return enc(map, dt, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -785,22 +923,29 @@ LtPlan lt_plan(int M, int T, int units, int stages_per_unit, int num_sms, size_t
 }
 
 template <bool FWD, int BN, bool BF16>
-int launch_tc(Ctx* c, const CUtensorMap& mx, const CUtensorMap& mu, const LtParams& p) {
+int launch_tc(Ctx* c, const CUtensorMap& mx, const CUtensorMap& mu,
+              const CUtensorMap& mc, const LtParams& p) {
+  // the register shares that the roles take (setmaxnreg) add up to what 96 a thread provide
+  static const int regs = [] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, k_lora_tc<FWD, BN, BF16>) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs < 96) GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "lora: kernel built with %d registers, not 96", regs);
   GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(k_lora_tc<FWD, BN, BF16>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          LtCfg<BN>::SMEM));
+                                          LtCfg<FWD, BN>::SMEM));
   const int grid = std::min(c->num_sms, p.mtiles * p.ttiles * p.splits);
-  GPTQ_LAUNCH(c, (k_lora_tc<FWD, BN, BF16>), grid, LT_THREADS, LtCfg<BN>::SMEM, mx, mu, p, c->status,
+  GPTQ_LAUNCH(c, (k_lora_tc<FWD, BN, BF16>), grid, LT_THREADS, LtCfg<FWD, BN>::SMEM, mx, mu, mc, p, c->status,
               c->timeout_cycles);
   return GPTQ_OK;
 }
 
 template <bool FWD>
 int launch_tc_any(Ctx* c, int BN, bool bf, const CUtensorMap& mx, const CUtensorMap& mu,
-                  const LtParams& p) {
-  if (BN == 64) return bf ? launch_tc<FWD, 64, true>(c, mx, mu, p) : launch_tc<FWD, 64, false>(c, mx, mu, p);
-  if (BN == 128) return bf ? launch_tc<FWD, 128, true>(c, mx, mu, p) : launch_tc<FWD, 128, false>(c, mx, mu, p);
-  return bf ? launch_tc<FWD, 256, true>(c, mx, mu, p) : launch_tc<FWD, 256, false>(c, mx, mu, p);
+                  const CUtensorMap& mc, const LtParams& p) {
+  if (BN == 64) return bf ? launch_tc<FWD, 64, true>(c, mx, mu, mc, p) : launch_tc<FWD, 64, false>(c, mx, mu, mc, p);
+  if (BN == 128) return bf ? launch_tc<FWD, 128, true>(c, mx, mu, mc, p) : launch_tc<FWD, 128, false>(c, mx, mu, mc, p);
+  return bf ? launch_tc<FWD, 256, true>(c, mx, mu, mc, p) : launch_tc<FWD, 256, false>(c, mx, mu, mc, p);
 }
 
 constexpr size_t kMaxParts = 8;   // splits' partial sums that the asked-for workspace holds
@@ -810,11 +955,12 @@ constexpr size_t kMaxParts = 8;   // splits' partial sums that the asked-for wor
 // Workspace in bytes: U, its parts, the lists, rows that have to be padded, widened codes, splits.
 size_t lora_tc_bytes(const LoraLayer& l) {
   const size_t Rp = (size_t)round_up(l.R, 32), T = l.T, F = std::max(l.m, l.d);
-  size_t b = 256 * 8;
+  size_t b = 256 * 9;
   b += T * l.R * 4 + 2 * T * Rp * 4;
   b += (T / 64 + 1) * 65 * 4 + (T / 256 + 1) * 257 * 4;
   b += T * round_up(F, 8) * 2;                                  // a padded X or dY
   b += (size_t)l.m * round_up((l.d + 7) / 8, 4) * 4;            // widened codes
+  b += (size_t)round_up(l.m, 128) * ((l.d + 127) / 128) * 8;    // the grid, column-major
   if (T <= 1024) b += kMaxParts * T * F * 4;
   return b;
 }
@@ -837,6 +983,9 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   const int wpr = (int)(((long long)l.d * l.bits + 31) / 32), wpr4 = (int)round_up((l.d + 7) / 8, 4);
   const bool widen = out && (l.bits != 4 || wpr != wpr4 || !aligned16(l.packed));
   uint32_t* codes = widen ? cv.take<uint32_t>((size_t)l.m * wpr4) : nullptr;
+  const int m_pad = (int)round_up(l.m, 128);
+  const int used = l.group == -1 ? 1 : (l.d + l.group - 1) / l.group;
+  float2* grid2 = out ? cv.take<float2>((size_t)used * m_pad) : nullptr;
   float* u_tmp = low ? low : cv.take<float>((size_t)l.T * l.R);
   float* parts = cv.take<float>((size_t)2 * l.T * Rp);
   int32_t* slots = cv.take<int32_t>((size_t)(l.T / 64 + 1) * 65 + (size_t)(l.T / 256 + 1) * 257);
@@ -845,6 +994,9 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   float* part = cv.take<float>(0);
   const size_t part_floats = cv.ok() ? (c->ws_bytes - cv.off) / sizeof(float) : 0;
 
+  if (out)
+    GPTQ_LAUNCH(c, k_lora_grid, dim3((used + 31) / 32, m_pad / 32), 256, 0, l.scales, l.zeros, l.m,
+                l.ng, used, m_pad, !forward && !bf ? 17.f : 0.f, grid2, c->status);
   if (widen) {
     const unsigned grid = (unsigned)(((long long)l.m * wpr4 + 255) / 256);
     switch (l.bits) {
@@ -899,18 +1051,19 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   }
   if (!out) return GPTQ_OK;
 
-  CUtensorMap mx, mu;
+  CUtensorMap mx, mu, mc;
   if (!lt_map(&mx, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, xs,
               ld, l.T, plan.BN) ||
-      !lt_map(&mu, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, parts, Rp, 2LL * l.T, plan.BN))
+      !lt_map(&mu, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, parts, Rp, 2LL * l.T, plan.BN) ||
+      !lt_map(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, widen ? codes : l.packed, wpr4, l.m,
+              forward ? 128 : 64, 64))
     GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "lora: tensor map failed");
   LtParams p{};
   p.M = M; p.K = K;
-  p.T = l.T; p.m = l.m; p.ng = l.ng; p.wpr = wpr4;
+  p.T = l.T;
   p.group_steps = l.group == -1 ? 0 : l.group / 128;
-  p.packed = widen ? codes : l.packed;
-  p.scales = l.scales;
-  p.zeros = l.zeros;
+  p.grid = grid2;
+  p.m_pad = m_pad;
   p.mtiles = (M + 127) / 128;
   p.ttiles = ttiles;
   p.splits = plan.splits;
@@ -927,8 +1080,8 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   p.part = fused ? nullptr : part;
   p.idesc = tc::idesc_f32acc(bf ? 1u : 0u, !forward, false, 128, plan.BN);
   p.idesc_tf32 = tc::idesc_f32acc(2u, false, false, 128, plan.BN);
-  const int rc = forward ? launch_tc_any<true>(c, plan.BN, bf, mx, mu, p)
-                         : launch_tc_any<false>(c, plan.BN, bf, mx, mu, p);
+  const int rc = forward ? launch_tc_any<true>(c, plan.BN, bf, mx, mu, mc, p)
+                         : launch_tc_any<false>(c, plan.BN, bf, mx, mu, mc, p);
   if (rc || fused) return rc;
   return lora_join(c, l, part, plan.splits, M, u_tmp, 1, nullptr, w2, out, out_f32, nullptr);
 }
