@@ -50,6 +50,18 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(OuterParams p) {
   const int cl = p.cluster, rank = blockIdx.x % cl;
   const int f0 = (int)(blockIdx.x / cl) * LO_FEATS + wf * 64, j0 = blockIdx.y * LO_RANKS;
   const int a = blockIdx.z, f = f0 + 8 * g;
+  // an adapter without tokens: its gradient is zero (the same for the whole cluster)
+  int any = 0;
+  for (int t = threadIdx.x; t < p.T && !any; t += LO_THREADS) any = p.adapter[t] == a;
+  if (!__syncthreads_or(any)) {
+    const int fb = (int)(blockIdx.x / cl) * LO_FEATS;
+    if (!p.accumulate)
+      for (int e = rank * LO_THREADS + threadIdx.x; e < LO_RANKS * LO_FEATS; e += cl * LO_THREADS) {
+        const int j = j0 + e / LO_FEATS, ff = fb + e % LO_FEATS;
+        if (j < p.R && ff < p.F) p.out[((long long)a * p.R + j) * p.F + ff] = 0.f;
+      }
+    return;
+  }
   float acc[2][8][4] = {};
   const int groups = (p.T + 7) / 8, stride = 4 * cl;
   for (int i0 = rank * 4 + wt; i0 < groups; i0 += 4 * stride) {

@@ -218,59 +218,128 @@ __global__ void __launch_bounds__(LS_THREADS, 2) k_lora_small(SmallParams p, Dev
       }
 }
 
-// out[t, f] = Σ_splits part[s, t, f] + Σ_j U[t, j] w[a_t, j, f], U = scaling Σ_chunks upart; one
-// feature per thread, one token per CTA row.
+// out[t, f] = Σ_splits part[s, t, f] + Σ_j U[t, j] w[a_t, j, f], U = scaling Σ_chunks upart.  A
+// thread has two features of TOKS tokens, whose loads are independent of one another.
 constexpr int LJ_THREADS = 128, LJ_AHEAD = 16;
-template <class TX, class TY>
+template <class TX, class TY, int TOKS>
 __global__ void __launch_bounds__(LJ_THREADS)
     k_lora_join(const float* __restrict__ part, int splits, int T, int F,
                 const float* __restrict__ upart, int chunks, int n, int R,
                 const int32_t* __restrict__ adapter, const float* __restrict__ scaling,
                 const TX* __restrict__ w, TY* __restrict__ out, float* __restrict__ U) {
-  extern __shared__ float us[];
-  const int f = blockIdx.x * LJ_THREADS + threadIdx.x, t = blockIdx.y;
-  int a = adapter[t];
-  if (a < 0 || a >= n) a = -1;
-  // the adapter's first rows, an input, while the products still run
-  const TX* wr = w + (long long)max(a, 0) * R * F + min(f, F - 1);
-  TX first[LJ_AHEAD];
+  extern __shared__ float us[];   // [TOKS, R]
+  const int f = 2 * (blockIdx.x * LJ_THREADS + threadIdx.x), t0 = blockIdx.y * TOKS;
+  const bool two = f + 1 < F, pairs = F % 2 == 0;
+  // the adapters' first rows, an input, while the products still run
+  TX first[TOKS][LJ_AHEAD][2];
+  int a[TOKS];
 #pragma unroll
-  for (int j = 0; j < LJ_AHEAD; ++j)
-    if (a >= 0 && j < R) first[j] = wr[(long long)j * F];
-  const float s = a >= 0 && scaling ? scaling[a] : 1.f;
+  for (int k = 0; k < TOKS; ++k) {
+    a[k] = t0 + k < T ? adapter[t0 + k] : -1;
+    if (a[k] >= n) a[k] = -1;
+  }
+  auto row_pair = [&](int k, int j, TX (&v)[2]) {
+    const TX* src = w + ((long long)a[k] * R + j) * F + f;
+    if (pairs && (reinterpret_cast<uintptr_t>(w) & 3) == 0) {
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(src);
+      v[0] = reinterpret_cast<const TX*>(&u)[0];
+      v[1] = reinterpret_cast<const TX*>(&u)[1];
+    } else {
+      v[0] = src[0];
+      v[1] = src[two ? 1 : 0];
+    }
+  };
+  if (TOKS == 1 && f < F) {
+#pragma unroll
+    for (int j = 0; j < LJ_AHEAD; ++j)
+      if (a[0] >= 0 && j < R) row_pair(0, j, first[0][j]);
+  }
   pdl_wait();
   pdl_release();
-  for (int j = threadIdx.x; j < R; j += LJ_THREADS) {
-    float u = 0.f;
-    if (a >= 0) {
-      for (int c = 0; c < chunks; ++c) u += upart[((long long)c * T + t) * R + j];
-      u *= s;
+#pragma unroll
+  for (int k = 0; k < TOKS; ++k) {
+    if (t0 + k >= T) break;
+    const float s = a[k] >= 0 && scaling ? scaling[a[k]] : 1.f;
+    for (int j = threadIdx.x; j < R; j += LJ_THREADS) {
+      float u = 0.f;
+      if (a[k] >= 0) {
+        for (int c = 0; c < chunks; ++c) u += upart[((long long)c * T + t0 + k) * R + j];
+        u *= s;
+      }
+      us[k * R + j] = u;
+      if (U && blockIdx.x == 0) U[(long long)(t0 + k) * R + j] = u;
     }
-    us[j] = u;
-    if (U && blockIdx.x == 0) U[(long long)t * R + j] = u;
   }
   __syncthreads();
   if (f >= F) return;
-  float y = 0.f;
-  for (int k = 0; k < splits; ++k) y += part[((long long)k * T + t) * F + f];
-  if (a >= 0) {
-    float v = 0.f;
+  float y[TOKS][2];
 #pragma unroll
-    for (int j = 0; j < LJ_AHEAD; ++j)
-      if (j < R) v = fmaf(us[j], to_f32<TX>(first[j]), v);
-    for (int j = LJ_AHEAD; j < R; ++j) v = fmaf(us[j], to_f32<TX>(wr[(long long)j * F]), v);
-    y += v;
+  for (int k = 0; k < TOKS; ++k) y[k][0] = y[k][1] = 0.f;
+  for (int s = 0; s < splits; ++s)
+#pragma unroll
+    for (int k = 0; k < TOKS; ++k) {
+      if (t0 + k >= T) break;
+      const float* src = part + ((long long)s * T + t0 + k) * F + f;
+      if (pairs) {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        y[k][0] += v.x;
+        y[k][1] += v.y;
+      } else {
+        y[k][0] += src[0];
+        if (two) y[k][1] += src[1];
+      }
+    }
+#pragma unroll
+  for (int k = 0; k < TOKS; ++k) {
+    if (t0 + k >= T) break;
+    if (a[k] >= 0) {
+      float v0 = 0.f, v1 = 0.f;
+      int j = 0;
+      if (TOKS == 1) {
+#pragma unroll
+        for (int i = 0; i < LJ_AHEAD; ++i)
+          if (i < R) {
+            v0 = fmaf(us[i], to_f32<TX>(first[0][i][0]), v0);
+            v1 = fmaf(us[i], to_f32<TX>(first[0][i][1]), v1);
+          }
+        j = LJ_AHEAD;
+      }
+#pragma unroll 8
+      for (; j < R; ++j) {
+        TX v[2];
+        row_pair(k, j, v);
+        v0 = fmaf(us[k * R + j], to_f32<TX>(v[0]), v0);
+        v1 = fmaf(us[k * R + j], to_f32<TX>(v[1]), v1);
+      }
+      y[k][0] += v0;
+      y[k][1] += v1;
+    }
+    TY* o = out + (long long)(t0 + k) * F + f;
+    if (pairs && (reinterpret_cast<uintptr_t>(out) & (2 * sizeof(TY) - 1)) == 0) {
+      struct alignas(2 * sizeof(TY)) Pair { TY v[2]; };
+      *reinterpret_cast<Pair*>(o) = Pair{{from_f32<TY>(y[k][0]), from_f32<TY>(y[k][1])}};
+    } else {
+      o[0] = from_f32<TY>(y[k][0]);
+      if (two) o[1] = from_f32<TY>(y[k][1]);
+    }
   }
-  out[(long long)t * F + f] = from_f32<TY>(y);
 }
 
 int lora_join(Ctx* c, const LoraLayer& l, const float* part, int splits, int F, const float* upart,
               int chunks, const float* scaling, const void* w, void* out, bool out_f32, float* U) {
-  const dim3 grid((F + LJ_THREADS - 1) / LJ_THREADS, l.T);
-  const size_t smem = l.R * sizeof(float);
-#define GPTQ_JOIN(TX, TY)                                                                       \
-  GPTQ_LAUNCH(c, k_lora_join<TX, TY>, grid, LJ_THREADS, smem, part, splits, l.T, F, upart, chunks, \
-              l.n, l.R, l.adapter, scaling, (const TX*)w, (TY*)out, U)
+  // one token per CTA while that leaves few CTAs per SM, four (fewer, longer CTAs) beyond
+  const int wide = (F + 2 * LJ_THREADS - 1) / (2 * LJ_THREADS);
+  const bool four = (long long)wide * l.T > 16LL * c->num_sms;
+  const dim3 grid(wide, four ? (l.T + 3) / 4 : l.T);
+  const size_t smem = (size_t)(four ? 4 : 1) * l.R * sizeof(float);
+#define GPTQ_JOIN_N(TX, TY, N)                                                                       \
+  GPTQ_LAUNCH(c, (k_lora_join<TX, TY, N>), grid, LJ_THREADS, smem, part, splits, l.T, F, upart,      \
+              chunks, l.n, l.R, l.adapter, scaling, (const TX*)w, (TY*)out, U)
+#define GPTQ_JOIN(TX, TY)                                                                            \
+  do {                                                                                               \
+    if (four) GPTQ_JOIN_N(TX, TY, 4);                                                                \
+    else GPTQ_JOIN_N(TX, TY, 1);                                                                     \
+  } while (0)
   if (l.dtype == GPTQ_BF16) {
     if (out_f32) GPTQ_JOIN(__nv_bfloat16, float);
     else GPTQ_JOIN(__nv_bfloat16, __nv_bfloat16);
@@ -279,6 +348,7 @@ int lora_join(Ctx* c, const LoraLayer& l, const float* part, int splits, int F, 
     else GPTQ_JOIN(__half, __half);
   }
 #undef GPTQ_JOIN
+#undef GPTQ_JOIN_N
   return GPTQ_OK;
 }
 

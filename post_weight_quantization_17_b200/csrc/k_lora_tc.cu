@@ -742,8 +742,10 @@ __global__ void __launch_bounds__(LU_THREADS) k_lora_shrink(ShrinkParams p, Devi
         }
       }
       // join the warps (fixed order), 16 ranks at a time
+      const int quarters = (min(64, p.Rp - j0) + 15) / 16;
 #pragma unroll
       for (int quarter = 0; quarter < 4; ++quarter) {
+        if (quarter >= quarters) break;
         __syncthreads();
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -763,24 +765,25 @@ __global__ void __launch_bounds__(LU_THREADS) k_lora_shrink(ShrinkParams p, Devi
       }
       if (cl > 1) tc::cluster_sync();
       else __syncthreads();
-      if (rank == 0) {
-        const float scale = p.scaling[a];
-        for (int e = threadIdx.x; e < 32 * 64; e += LU_THREADS) {
-          const int row = e >> 6, j = j0 + (e & 63);
-          if (j >= p.Rp || !((mine >> row) & 1u)) continue;
-          float v = total[e];
-          for (int c = 1; c < cl; ++c) {
-            float u;
+      // each CTA of the cluster finishes its share of the tokens
+      const float scale = p.scaling[a];
+      const int rows = 32 / cl, cols = 16 * quarters;
+      for (int e = threadIdx.x; e < rows * cols; e += LU_THREADS) {
+        const int row = rank * rows + e / cols, col = e % cols, j = j0 + col;
+        if (!((mine >> row) & 1u)) continue;
+        float v = 0.f;
+        for (int c = 0; c < cl; ++c) {
+          float u = total[row * 64 + col];
+          if (cl > 1)
             asm volatile("ld.shared::cluster.f32 %0, [%1];"
                          : "=f"(u)
-                         : "r"(tc::map_to_rank(&total[e], c))
+                         : "r"(tc::map_to_rank(&total[row * 64 + col], c))
                          : "memory");
-            v += u;
-          }
-          write_low_rank(p, t0 + row, j, j < p.R ? v * scale : 0.f);
+          v += u;
         }
+        write_low_rank(p, t0 + row, j, j < p.R ? v * scale : 0.f);
       }
-      if (cl > 1) tc::cluster_sync();   // the other CTAs' sums are read before they are reused
+      if (cl > 1) tc::cluster_sync();   // every CTA's sums are read before they are reused
       else __syncthreads();
     }
   }
@@ -807,7 +810,7 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   pdl_release();
   __shared__ float2 tile[32][33];
-  const int g0 = blockIdx.x * 32, r0 = blockIdx.y * 32, x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int g0 = blockIdx.y * 32, r0 = blockIdx.x * 32, x = threadIdx.x & 31, y = threadIdx.x >> 5;
   bool bad = false;
 #pragma unroll
   for (int i = y; i < 32; i += 8) {
@@ -828,26 +831,23 @@ __global__ void __launch_bounds__(256)
     if (g0 + i < used && r0 + x < m_pad) out[(long long)(g0 + i) * m_pad + r0 + x] = tile[x][i];
 }
 
-// Codes of BITS bits -> 4-bit codes in rows of `wpr4` words (zeros behind d): eight codes a thread.
+// Codes of BITS bits -> 4-bit codes in rows of `wpr4` words (a multiple of 4; zeros behind d): 32
+// codes a thread.
 template <int BITS>
 __global__ void __launch_bounds__(256)
-    k_lora_widen(const uint32_t* __restrict__ packed, int m, int wpr, int wpr4,
-                 uint32_t* __restrict__ out) {
+    k_lora_widen(const uint32_t* __restrict__ packed, int wpr, int wpr4, uint32_t* __restrict__ out) {
   pdl_wait();
   pdl_release();
-  const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (e >= (long long)m * wpr4) return;
-  const long long row = e / wpr4;
-  const int i = (int)(e % wpr4);
-  const long long bit = (long long)i * 8 * BITS;
-  const int w = (int)(bit >> 5), s = (int)(bit & 31);
-  uint32_t v = 0;
-  if (w < wpr) {
-    v = packed[row * wpr + w] >> s;
-    if (s + 8 * BITS > 32 && w + 1 < wpr) v |= packed[row * wpr + w + 1] << (32 - s);
-    v = expand8<BITS>(v);
-  }
-  out[e] = v;
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  const long long row = blockIdx.y;
+  if (4 * i >= wpr4) return;
+  const uint32_t* src = packed + row * wpr;
+  uint32_t w[BITS], v[4];
+#pragma unroll
+  for (int k = 0; k < BITS; ++k) w[k] = i * BITS + k < wpr ? src[i * BITS + k] : 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = eight_codes<BITS>(w, k);
+  *reinterpret_cast<uint4*>(out + row * wpr4 + 4 * i) = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // Rows of `cols` 16-bit values -> rows of `ld` (zeros behind), so that they start on 16 bytes.
@@ -995,15 +995,20 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   const size_t part_floats = cv.ok() ? (c->ws_bytes - cv.off) / sizeof(float) : 0;
 
   if (out)
-    GPTQ_LAUNCH(c, k_lora_grid, dim3((used + 31) / 32, m_pad / 32), 256, 0, l.scales, l.zeros, l.m,
+    GPTQ_LAUNCH(c, k_lora_grid, dim3(m_pad / 32, (used + 31) / 32), 256, 0, l.scales, l.zeros, l.m,
                 l.ng, used, m_pad, !forward && !bf ? 17.f : 0.f, grid2, c->status);
   if (widen) {
-    const unsigned grid = (unsigned)(((long long)l.m * wpr4 + 255) / 256);
-    switch (l.bits) {
-      case 1: GPTQ_LAUNCH(c, k_lora_widen<1>, grid, 256, 0, l.packed, l.m, wpr, wpr4, codes); break;
-      case 2: GPTQ_LAUNCH(c, k_lora_widen<2>, grid, 256, 0, l.packed, l.m, wpr, wpr4, codes); break;
-      case 3: GPTQ_LAUNCH(c, k_lora_widen<3>, grid, 256, 0, l.packed, l.m, wpr, wpr4, codes); break;
-      default: GPTQ_LAUNCH(c, k_lora_widen<4>, grid, 256, 0, l.packed, l.m, wpr, wpr4, codes); break;
+    // rows in the grid's y: in pieces, should there be more than it holds
+    for (int r0 = 0; r0 < l.m; r0 += 65535) {
+      const dim3 grid((wpr4 / 4 + 255) / 256, std::min(65535, l.m - r0));
+      const uint32_t* src = l.packed + (long long)r0 * wpr;
+      uint32_t* dst = codes + (long long)r0 * wpr4;
+      switch (l.bits) {
+        case 1: GPTQ_LAUNCH(c, k_lora_widen<1>, grid, 256, 0, src, wpr, wpr4, dst); break;
+        case 2: GPTQ_LAUNCH(c, k_lora_widen<2>, grid, 256, 0, src, wpr, wpr4, dst); break;
+        case 3: GPTQ_LAUNCH(c, k_lora_widen<3>, grid, 256, 0, src, wpr, wpr4, dst); break;
+        default: GPTQ_LAUNCH(c, k_lora_widen<4>, grid, 256, 0, src, wpr, wpr4, dst); break;
+      }
     }
   }
   if (pad)
@@ -1032,7 +1037,9 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
     s.U = (low || !fused) ? u_tmp : nullptr;
     const int tiles = (l.T + 31) / 32;
     s.cluster = 1;
-    while (s.cluster < 8 && 2 * tiles * s.cluster <= c->num_sms && (K + 63) / 64 > 16 * s.cluster)
+    // up to about four CTAs per SM, and a step of 64 features at least per warp: a warp's steps follow
+    // one another at the latency of a load
+    while (s.cluster < 8 && tiles * s.cluster <= 2 * c->num_sms && (K + 63) / 64 > 8 * s.cluster)
       s.cluster *= 2;
     s.shrink_ctas = tiles * s.cluster;
     const int grid = s.shrink_ctas + (int)round_up(s.ttiles, s.cluster);
