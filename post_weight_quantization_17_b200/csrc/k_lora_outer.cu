@@ -7,8 +7,10 @@
 // one token, and tile i of the warp's eight takes feature 8 n + i as its column n, so no
 // shared-memory pass is needed.  A CTA covers 128 features and 32 ranks; its four token warps, and
 // the CTAs of a cluster, take the 8-token groups in turn (adapters' runs spread evenly) and are
-// joined in a fixed order in (distributed) shared memory.  Groups without a token of the adapter are
-// skipped; in mixed groups the others' rows are replaced by zeros, not multiplied.
+// joined in a fixed order in (distributed) shared memory.  A cluster takes several adapters one after
+// the other (one in turn would leave most CTAs of a large adapter table with nothing to do); those
+// without a token are cleared.  Groups without a token of the adapter are skipped; in mixed groups the
+// others' rows are replaced by zeros, not multiplied.
 #include <algorithm>
 
 #include "lora_util.cuh"
@@ -25,7 +27,7 @@ struct OuterParams {
   const void* x;           // [T, F]
   int T, F, R, wide;       // wide: x may be read in 16-byte pieces
   const int32_t* adapter;
-  int accumulate, cluster;
+  int accumulate, cluster, n;
   float* out;              // [n, R, F]
 };
 
@@ -49,18 +51,26 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(OuterParams p) {
   const int wf = warp & 1, wt = warp >> 1;
   const int cl = p.cluster, rank = blockIdx.x % cl;
   const int f0 = (int)(blockIdx.x / cl) * LO_FEATS + wf * 64, j0 = blockIdx.y * LO_RANKS;
-  const int a = blockIdx.z, f = f0 + 8 * g;
-  // an adapter without tokens: its gradient is zero (the same for the whole cluster)
-  int any = 0;
-  for (int t = threadIdx.x; t < p.T && !any; t += LO_THREADS) any = p.adapter[t] == a;
-  if (!__syncthreads_or(any)) {
-    const int fb = (int)(blockIdx.x / cl) * LO_FEATS;
+  const int f = f0 + 8 * g, fb = (int)(blockIdx.x / cl) * LO_FEATS;
+  // which adapters have tokens
+  uint32_t* present = reinterpret_cast<uint32_t*>(total + LO_RANKS * LO_FEATS);
+  for (int i = threadIdx.x; i < (p.n + 31) / 32; i += LO_THREADS) present[i] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int t = threadIdx.x; t < p.T; t += LO_THREADS) {
+    const int a = p.adapter[t];
+    if (a >= 0 && a < p.n && !((present[a >> 5] >> (a & 31)) & 1u))
+      atomicOr(&present[a >> 5], 1u << (a & 31));
+  }
+  __syncthreads();
+  for (int a = blockIdx.z; a < p.n; a += gridDim.z) {
+  if (!((present[a >> 5] >> (a & 31)) & 1u)) {   // its gradient is zero
     if (!p.accumulate)
       for (int e = rank * LO_THREADS + threadIdx.x; e < LO_RANKS * LO_FEATS; e += cl * LO_THREADS) {
         const int j = j0 + e / LO_FEATS, ff = fb + e % LO_FEATS;
         if (j < p.R && ff < p.F) p.out[((long long)a * p.R + j) * p.F + ff] = 0.f;
       }
-    return;
+    continue;
   }
   float acc[2][8][4] = {};
   const int groups = (p.T + 7) / 8, stride = 4 * cl;
@@ -150,7 +160,6 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(OuterParams p) {
   else __syncthreads();
   // each CTA of the cluster finishes its share of the tile
   const int share = LO_RANKS * LO_FEATS / cl;
-  const int fb = (int)(blockIdx.x / cl) * LO_FEATS;
   for (int e = rank * share + threadIdx.x; e < (rank + 1) * share; e += LO_THREADS) {
     const int j = j0 + e / LO_FEATS, ff = fb + e % LO_FEATS;
     float s = 0.f;
@@ -170,7 +179,9 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(OuterParams p) {
       *o = p.accumulate ? *o + s : s;
     }
   }
-  if (cl > 1) tc::cluster_sync();   // no CTA leaves while its sums are being read
+  if (cl > 1) tc::cluster_sync();   // no CTA leaves, or forms new sums, while its sums are being read
+  else __syncthreads();
+  }
 }
 
 int lora_outer(Ctx* c, const LoraLayer& l, const float* u, const void* x, int F, int accumulate,
@@ -183,12 +194,16 @@ int lora_outer(Ctx* c, const LoraLayer& l, const float* u, const void* x, int F,
   p.adapter = l.adapter;
   p.accumulate = accumulate;
   p.out = out;
+  p.n = l.n;
   p.cluster = 1;
   while (p.cluster < 8 && l.T > 32 * p.cluster) p.cluster *= 2;
-  const dim3 grid((F + LO_FEATS - 1) / LO_FEATS * p.cluster, (l.R + LO_RANKS - 1) / LO_RANKS, l.n);
+  const int gx = (F + LO_FEATS - 1) / LO_FEATS * p.cluster, gy = (l.R + LO_RANKS - 1) / LO_RANKS;
+  // two CTAs fit on an SM
+  const dim3 grid(gx, gy, std::max(1, std::min(l.n, 2 * c->num_sms / (gx * gy))));
+  const int smem = LO_SMEM + (l.n + 31) / 32 * 4;
   auto kernel = l.dtype == GPTQ_BF16 ? k_lora_outer<true> : k_lora_outer<false>;
-  GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LO_SMEM));
-  GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, p.cluster, kernel, grid, dim3(LO_THREADS), LO_SMEM, p));
+  GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, p.cluster, kernel, grid, dim3(LO_THREADS), smem, p));
   return GPTQ_OK;
 }
 

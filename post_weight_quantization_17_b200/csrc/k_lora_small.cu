@@ -1,12 +1,14 @@
 // The packed layer with adapters for a few tokens (decoding): up to 32 tokens at once.
 //
-// Bound by reading the codes from HBM, so the kernel is built around that stream: every warp reads
-// its codes straight into registers, 16 bytes a lane (4 lanes cover the 64 bytes of a row's 128
-// 4-bit codes), a step ahead of their use, and multiplies on mma.sync (16 rows x 8 tokens x 16
-// columns).  The tensor instruction's column order is free as long as both operands share it, so
-// lane t of a row's four holds columns 32 t .. 32 t + 31 of each 128-column step: its codes are one
-// 16-byte load, its activations four, and neither passes through shared memory.  (c - z) is exact in
-// 16 bits; a step's fp32 sum is scaled by the group's Δ, so Ŵ is never rounded.
+// Bound by reading the codes from HBM, so the kernel is built around that stream: every lane copies
+// its own codes, 16 bytes at a time (4 lanes cover the 64 bytes of a row's 128 4-bit codes), into its
+// own slots of a ring in shared memory several steps ahead of their use (no barrier is needed, and
+// 128 KB per SM are on their way), and multiplies on mma.sync (16 rows x 8 tokens x 16 columns).  The
+// tensor instruction's column order is free as long as both operands share it, so lane t of a row's
+// four holds columns 32 t .. 32 t + 31 of each 128-column step: its codes are one 16-byte piece and
+// its activations four.  The grid of four steps is read at once, a step to each of the four lanes, and
+// passed round by shuffles.  (c - z) is exact in 16 bits; a step's fp32 sum is scaled by the group's
+// Δ, so Ŵ is never rounded.
 //
 // A X runs in the same launch, as CTAs of its own (one warp per token, rank index and 4096
 // columns); k_lora_join then adds the K splits of the base product in a fixed order, forms
@@ -22,6 +24,9 @@ constexpr int LS_THREADS = 256;
 // 16-row tiles per warp: two halve the reads of X per code; at 32 tokens the registers of their
 // sums leave room for one (two spilled).
 inline constexpr int ls_row_tiles(int token_tiles) { return token_tiles == 4 ? 1 : 2; }
+// steps of codes in the ring: 64 KB per CTA, two CTAs per SM
+__host__ __device__ constexpr int ls_depth(int token_tiles) { return token_tiles == 4 ? 8 : 4; }
+constexpr int LS_SMEM = 8 * 4 * 4 * 512;
 // rows per CTA: 4 row warps x 2 column warps
 constexpr int ls_rows(int token_tiles) { return 64 * ls_row_tiles(token_tiles); }
 constexpr int LS_KC = 4096;                    // columns per warp of A X
@@ -42,37 +47,28 @@ struct SmallParams {
   float* upart;              // [chunks, T, R]
 };
 
-// 16 bytes that are used once.
-__device__ __forceinline__ uint4 ld_stream16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
+// One piece (32 codes, BITS words) of a row into this lane's slot; zeros outside the row.
 template <int BITS>
-__device__ __forceinline__ void load_codes(const SmallParams& p, int row, int step, int t4,
-                                           uint32_t (&w)[BITS]) {
-#pragma unroll
-  for (int i = 0; i < BITS; ++i) w[i] = 0;
-  const int w0 = (step * 4 + t4) * BITS;
-  if (row >= p.m || w0 >= p.wpr) return;
-  const uint32_t* src = p.packed + (long long)row * p.wpr + w0;
-  if (p.wide && BITS == 4) {
-    const uint4 v = ld_stream16(src);
-    w[0] = v.x;
-    w[1 % BITS] = v.y;
-    w[2 % BITS] = v.z;
-    w[3 % BITS] = v.w;
-  } else if (p.wide && BITS == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(src);
-    w[0] = v.x;
-    w[1 % BITS] = v.y;
+__device__ __forceinline__ void copy_codes(const SmallParams& p, const uint32_t* src, int words_left,
+                                           uint32_t dst) {
+  if (p.wide && (BITS == 4 || BITS == 2)) {
+    const int n = words_left > 0 ? 4 * BITS : 0;
+    if (BITS == 4)
+      asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
+                   "l"(n ? src : p.packed), "r"(n)
+                   : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst),
+                   "l"(n ? src : p.packed), "r"(n)
+                   : "memory");
   } else {
 #pragma unroll
-    for (int i = 0; i < BITS; ++i)
-      if (w0 + i < p.wpr) w[i] = src[i];
+    for (int i = 0; i < BITS; ++i) {
+      const int n = i < words_left ? 4 : 0;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * i),
+                   "l"(n ? src + i : p.packed), "r"(n)
+                   : "memory");
+    }
   }
 }
 
@@ -115,8 +111,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2) k_lora_small(SmallParams p, Dev
     small_shrink<BF16>(p, st);
     return;
   }
-  constexpr int LS_MT = NT == 4 ? 1 : 2;
-  __shared__ float joined[4][32][LS_MT * NT * 4 + 1];
+  constexpr int LS_MT = NT == 4 ? 1 : 2, DEPTH = ls_depth(NT), PIECES = 2 * LS_MT;
+  extern __shared__ __align__(16) uint8_t ls_smem[];
   const int bid = blockIdx.x - p.shrink_ctas;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wr = warp & 3, wk = warp >> 2, g = lane >> 2, t4 = lane & 3;
@@ -124,75 +120,160 @@ __global__ void __launch_bounds__(LS_THREADS, 2) k_lora_small(SmallParams p, Dev
   const int n = min(p.steps, (split + 1) * p.per) - split * p.per;
   const int s0 = split * p.per + (wk ? (n + 1) / 2 : 0), s1 = split * p.per + (wk ? n : (n + 1) / 2);
   float acc[LS_MT][NT][4] = {};
-  uint32_t cw[LS_MT][2][BITS];
-  float sc[LS_MT][2];
-  int zs[LS_MT][2];
   bool bad = false;
 
-  auto fetch = [&](int s) {
-    const int gi = p.group_steps ? s / p.group_steps : 0;
+  // Integer instructions bound this loop once the loads are far enough ahead (ALU pipe 72 % busy at
+  // 2.7 TB/s with addresses and checks formed in every step), so pointers move by constants, rows and
+  // tokens outside are clamped instead of tested (their results are not stored), and only the last
+  // step of a row that is not a multiple of 128 columns is checked.
+  // This lane's slots: [DEPTH][PIECES] of 16 bytes, 32 lanes side by side.
+  const uint8_t* const slot0 = ls_smem + warp * (DEPTH * PIECES * 512) + lane * 16;
+  const uint32_t slot0_u = (uint32_t)__cvta_generic_to_shared(slot0);
+  const uint32_t* csrc[PIECES];
 #pragma unroll
-    for (int mt = 0; mt < LS_MT; ++mt)
+  for (int i = 0; i < PIECES; ++i)
+    csrc[i] = p.packed + (long long)min(row0 + 8 * i, p.m - 1) * p.wpr + (s0 * 4 + t4) * BITS;
+  int ahead = s0, put = 0;   // the next step to copy, and its place
+  auto copy_step = [&] {
+    if (ahead < s1) {
+      const int left = p.wpr - (ahead * 4 + t4) * BITS;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = row0 + 16 * mt + 8 * h;
-        load_codes<BITS>(p, row, s, t4, cw[mt][h]);
-        const long long at = (long long)min(row, p.m - 1) * p.ng + gi;
-        sc[mt][h] = p.scales[at];
-        zs[mt][h] = p.zeros[at];
-      }
-  };
-  if (s0 < s1) fetch(s0);
-  for (int s = s0; s < s1; ++s) {
-    uint32_t cur[LS_MT][2][BITS], zz[LS_MT][2];
-    float delta[LS_MT][2];
-#pragma unroll
-    for (int mt = 0; mt < LS_MT; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < BITS; ++i) cur[mt][h][i] = cw[mt][h][i];
-        delta[mt][h] = sc[mt][h];
-        int z = zs[mt][h];
-        if (z < 0 || z > 15) {
-          bad = true;
-          z = 0;
-        }
-        zz[mt][h] = zero_pair<BF16>(z);
-      }
-    if (s + 1 < s1) fetch(s + 1);
-    float dd[LS_MT][NT][4] = {};
-    const int k0 = s * 128 + t4 * 32;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint4 x[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int t = nt * 8 + g;
-        x[nt] = make_uint4(0, 0, 0, 0);
-        if (t < p.T && k0 + 8 * q < p.d)
-          x[nt] = *reinterpret_cast<const uint4*>((const uint16_t*)p.X + (long long)t * p.d + k0 + 8 * q);
-      }
-#pragma unroll
-      for (int mt = 0; mt < LS_MT; ++mt) {
-        uint32_t u[4], v[4];
-        centered8<BF16>(eight_codes<BITS>(cur[mt][0], q), zz[mt][0], u);
-        centered8<BF16>(eight_codes<BITS>(cur[mt][1], q), zz[mt][1], v);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816<BF16>(dd[mt][nt], u[0], v[0], u[1], v[1], x[nt].x, x[nt].y);
-          mma16816<BF16>(dd[mt][nt], u[2], v[2], u[3], v[3], x[nt].z, x[nt].w);
-        }
+      for (int i = 0; i < PIECES; ++i) {
+        copy_codes<BITS>(p, csrc[i], left, slot0_u + (put * PIECES + i) * 512);
+        csrc[i] += 4 * BITS;
       }
     }
+    ++ahead;
+    put = (put + 1) % DEPTH;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-    for (int mt = 0; mt < LS_MT; ++mt)
+  for (int i = 0; i < DEPTH - 1; ++i) copy_step();
+  // the grid of steps s .. s + 3: lane t of a row's four reads step s + t
+  float sc[PIECES];
+  uint32_t zs[PIECES];
+  auto fetch_grid = [&](int s, float (&d)[PIECES], uint32_t (&zz)[PIECES]) {
+    const int gi = p.group_steps ? min(s + t4, p.steps - 1) / p.group_steps : 0;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int i = 0; i < PIECES; ++i) {
+      const long long at = (long long)min(row0 + 8 * i, p.m - 1) * p.ng + gi;
+      d[i] = p.scales[at];
+      zz[i] = (uint32_t)p.zeros[at];
+    }
+  };
+  auto zero_pairs = [&](uint32_t (&zz)[PIECES]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[mt][nt][i] = fmaf(delta[mt][i >> 1], dd[mt][nt][i], acc[mt][nt][i]);
+    for (int i = 0; i < PIECES; ++i) {
+      if (zz[i] > 15u) {
+        bad = true;
+        zz[i] = 0;
+      }
+      zz[i] = zero_pair<BF16>((int)zz[i]);
+    }
+  };
+  if (s0 < s1) fetch_grid(s0, sc, zs);
+  const uint4* xrow[NT];   // this lane's columns of its token of every tile
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+    xrow[nt] = reinterpret_cast<const uint4*>((const uint16_t*)p.X + (long long)min(nt * 8 + g, p.T - 1) * p.d +
+                                              s0 * 128 + t4 * 32);
+  const int ragged = p.d % 128 ? p.steps - 1 : -1;   // the step that ends before its last column
+  auto load_x = [&](int s, int q, uint4 (&x)[NT]) {   // q 4: the first of the next step
+    if ((s == ragged && s * 128 + t4 * 32 + 8 * q >= p.d && q < 4) ||
+        (q == 4 && (s + 1 >= s1 || (s + 1 == ragged && (s + 1) * 128 + t4 * 32 >= p.d)))) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[nt] = make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[nt] = xrow[nt][q == 4 ? 16 : q];
+    }
+  };
+  uint4 x[2][NT];
+  if (s0 < s1) load_x(s0, 0, x[0]);
+  int get = 0;
+  for (int sb = s0; sb < s1; sb += 4) {
+    float sn[PIECES];
+    uint32_t zn[PIECES];
+    if (sb + 4 < s1) fetch_grid(sb + 4, sn, zn);
+    zero_pairs(zs);
+    const int se = min(sb + 4, s1);
+    for (int s = sb; s < se; ++s) {
+      copy_step();
+      asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+      uint32_t cur[PIECES][BITS], zz[PIECES];
+      float delta[PIECES];
+      const int from = (lane & ~3) | (s - sb);
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const uint8_t* slot = slot0 + (get * PIECES + i) * 512;
+        if (BITS == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(slot);
+          cur[i][0] = v.x;
+          cur[i][1 % BITS] = v.y;
+          cur[i][2 % BITS] = v.z;
+          cur[i][3 % BITS] = v.w;
+        } else {
+#pragma unroll
+          for (int w = 0; w < BITS; ++w) cur[i][w] = reinterpret_cast<const uint32_t*>(slot)[w];
+        }
+        delta[i] = __shfl_sync(0xffffffffu, sc[i], from);
+        zz[i] = __shfl_sync(0xffffffffu, zs[i], from);
+      }
+      get = (get + 1) % DEPTH;
+      float dd[LS_MT][NT][4] = {};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        load_x(s, q + 1, x[(q + 1) & 1]);
+        if (q == 3) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) xrow[nt] += 16;
+        }
+        const uint4 (&xq)[NT] = x[q & 1];
+        // Eight tokens: codes two apart make a pair (one byte permute each, from the even and the odd
+        // nibbles), and the activations are put in the same order; with more tokens that would cost
+        // more than the pairs in column order do.
+        uint4 xs[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          xs[nt] = NT == 1 ? make_uint4(__byte_perm(xq[nt].x, xq[nt].y, 0x5410),
+                                        __byte_perm(xq[nt].z, xq[nt].w, 0x5410),
+                                        __byte_perm(xq[nt].x, xq[nt].y, 0x7632),
+                                        __byte_perm(xq[nt].z, xq[nt].w, 0x7632))
+                           : xq[nt];
+#pragma unroll
+        for (int mt = 0; mt < LS_MT; ++mt) {
+          uint32_t u[4], v[4];
+          if (NT == 1) {
+            centered8_even_odd<BF16>(eight_codes<BITS>(cur[2 * mt], q), zz[2 * mt], u);
+            centered8_even_odd<BF16>(eight_codes<BITS>(cur[2 * mt + 1], q), zz[2 * mt + 1], v);
+          } else {
+            centered8<BF16>(eight_codes<BITS>(cur[2 * mt], q), zz[2 * mt], u);
+            centered8<BF16>(eight_codes<BITS>(cur[2 * mt + 1], q), zz[2 * mt + 1], v);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816<BF16>(dd[mt][nt], u[0], v[0], u[1], v[1], xs[nt].x, xs[nt].y);
+            mma16816<BF16>(dd[mt][nt], u[2], v[2], u[3], v[3], xs[nt].z, xs[nt].w);
+          }
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < LS_MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[mt][nt][i] = fmaf(delta[2 * mt + (i >> 1)], dd[mt][nt][i], acc[mt][nt][i]);
+    }
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      sc[i] = sn[i];
+      zs[i] = zn[i];
+    }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();   // the ring's memory serves the join of the two column warps
+  float (*joined)[32][LS_MT * NT * 4 + 1] = reinterpret_cast<float (*)[32][LS_MT * NT * 4 + 1]>(ls_smem);
   if (bad) raise_error(st, GPTQ_ERR_ARG, row0);
   float* mine = joined[wr][lane];
   if (wk == 1) {
@@ -361,8 +442,10 @@ int launch_small(Ctx* c, const SmallParams& p, int grid, bool bf) {
   const int nt = token_tiles(p.T);
 #define GPTQ_SMALL(NT)                                                                              \
   do {                                                                                              \
-    if (bf) GPTQ_LAUNCH(c, (k_lora_small<BITS, NT, true>), grid, LS_THREADS, 0, p, c->status);      \
-    else GPTQ_LAUNCH(c, (k_lora_small<BITS, NT, false>), grid, LS_THREADS, 0, p, c->status);        \
+    auto kernel = bf ? k_lora_small<BITS, NT, true> : k_lora_small<BITS, NT, false>;                \
+    GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(                                                        \
+                           kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LS_SMEM));          \
+    GPTQ_LAUNCH(c, kernel, grid, LS_THREADS, LS_SMEM, p, c->status);                                \
   } while (0)
   if (nt == 1) GPTQ_SMALL(1);
   else if (nt == 2) GPTQ_SMALL(2);

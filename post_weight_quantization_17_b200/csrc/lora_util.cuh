@@ -71,6 +71,27 @@ __device__ __forceinline__ void centered8(uint32_t word, uint32_t zz, uint32_t (
     }
   }
 }
+// The same in the order (0, 2), (4, 6), (1, 3), (5, 7): the even and the odd nibbles as bytes, to which
+// one byte permute each adds the constant high byte.
+template <bool BF16>
+__device__ __forceinline__ void centered8_even_odd(uint32_t word, uint32_t zz, uint32_t (&out)[4]) {
+  constexpr uint32_t high = BF16 ? 0x43434343u : 0x64646464u;
+  const uint32_t even = word & 0x0F0F0F0Fu, odd = (word >> 4) & 0x0F0F0F0Fu;
+  const uint32_t t[4] = {__byte_perm(even, high, 0x4140), __byte_perm(even, high, 0x4342),
+                         __byte_perm(odd, high, 0x4140), __byte_perm(odd, high, 0x4342)};
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    if (BF16) {
+      const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&t[p]),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&zz));
+      out[p] = *reinterpret_cast<const uint32_t*>(&d);
+    } else {
+      const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&t[p]),
+                                *reinterpret_cast<const __half2*>(&zz));
+      out[p] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+  }
+}
 // 128 + z or 1024 + z in both halves: z in 0..15 sits in the mantissa's last bits (a bf16 in
 // [128, 256) steps by 1, an fp16 in [1024, 2048) too).
 template <bool BF16> __device__ __forceinline__ uint32_t zero_pair(int z) {
