@@ -209,11 +209,10 @@ int forward_any(Ctx* c, const LoraLayer& l, const TX* X, void* Y, bool y_f32, fl
   return GPTQ_OK;
 }
 
-int outer(Ctx* c, const LoraLayer& l, const float* u, const void* x, int F, int accumulate,
-          float* out) {
-  if (l.dtype != GPTQ_F32) return lora_outer(c, l, u, x, F, accumulate, out);
-  GPTQ_LAUNCH(c, k_lora_outer_f32, dim3((F + 127) / 128, (l.R + 7) / 8, l.n), 128, 0, u,
-              (const float*)x, l.T, F, l.R, l.adapter, accumulate, out);
+int outer_f32(Ctx* c, const LoraLayer& l, const float* u, const float* x, int F, int accumulate,
+              float* out) {
+  GPTQ_LAUNCH(c, k_lora_outer_f32, dim3((F + 127) / 128, (l.R + 7) / 8, l.n), 128, 0, u, x, l.T, F,
+              l.R, l.adapter, accumulate, out);
   return GPTQ_OK;
 }
 
@@ -284,9 +283,10 @@ int lora_backward(Ctx* c, const LoraLayer& l, const void* dY, const void* X, con
     else if (l.dtype == GPTQ_F16) rc = dx_any(c, l, (const __half*)dY, (__half*)dX, G);
     else rc = dx_any(c, l, (const float*)dY, (float*)dX, G);
   }
-  if (!rc && dA) rc = outer(c, l, G, X, l.d, accumulate, dA);
-  if (!rc && dB) rc = outer(c, l, U, dY, l.m, accumulate, dB);
-  return rc;
+  if (rc || (!dA && !dB)) return rc;
+  if (l.dtype != GPTQ_F32) return lora_outers(c, l, G, X, dA, U, dY, dB, accumulate);
+  if (dA && (rc = outer_f32(c, l, G, (const float*)X, l.d, accumulate, dA))) return rc;
+  return dB ? outer_f32(c, l, U, (const float*)dY, l.m, accumulate, dB) : GPTQ_OK;
 }
 
 }  // namespace gptq

@@ -19,16 +19,23 @@
 namespace gptq {
 
 constexpr int LO_THREADS = 256;
-constexpr int LO_FEATS = 128, LO_RANKS = 32, LO_PAD = 68;
-constexpr int LO_SMEM = (8 * LO_RANKS * LO_PAD + LO_RANKS * LO_FEATS) * 4;
+constexpr int LO_FEATS = 128, LO_PAD = 68;
+// Shared memory: the warps' sums [8][16 RT][64 + 4], the CTA's [16 RT][128], the adapters' bits.  Up to
+// rank 16 a tile of 16 ranks takes half of it, and more CTAs fit on an SM.
+constexpr int lo_smem(int rank_tiles) { return (8 * 16 * rank_tiles * LO_PAD + 16 * rank_tiles * LO_FEATS) * 4; }
 
-struct OuterParams {
+struct OuterProblem {
   const float* u;          // [T, R]
   const void* x;           // [T, F]
-  int T, F, R, wide;       // wide: x may be read in 16-byte pieces
-  const int32_t* adapter;
-  int accumulate, cluster, n;
   float* out;              // [n, R, F]
+  int F, wide;             // wide: x may be read in 16-byte pieces
+};
+struct OuterParams {
+  OuterProblem two[2];
+  int first_ctas;          // CTAs of two[0]
+  int T, R, n;
+  const int32_t* adapter;
+  int accumulate, cluster;
 };
 
 __device__ __forceinline__ void mma_tf32_1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -40,27 +47,43 @@ __device__ __forceinline__ void mma_tf32_1688(float (&d)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(OuterParams p) {
+// Two groups of 8 tokens of a warp: a lane's 8 features of four of the tokens, and their ranks.
+template <int RT> struct OuterGroup {
+  uint32_t members;
+  uint4 x[2][2];
+  float u[2][2][2 * RT];
+};
+
+template <int RT, bool BF16>
+__global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_constant__ OuterParams p) {
+  constexpr int LO_RANKS = 16 * RT;
   pdl_wait();
   pdl_release();
-  extern __shared__ __align__(16) float lo_smem[];
-  float* sums = lo_smem;                                   // [8 warps][32 ranks][64 + 4]
-  float* total = lo_smem + 8 * LO_RANKS * LO_PAD;          // [32 ranks][128]
+  extern __shared__ __align__(16) float lo_smem_[];
+  float* sums = lo_smem_;                                   // [8 warps][ranks][64 + 4]
+  float* total = lo_smem_ + 8 * LO_RANKS * LO_PAD;          // [ranks][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int wf = warp & 1, wt = warp >> 1;
   const int cl = p.cluster, rank = blockIdx.x % cl;
-  const int f0 = (int)(blockIdx.x / cl) * LO_FEATS + wf * 64, j0 = blockIdx.y * LO_RANKS;
-  const int f = f0 + 8 * g, fb = (int)(blockIdx.x / cl) * LO_FEATS;
+  const bool second = (int)blockIdx.x >= p.first_ctas;
+  const float* pu = second ? p.two[1].u : p.two[0].u;
+  const uint16_t* px = (const uint16_t*)(second ? p.two[1].x : p.two[0].x);
+  float* const out = second ? p.two[1].out : p.two[0].out;
+  const int F = second ? p.two[1].F : p.two[0].F, wide = second ? p.two[1].wide : p.two[0].wide;
+  const int fb = ((int)blockIdx.x - (second ? p.first_ctas : 0)) / cl * LO_FEATS;
+  const int f0 = fb + wf * 64, j0 = blockIdx.y * LO_RANKS, f = f0 + 8 * g;
   // which adapters have tokens
   uint32_t* present = reinterpret_cast<uint32_t*>(total + LO_RANKS * LO_FEATS);
   for (int i = threadIdx.x; i < (p.n + 31) / 32; i += LO_THREADS) present[i] = 0;
   __syncthreads();
-#pragma unroll 4
-  for (int t = threadIdx.x; t < p.T; t += LO_THREADS) {
-    const int a = p.adapter[t];
-    if (a >= 0 && a < p.n && !((present[a >> 5] >> (a & 31)) & 1u))
-      atomicOr(&present[a >> 5], 1u << (a & 31));
+  for (int t = threadIdx.x; t < p.T; t += 8 * LO_THREADS) {
+    int id[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) id[i] = t + i * LO_THREADS < p.T ? p.adapter[t + i * LO_THREADS] : -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (id[i] >= 0 && id[i] < p.n && !((present[id[i] >> 5] >> (id[i] & 31)) & 1u))
+        atomicOr(&present[id[i] >> 5], 1u << (id[i] & 31));
   }
   __syncthreads();
   for (int a = blockIdx.z; a < p.n; a += gridDim.z) {
@@ -68,58 +91,58 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(OuterParams p) {
     if (!p.accumulate)
       for (int e = rank * LO_THREADS + threadIdx.x; e < LO_RANKS * LO_FEATS; e += cl * LO_THREADS) {
         const int j = j0 + e / LO_FEATS, ff = fb + e % LO_FEATS;
-        if (j < p.R && ff < p.F) p.out[((long long)a * p.R + j) * p.F + ff] = 0.f;
+        if (j < p.R && ff < F) out[((long long)a * p.R + j) * F + ff] = 0.f;
       }
     continue;
   }
-  float acc[2][8][4] = {};
+  float acc[RT][8][4] = {};
+  // this warp's groups: i0, i0 + stride, ...; two at a time, the next two on their way
   const int groups = (p.T + 7) / 8, stride = 4 * cl;
-  for (int i0 = rank * 4 + wt; i0 < groups; i0 += 4 * stride) {
-    // the adapters of four 8-token groups
-    const int mt = (i0 + (lane >> 3) * stride) * 8 + (lane & 7);
-    const uint32_t members = __ballot_sync(0xffffffffu, mt < p.T && p.adapter[mt] == a);
-    if (!members) continue;
-    uint4 x[4][2];
-    float u[4][2][4];
+  auto ids = [&](int i) {
+    const int t = (i + ((lane >> 3) & 1) * stride) * 8 + (lane & 7);
+    return lane < 16 && i < groups && t < p.T ? p.adapter[t] : -1;
+  };
+  auto fetch = [&](OuterGroup<RT>& o, int i, int id) {
+    o.members = __ballot_sync(0xffffffffu, id == a);
+    if (!o.members) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t m8 = (members >> (8 * i)) & 0xffu;
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int k = t4 + 4 * h;
-        const long long t = (long long)(i0 + i * stride) * 8 + k;
-        const bool in = (m8 >> k) & 1u;
-        x[i][h] = make_uint4(0, 0, 0, 0);
-        if (in && p.wide) {
-          if (f < p.F)
-            x[i][h] = *reinterpret_cast<const uint4*>((const uint16_t*)p.x + t * p.F + f);
+        const int r8 = t4 + 4 * h;
+        const long long t = (long long)(i + k * stride) * 8 + r8;
+        const bool in = (o.members >> (8 * k + r8)) & 1u;
+        o.x[k][h] = make_uint4(0, 0, 0, 0);
+        if (in && wide) {
+          if (f < F) o.x[k][h] = *reinterpret_cast<const uint4*>(px + t * F + f);
         } else if (in) {
-          const uint16_t* src = (const uint16_t*)p.x + t * p.F + f;
+          const uint16_t* src = px + t * F + f;
           uint32_t w[4] = {};
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (f + e < p.F) w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
-          x[i][h] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (f + e < F) w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+          o.x[k][h] = make_uint4(w[0], w[1], w[2], w[3]);
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {   // ranks g, g + 8, g + 16, g + 24
+        for (int r = 0; r < 2 * RT; ++r) {   // ranks g, g + 8, ...
           const int j = j0 + g + 8 * r;
-          u[i][h][r] = (in && j < p.R) ? p.u[t * p.R + j] : 0.f;
+          o.u[k][h][r] = (in && j < p.R) ? pu[t * p.R + j] : 0.f;
         }
       }
     }
+  };
+  auto multiply = [&](const OuterGroup<RT>& o) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!((members >> (8 * i)) & 0xffu)) continue;
-      const uint32_t x0[4] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w};
-      const uint32_t x1[4] = {x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+    for (int k = 0; k < 2; ++k) {
+      if (!((o.members >> (8 * k)) & 0xffu)) continue;
+      const uint32_t x0[4] = {o.x[k][0].x, o.x[k][0].y, o.x[k][0].z, o.x[k][0].w};
+      const uint32_t x1[4] = {o.x[k][1].x, o.x[k][1].y, o.x[k][1].z, o.x[k][1].w};
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (j0 + 16 * m >= p.R) break;
+      for (int m = 0; m < RT; ++m) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {   // (rank g, token t4), (g + 8, t4), (g, t4 + 4), (g + 8, t4 + 4)
-          const float v = u[i][e >> 1][2 * m + (e & 1)];
+          const float v = o.u[k][e >> 1][2 * m + (e & 1)];
           const bool finite = fabsf(v) <= 3.0e38f;   // the split is for finite values
           const float h = finite ? tc::tf32_rna(v) : v;
           hi[e] = __float_as_uint(h);
@@ -135,11 +158,25 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(OuterParams p) {
         }
       }
     }
+  };
+  {
+    const int i0 = rank * 4 + wt;
+    OuterGroup<RT> one, other;
+    int id_next = ids(i0 + 2 * stride);
+    fetch(one, i0, ids(i0));
+    for (int i = i0; i < groups; i += 4 * stride) {
+      const int id_after = ids(i + 4 * stride);
+      fetch(other, i + 2 * stride, id_next);
+      multiply(one);
+      id_next = ids(i + 6 * stride);
+      fetch(one, i + 4 * stride, id_after);
+      multiply(other);
+    }
   }
   // tile i's column n is feature 8 n + i: a lane holds features 16 t4 + (0..7) and + 8
   float* mine = sums + warp * LO_RANKS * LO_PAD;
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int m = 0; m < RT; ++m)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       float4* dst = reinterpret_cast<float4*>(mine + (16 * m + 8 * (c >> 1) + g) * LO_PAD + 16 * t4 +
@@ -174,8 +211,8 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(OuterParams p) {
         v = total[e];
       s += v;
     }
-    if (j < p.R && ff < p.F) {
-      float* o = p.out + ((long long)a * p.R + j) * p.F + ff;
+    if (j < p.R && ff < F) {
+      float* o = out + ((long long)a * p.R + j) * F + ff;
       *o = p.accumulate ? *o + s : s;
     }
   }
@@ -184,24 +221,30 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(OuterParams p) {
   }
 }
 
-int lora_outer(Ctx* c, const LoraLayer& l, const float* u, const void* x, int F, int accumulate,
-               float* out) {
+// dA from (G, X) and dB from (U, dY) in one launch (each alone is too short to fill the GPU); either may
+// be left out (null).
+int lora_outers(Ctx* c, const LoraLayer& l, const float* G, const void* X, float* dA, const float* U,
+                const void* dY, float* dB, int accumulate) {
   OuterParams p{};
-  p.u = u;
-  p.x = x;
-  p.T = l.T; p.F = F; p.R = l.R;
-  p.wide = F % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0;
+  p.T = l.T; p.R = l.R; p.n = l.n;
   p.adapter = l.adapter;
   p.accumulate = accumulate;
-  p.out = out;
-  p.n = l.n;
   p.cluster = 1;
   while (p.cluster < 8 && l.T > 32 * p.cluster) p.cluster *= 2;
-  const int gx = (F + LO_FEATS - 1) / LO_FEATS * p.cluster, gy = (l.R + LO_RANKS - 1) / LO_RANKS;
-  // two CTAs fit on an SM
-  const dim3 grid(gx, gy, std::max(1, std::min(l.n, 2 * c->num_sms / (gx * gy))));
-  const int smem = LO_SMEM + (l.n + 31) / 32 * 4;
-  auto kernel = l.dtype == GPTQ_BF16 ? k_lora_outer<true> : k_lora_outer<false>;
+  auto problem = [](const float* u, const void* x, float* out, int F) {
+    return OuterProblem{u, x, out, F, F % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0};
+  };
+  const int ca = dA ? (l.d + LO_FEATS - 1) / LO_FEATS * p.cluster : 0;
+  const int cb = dB ? (l.m + LO_FEATS - 1) / LO_FEATS * p.cluster : 0;
+  p.two[0] = problem(G, X, dA, l.d);
+  p.two[1] = problem(U, dY, dB, l.m);
+  p.first_ctas = ca;
+  const int rt = l.R <= 16 ? 1 : 2, ranks = (l.R + 16 * rt - 1) / (16 * rt);
+  const dim3 grid(ca + cb, ranks, std::max(1, std::min(l.n, 4 * c->num_sms / ((ca + cb) * ranks))));
+  const int smem = lo_smem(rt) + (l.n + 31) / 32 * 4;
+  const bool bf = l.dtype == GPTQ_BF16;
+  auto kernel = rt == 1 ? (bf ? k_lora_outer<1, true> : k_lora_outer<1, false>)
+                        : (bf ? k_lora_outer<2, true> : k_lora_outer<2, false>);
   GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, p.cluster, kernel, grid, dim3(LO_THREADS), smem, p));
   return GPTQ_OK;

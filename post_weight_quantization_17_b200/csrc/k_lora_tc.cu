@@ -673,12 +673,13 @@ __device__ __forceinline__ void list_slots(const ShrinkParams& p, int nt) {
   if (tid == 0) out[0] = total;
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(LU_THREADS) k_lora_shrink(ShrinkParams p, DeviceStatus* st) {
+// NTL: 8-rank tiles of a pass (16 or 32 ranks, so that the sums leave registers for two CTAs per SM)
+template <bool BF16, int NTL>
+__global__ void __launch_bounds__(LU_THREADS, 2) k_lora_shrink(ShrinkParams p, DeviceStatus* st) {
   pdl_wait();
   pdl_release();
-  __shared__ float sums[8][32][64 / 4 + 1];   // a quarter of the ranks at a time, per warp
-  __shared__ float total[32 * 64];
+  __shared__ float sums[8][32][16 + 1];   // 16 ranks at a time, per warp
+  __shared__ float total[32 * 8 * NTL];
   const int cl = p.cluster, rank = blockIdx.x % cl;
   if ((int)blockIdx.x >= p.shrink_ctas) {
     if ((int)blockIdx.x - p.shrink_ctas < p.ttiles) list_slots(p, blockIdx.x - p.shrink_ctas);
@@ -690,6 +691,22 @@ __global__ void __launch_bounds__(LU_THREADS) k_lora_shrink(ShrinkParams p, Devi
   // features in steps of 64, spread over the cluster's CTAs and their warps in contiguous runs
   const int steps = (p.F + 63) / 64, lanes = cl * 8, per = (steps + lanes - 1) / lanes;
   const int s0 = min(steps, (rank * 8 + warp) * per), s1 = min(steps, s0 + per);
+  const uint16_t* xb = (const uint16_t*)p.x + (long long)t0 * p.F;
+  auto load_x = [&](uint4 (&xv)[2][2], int k) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 16 * mt + 8 * h + g;
+        xv[mt][h] = (k < p.F && t0 + row < p.T)
+                        ? *reinterpret_cast<const uint4*>(xb + (long long)row * p.F + k)
+                        : make_uint4(0, 0, 0, 0);
+      }
+  };
+  // the first 64 columns stay in registers: with the cluster's split most warps have no others
+  uint4 x0[2][2][2];
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) load_x(x0[hh], s0 < s1 ? s0 * 64 + hh * 32 + t4 * 8 : p.F);
   // tokens without an adapter
   if (rank == 0)
     for (int e = threadIdx.x; e < 32 * p.Rp; e += LU_THREADS) {
@@ -704,48 +721,42 @@ __global__ void __launch_bounds__(LU_THREADS) k_lora_shrink(ShrinkParams p, Devi
     const int a = __shfl_sync(0xffffffffu, id, __ffs(todo) - 1);
     const uint32_t mine = __ballot_sync(0xffffffffu, id == a);
     todo &= ~mine;
-    for (int j0 = 0; j0 < p.Rp; j0 += 64) {
-      const int ntile = min(8, (p.R - j0 + 7) / 8);   // <= 0 behind R cannot occur: Rp - R < 32
-      float acc[2][8][4] = {};
-      const uint16_t* xb = (const uint16_t*)p.x + (long long)t0 * p.F;
+    for (int j0 = 0; j0 < p.Rp; j0 += 8 * NTL) {
+      const int ntile = min(NTL, (p.R - j0 + 7) / 8);   // <= 0 behind R
+      float acc[2][NTL][4] = {};
       const uint16_t* wb = (const uint16_t*)p.w + ((long long)a * p.R + j0) * p.F;
-      for (int s = s0; s < s1; ++s) {
+      auto multiply = [&](const uint4 (&xv)[2][2], int k) {
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int k = s * 64 + hh * 32 + t4 * 8;
-          const bool in = k < p.F;
-          uint4 xv[2][2];
+        for (int nt = 0; nt < NTL; ++nt) {
+          if (nt >= ntile) break;
+          const int j = 8 * nt + g;
+          const uint4 wv = (k < p.F && j0 + j < p.R)
+                               ? *reinterpret_cast<const uint4*>(wb + (long long)j * p.F + k)
+                               : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int row = 16 * mt + 8 * h + g;
-              xv[mt][h] = (in && t0 + row < p.T)
-                              ? *reinterpret_cast<const uint4*>(xb + (long long)row * p.F + k)
-                              : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-          for (int nt = 0; nt < 8; ++nt) {
-            if (nt >= ntile) break;
-            const int j = 8 * nt + g;
-            const uint4 wv = (in && j0 + j < p.R)
-                                 ? *reinterpret_cast<const uint4*>(wb + (long long)j * p.F + k)
-                                 : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              mma16816<BF16>(acc[mt][nt], xv[mt][0].x, xv[mt][1].x, xv[mt][0].y, xv[mt][1].y, wv.x,
-                             wv.y);
-              mma16816<BF16>(acc[mt][nt], xv[mt][0].z, xv[mt][1].z, xv[mt][0].w, xv[mt][1].w, wv.z,
-                             wv.w);
-            }
+          for (int mt = 0; mt < 2; ++mt) {
+            mma16816<BF16>(acc[mt][nt], xv[mt][0].x, xv[mt][1].x, xv[mt][0].y, xv[mt][1].y, wv.x,
+                           wv.y);
+            mma16816<BF16>(acc[mt][nt], xv[mt][0].z, xv[mt][1].z, xv[mt][0].w, xv[mt][1].w, wv.z,
+                           wv.w);
           }
         }
+      };
+      if (s0 < s1) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) multiply(x0[hh], s0 * 64 + hh * 32 + t4 * 8);
+      }
+      for (int s = s0 + 1; s < s1; ++s) {
+        uint4 xv[2][2][2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) load_x(xv[hh], s * 64 + hh * 32 + t4 * 8);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) multiply(xv[hh], s * 64 + hh * 32 + t4 * 8);
       }
       // join the warps (fixed order), 16 ranks at a time
-      const int quarters = (min(64, p.Rp - j0) + 15) / 16;
+      const int quarters = NTL / 2;
 #pragma unroll
-      for (int quarter = 0; quarter < 4; ++quarter) {
-        if (quarter >= quarters) break;
+      for (int quarter = 0; quarter < NTL / 2; ++quarter) {
         __syncthreads();
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -760,7 +771,7 @@ __global__ void __launch_bounds__(LU_THREADS) k_lora_shrink(ShrinkParams p, Devi
           float v = 0.f;
 #pragma unroll
           for (int w = 0; w < 8; ++w) v += sums[w][e >> 4][e & 15];
-          total[(e >> 4) * 64 + 16 * quarter + (e & 15)] = v;
+          total[(e >> 4) * (8 * NTL) + 16 * quarter + (e & 15)] = v;
         }
       }
       if (cl > 1) tc::cluster_sync();
@@ -770,14 +781,14 @@ __global__ void __launch_bounds__(LU_THREADS) k_lora_shrink(ShrinkParams p, Devi
       const int rows = 32 / cl, cols = 16 * quarters;
       for (int e = threadIdx.x; e < rows * cols; e += LU_THREADS) {
         const int row = rank * rows + e / cols, col = e % cols, j = j0 + col;
-        if (!((mine >> row) & 1u)) continue;
+        if (!((mine >> row) & 1u) || j >= p.Rp) continue;
         float v = 0.f;
         for (int c = 0; c < cl; ++c) {
-          float u = total[row * 64 + col];
+          float u = total[row * (8 * NTL) + col];
           if (cl > 1)
             asm volatile("ld.shared::cluster.f32 %0, [%1];"
                          : "=f"(u)
-                         : "r"(tc::map_to_rank(&total[row * 64 + col], c))
+                         : "r"(tc::map_to_rank(&total[row * (8 * NTL) + col], c))
                          : "memory");
           v += u;
         }
@@ -1043,12 +1054,10 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
       s.cluster *= 2;
     s.shrink_ctas = tiles * s.cluster;
     const int grid = s.shrink_ctas + (int)round_up(s.ttiles, s.cluster);
-    if (bf)
-      GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, s.cluster, k_lora_shrink<true>, dim3(grid),
-                                            dim3(LU_THREADS), 0, s, c->status));
-    else
-      GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, s.cluster, k_lora_shrink<false>, dim3(grid),
-                                            dim3(LU_THREADS), 0, s, c->status));
+    auto kernel = l.R <= 16 ? (bf ? k_lora_shrink<true, 2> : k_lora_shrink<false, 2>)
+                            : (bf ? k_lora_shrink<true, 4> : k_lora_shrink<false, 4>);
+    GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, s.cluster, kernel, dim3(grid), dim3(LU_THREADS), 0, s,
+                                          c->status));
   } else {
     const int rc = lora_shrink_any(c, l, x, K, w1, u_tmp);
     if (rc) return rc;

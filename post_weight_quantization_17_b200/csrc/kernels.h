@@ -132,9 +132,10 @@ size_t lora_tc_bytes(const LoraLayer& l);
 int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, bool out_f32,
             float* low, size_t ws_offset);
 
-// 16-bit x: out [n, R, F] (+)= Σ_{t of adapter a} u [T, R]ᵀ x [T, F] (k_lora_outer.cu)
-int lora_outer(Ctx* c, const LoraLayer& l, const float* u, const void* x, int F, int accumulate,
-               float* out);
+// 16-bit X, dY: dA [n, R, d] (+)= Σ_{t of adapter a} G[t]ᵀ X[t], dB [n, R, m] (+)= Σ U[t]ᵀ dY[t]; either
+// may be null (k_lora_outer.cu)
+int lora_outers(Ctx* c, const LoraLayer& l, const float* G, const void* X, float* dA, const float* U,
+                const void* dY, float* dB, int accumulate);
 
 // ---- distillation from a teacher's top logits (k_distill.cu)
 struct DistillArgs {
