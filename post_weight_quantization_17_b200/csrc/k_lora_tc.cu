@@ -1,7 +1,10 @@
 // The packed layer with adapters for many tokens, on tcgen05: both directions of
 //   forward   out[t, r] = Σ_k X[t, k] Ŵ[r, k]  + Σ_j U[t, j] B[a_t, j, r]
 //   backward  out[t, k] = Σ_r dY[t, r] Ŵ[r, k] + Σ_j G[t, j] A[a_t, j, k]
-// as D[feature, token] tiles of 128 x BN.  The weight operand is made from the codes on the way into
+// as D[feature, token] tiles of 256 x BN on CTA pairs (cta_group::2): each CTA makes the weight operand
+// of its own 128 features and copies its half of the tokens, so that a stage costs 64 KB of its shared
+// memory's bandwidth (MMA reads, copies and stores) instead of the 96 KB that held a single-CTA version
+// at about 60 % of the tensor cores' rate.  The weight operand is made from the codes on the way into
 // shared memory; the stage's image is the same in both directions (row = weight row, 128 bytes = 64
 // columns, 128-byte swizzle), read K-major forward (the contraction runs along the row) and MN-major
 // backward (it runs down the rows), so one kernel serves both.
@@ -17,12 +20,16 @@
 //   shared memory (kind::tf32); the epilogue adds it to that adapter's tokens only, so one request's
 //   non-finite values never reach another's.
 //
-// Roles (one CTA per SM, persistent over tiles):
+// Roles (one CTA per SM, persistent over tiles; barriers that the MMAs wait for are the leader's, and
+// the other CTA's warps arrive on them remotely):
 //   warps 0-7     the weight operand: codes and grid of a unit, shared -> registers -> shared
 //   warps 8-15    epilogue: TMEM -> fp32 sums in registers -> out, or a split's partial
-//   warp 16       TMA producer of the tokens' operand (BN rows x 128 bytes per stage)
-//   warp 17       MMA issuer, owner of TMEM (two partial-sum buffers of BN columns)
+//   warp 16       TMA producer of the tokens' operand (BN / 2 rows x 128 bytes per stage)
+//   warp 17       MMA issuer (the leader's), owner of TMEM (two partial-sum buffers of BN columns)
 //   warp 18       copies of the codes (TMA boxes) and of the grid, some units ahead; 19 idle
+// The barriers' arrivals and waits are the plain ones, also across the pair: each CTA's shared memory is
+// written, fenced for the tensor core's proxy and read by that same SM's tensor core, and what crosses
+// the pair is the order alone.  With cluster-wide release and acquire a stage took 0.87 us for 0.53.
 // The grid is first turned column-major (k_lora_grid), so that the (Δ, z) of a unit's rows are one
 // contiguous copy: read in place they are 128 scattered words per step, and loads of codes and grid
 // into the weight warps' registers, though issued two to four stages ahead, took as long as the
@@ -43,9 +50,9 @@ constexpr float LT_F16_SCALE = 256.f;
 
 template <bool FWD, int BN>
 struct LtCfg {
-  static constexpr int X_BYTES = BN * 128;
+  static constexpr int X_BYTES = BN / 2 * 128;
   static constexpr int STAGE = LT_A_BYTES + X_BYTES;
-  static constexpr int NS = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
+  static constexpr int NS = BN == 256 ? 6 : 8;
   // a unit of codes and grid: 128 rows x 128 columns forward, 64 rows backward
   static constexpr int C_BYTES = FWD ? 8192 : 4096, G_BYTES = FWD ? 1024 : 512;
   static constexpr int NC = FWD ? 3 : 6;
@@ -59,7 +66,7 @@ struct LtParams {
   int T;
   int group_steps;          // groups in 128-column steps; 0: one grid per row
   const float2* grid;       // [n_g, m_pad] (Δ, z), zero behind m
-  int m_pad;
+  int m_pad, used;          // its columns, and how many n_g there are
   int mtiles, ttiles, splits;
   int units, per;           // the contraction in 128-column steps (forward) or 64-row stages
                             // (backward): in all and per split
@@ -85,6 +92,20 @@ __device__ __forceinline__ bool lt_try(uint64_t* bar, uint32_t parity) {
       : "r"(tc::smem_u32(bar)), "r"(parity), "r"(20000u)
       : "memory");
   return ok != 0;
+}
+__device__ __forceinline__ bool lt_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void lt_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // Waits for a phase, suspended in hardware between tries; false after `budget` cycles.
 __device__ __forceinline__ bool lt_wait(uint64_t* bar, uint32_t parity, long long budget) {
@@ -147,14 +168,15 @@ template <int N> struct LtRing {
   }
 };
 
-// One work item: a tile of features x tokens and a range of the contraction.
+// One work item of a pair: a tile of features x tokens and a range of the contraction; f0 is this
+// CTA's half.
 struct LtTile {
   int f0, t0, nt, split, u0, u1;
-  __device__ __forceinline__ LtTile(const LtParams& p, int i, int BN) {
+  __device__ __forceinline__ LtTile(const LtParams& p, int i, int BN, int rank) {
     const int mt = i % p.mtiles, r = i / p.mtiles;
     nt = r % p.ttiles;
     split = r / p.ttiles;
-    f0 = mt * 128;
+    f0 = mt * 256 + 128 * rank;
     t0 = nt * BN;
     u0 = split * p.per;
     u1 = min(p.units, u0 + p.per);
@@ -162,7 +184,7 @@ struct LtTile {
 };
 
 template <bool FWD, int BN, bool BF16>
-__global__ void __launch_bounds__(LT_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     k_lora_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
               const __grid_constant__ CUtensorMap tmC,
               const __grid_constant__ LtParams p, DeviceStatus* st, long long budget) {
@@ -188,15 +210,16 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int items = p.mtiles * p.ttiles * p.splits;
+  const int rank = (int)tc::cluster_rank(), pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       tc::mbar_init(&full_x[s], 1);
-      tc::mbar_init(&full_a[s], 8);
+      tc::mbar_init(&full_a[s], 16);   // the weight warps of both CTAs
       tc::mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < ND; ++b) {
       tc::mbar_init(&d_full[b], 1);
-      tc::mbar_init(&d_empty[b], 8);
+      tc::mbar_init(&d_empty[b], 16);
     }
     for (int b = 0; b < NC; ++b) {
       tc::mbar_init(&full_c[b], 1);
@@ -209,14 +232,18 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
     tc::prefetch_tmap(&tmU);
     tc::prefetch_tmap(&tmC);
   }
-  if (warp == 17) tc::tmem_alloc(tmem_slot, ND * BN);
+  tc::cluster_sync();   // both CTAs' barriers exist before any remote arrive
+  if (warp == 17) tc::tmem_alloc_pair(tmem_slot, ND * BN);
   tc::fence_before_sync();
-  __syncthreads();
+  tc::cluster_sync();   // TMEM allocated in both before the first MMA
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   // The kernel right before (A X or B dY of this call) has itself waited for everything earlier, so
   // the layer, X and dY may be read now; only its own results (slots, the split U) wait for it.
   pdl_release();
+  // the leader's barriers
+  const uint32_t lead_full_x = tc::map_to_rank(full_x, 0), lead_full_a = tc::map_to_rank(full_a, 0);
+  const uint32_t lead_d_empty = tc::map_to_rank(d_empty, 0);
 
   // registers: 640 threads start with 96 (61440); 128 x 40 + 256 x 64 + 256 x 152 = 60416
   if (warp >= 16) {
@@ -234,13 +261,14 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
           ok = false;
           return;
         }
-        tc::mbar_expect_tx(&full_x[ring.i], Cfg::X_BYTES);
-        tc::tma_load_2d(smem + ring.i * Cfg::STAGE + LT_A_BYTES, map, &full_x[ring.i], x, y);
+        if (rank == 0) tc::mbar_expect_tx(&full_x[ring.i], 2 * Cfg::X_BYTES);   // both CTAs' copies
+        tc::tma_load_2d_pair(smem + ring.i * Cfg::STAGE + LT_A_BYTES, map, lead_full_x + 8u * ring.i, x,
+                             y + rank * (BN / 2));
         ring.next();
         ++issued;
       };
-      for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
-        const LtTile t(p, i, BN);
+      for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
+        const LtTile t(p, i, BN, rank);
         const int k1 = FWD ? 2 * t.u1 : t.u1;
         for (int k = FWD ? 2 * t.u0 : t.u0; k < k1 && ok; ++k) stage(&tmX, k * 64, t.t0);
         if (!p.rank_chunks) continue;
@@ -251,14 +279,14 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
           for (int c = 0; c < 2 * p.rank_chunks && ok; ++c)
             stage(&tmU, (c >> 1) * 32, (c & 1) * p.T_rows + t.t0);
       }
-      // every copy this thread issued has landed before the CTA may exit
-      const int left = min(issued, NS);
+      // every copy has landed before the CTAs may exit: the leader's barriers count both CTAs'
+      const int left = rank == 0 ? min(issued, NS) : 0;
       for (int s = 0; s < left; ++s) {
         const int j = issued - left + s;
         if (!lt_wait(&full_x[j % NS], (uint32_t)(j / NS) & 1u, kDrainCycles))
           raise_error(st, GPTQ_ERR_TIMEOUT, 72);
       }
-    } else if (warp == 17 && lane == 0) {
+    } else if (warp == 17 && lane == 0 && rank == 0) {
       // -------------------------------------------------------------- MMA issuer
       LtRing<NS> ring;
       LtRing<ND> dr;
@@ -296,28 +324,27 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
             const uint64_t da = dk0 + at;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc::mma_tf32(d, da + 2 * kk, db + 2 * kk, p.idesc_tf32, (s | kk) ? 1u : 0u);
+              tc::mma_tf32_pair(d, da + 2 * kk, db + 2 * kk, p.idesc_tf32, (s | kk) ? 1u : 0u);
             ready = false;
           } else {
             const uint64_t da = da0 + at;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              tc::mma_f16(d, da + A_STEP * kk, db + 2 * kk, p.idesc, (s | kk) ? 1u : 0u);
+              tc::mma_f16_pair(d, da + A_STEP * kk, db + 2 * kk, p.idesc, (s | kk) ? 1u : 0u);
               // the next stage's barriers, while MMAs are still queued behind this one
               if (kk == 1)
-                ready = tc::mbar_try_wait(&full_x[next.i], next.phase) &&
-                        tc::mbar_try_wait(&full_a[next.i], next.phase);
+                ready = lt_test(&full_x[next.i], next.phase) && lt_test(&full_a[next.i], next.phase);
             }
           }
           any = true;
-          tc::mma_commit(&empty[ring.i]);
+          tc::mma_commit_pair(&empty[ring.i]);
           ring = next;
         }
-        tc::mma_commit(&d_full[dr.i]);
+        tc::mma_commit_pair(&d_full[dr.i]);
         dr.next();
       };
-      for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
-        const LtTile t(p, i, BN);
+      for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
+        const LtTile t(p, i, BN, rank);
         if (FWD)
           for (int u = t.u0; u < t.u1 && ok; ++u) partial(2, false);
         else
@@ -330,7 +357,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
       }
       // every MMA has completed before TMEM is freed
       if (any) {
-        tc::mma_commit(drain);
+        tc::mma_commit_pair(drain);
         if (!lt_wait(drain, 0, kDrainCycles)) raise_error(st, GPTQ_ERR_TIMEOUT, 75);
       }
     } else if (warp == 18 && lane == 0) {
@@ -338,8 +365,8 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
       LtRing<NC> ring;
       int issued = 0;
       bool ok = true;
-      for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
-        const LtTile t(p, i, BN);
+      for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
+        const LtTile t(p, i, BN, rank);
         for (int u = t.u0; u < t.u1; ++u) {
           if (!lt_wait(&empty_c[ring.i], ring.phase ^ 1u, budget)) {
             raise_error(st, GPTQ_ERR_TIMEOUT, 79);
@@ -347,7 +374,8 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
             ok = false;
             break;
           }
-          const int g = p.group_steps ? (FWD ? u : t.f0 / 128) / p.group_steps : 0;
+          // (the second CTA's columns may lie behind the last group: they are not stored)
+          const int g = p.group_steps ? min((FWD ? u : t.f0 / 128) / p.group_steps, p.used - 1) : 0;
           const int row = FWD ? t.f0 : 64 * u;
           tc::mbar_expect_tx(&full_c[ring.i], Cfg::C_BYTES + Cfg::G_BYTES);
           tc::tma_load_2d(codes + ring.i * Cfg::C_BYTES, &tmC, &full_c[ring.i],
@@ -383,8 +411,8 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
     const int q = (tid >> 3) & 3, brow = (tid & 7) + 8 * (tid >> 5);
     constexpr int PIECES = FWD ? 2 : 1;
     uint32_t pc = 0;   // partial sums so far
-    for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
-      const LtTile t(p, i, BN);
+    for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
+      const LtTile t(p, i, BN, rank);
       for (int k = t.u0; k < t.u1; ++k) {
         LtRing<NS> second = ring;
         second.next();
@@ -466,8 +494,8 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          tc::mbar_arrive(&full_a[ring.i]);
-          if (FWD) tc::mbar_arrive(&full_a[second.i]);
+          lt_arrive_remote(lead_full_a + 8u * ring.i);
+          if (FWD) lt_arrive_remote(lead_full_a + 8u * second.i);
           tc::mbar_arrive(&empty_c[cring.i]);
         }
         ring.next();
@@ -509,7 +537,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&full_a[ring.i]);
+            if (lane == 0) lt_arrive_remote(lead_full_a + 8u * ring.i);
             ring.next();
           }
         }
@@ -523,8 +551,8 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
     LtRing<ND> dr;
     uint32_t pc = 0;
     bool ok = true, waited = false;
-    for (int i = blockIdx.x; i < items && ok && !*abort_flag; i += gridDim.x) {
-      const LtTile t(p, i, BN);
+    for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
+      const LtTile t(p, i, BN, rank);
       const int f = t.f0 + r, tok = t.t0 + half * EBN;
       float acc[EBN];
 #pragma unroll
@@ -563,7 +591,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&d_empty[dr.i]);
+        if (lane == 0) tc::mbar_arrive_remote_relaxed(lead_d_empty + 8u * dr.i);
         dr.next();
         ++pc;
       };
@@ -611,10 +639,10 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
   pdl_wait();
   __syncwarp();
   tc::fence_before_sync();
-  __syncthreads();
+  tc::cluster_sync();   // neither CTA frees TMEM or exits while the other still uses its memory
   if (warp == 17) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, ND * BN);
+    tc::tmem_dealloc_pair(tmem, ND * BN);
   }
 }
 
@@ -907,27 +935,25 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 long long round_up(long long x, long long a) { return (x + a - 1) / a * a; }
 
 // Tile width and splits of the contraction: the smallest waves x (stages of an item x the cycles of
-// a stage + what an item costs besides).  A stage of 256 tokens is bound by the MMAs (about 512
-// cycles), narrower ones by making the weight operand (about 330); an item costs about 2000 cycles,
-// a split's sums their traffic.
+// a stage + what an item costs besides).  A stage costs about the same whatever the tile's width (the
+// MMAs read the weight operand at 32 bytes a cycle, 128 cycles per 16 columns: measured 126 at 128
+// tokens, 128 at 256), so 128 tokens are for batches that fit in them; an item costs about 3000 cycles
+// besides, a split's sums their traffic.
 struct LtPlan { int BN, splits, per; };
 LtPlan lt_plan(int M, int T, int units, int stages_per_unit, int num_sms, size_t part_floats) {
-  LtPlan best{0, 1, units};
+  const int BN = T <= 128 ? 128 : 256;
+  const long long tiles = ((M + 255) / 256) * (long long)((T + BN - 1) / BN), pairs = num_sms / 2;
+  LtPlan best{BN, 1, units};
   double best_cost = 0;
-  for (int BN : {64, 128, 256}) {
-    if (BN < 256 && T > 4 * BN) continue;
-    const long long tiles = ((M + 127) / 128) * (long long)((T + BN - 1) / BN);
-    const double stage = BN == 256 ? 512 : 330;
-    for (int s = 1; s <= 32 && s <= units; ++s) {
-      const int per = (units + s - 1) / s, splits = (units + per - 1) / per;
-      if (splits > 1 && (T > 1024 || (size_t)splits * T * M > part_floats)) break;
-      const long long waves = (tiles * splits + num_sms - 1) / num_sms;
-      const double cost = waves * ((double)per * stages_per_unit * stage + 2000) +
-                          (splits > 1 ? 4000 + splits * (double)T * M * 8 / 3000 : 0);
-      if (!best.BN || cost < best_cost) {
-        best = {BN, splits, per};
-        best_cost = cost;
-      }
+  for (int s = 1; s <= 64 && s <= units; ++s) {
+    const int per = (units + s - 1) / s, splits = (units + per - 1) / per;
+    if (splits > 1 && (T > 1024 || (size_t)splits * T * M > part_floats)) break;
+    const long long waves = (tiles * splits + pairs - 1) / pairs;
+    const double cost = waves * ((double)per * stages_per_unit * 700 + 3000) +
+                        (splits > 1 ? 6000 + splits * (double)T * M * 8 / 3000 : 0);
+    if (s == 1 || cost < best_cost) {
+      best = {BN, splits, per};
+      best_cost = cost;
     }
   }
   return best;
@@ -945,7 +971,7 @@ int launch_tc(Ctx* c, const CUtensorMap& mx, const CUtensorMap& mu,
   GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(k_lora_tc<FWD, BN, BF16>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           LtCfg<FWD, BN>::SMEM));
-  const int grid = std::min(c->num_sms, p.mtiles * p.ttiles * p.splits);
+  const int grid = 2 * std::min(c->num_sms / 2, p.mtiles * p.ttiles * p.splits);
   GPTQ_LAUNCH(c, (k_lora_tc<FWD, BN, BF16>), grid, LT_THREADS, LtCfg<FWD, BN>::SMEM, mx, mu, mc, p, c->status,
               c->timeout_cycles);
   return GPTQ_OK;
@@ -954,7 +980,6 @@ int launch_tc(Ctx* c, const CUtensorMap& mx, const CUtensorMap& mu,
 template <bool FWD>
 int launch_tc_any(Ctx* c, int BN, bool bf, const CUtensorMap& mx, const CUtensorMap& mu,
                   const CUtensorMap& mc, const LtParams& p) {
-  if (BN == 64) return bf ? launch_tc<FWD, 64, true>(c, mx, mu, mc, p) : launch_tc<FWD, 64, false>(c, mx, mu, mc, p);
   if (BN == 128) return bf ? launch_tc<FWD, 128, true>(c, mx, mu, mc, p) : launch_tc<FWD, 128, false>(c, mx, mu, mc, p);
   return bf ? launch_tc<FWD, 256, true>(c, mx, mu, mc, p) : launch_tc<FWD, 256, false>(c, mx, mu, mc, p);
 }
@@ -971,7 +996,7 @@ size_t lora_tc_bytes(const LoraLayer& l) {
   b += (T / 64 + 1) * 65 * 4 + (T / 256 + 1) * 257 * 4;
   b += T * round_up(F, 8) * 2;                                  // a padded X or dY
   b += (size_t)l.m * round_up((l.d + 7) / 8, 4) * 4;            // widened codes
-  b += (size_t)round_up(l.m, 128) * ((l.d + 127) / 128) * 8;    // the grid, column-major
+  b += (size_t)round_up(l.m, 256) * ((l.d + 127) / 128) * 8;    // the grid, column-major
   if (T <= 1024) b += kMaxParts * T * F * 4;
   return b;
 }
@@ -994,7 +1019,7 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   const int wpr = (int)(((long long)l.d * l.bits + 31) / 32), wpr4 = (int)round_up((l.d + 7) / 8, 4);
   const bool widen = out && (l.bits != 4 || wpr != wpr4 || !aligned16(l.packed));
   uint32_t* codes = widen ? cv.take<uint32_t>((size_t)l.m * wpr4) : nullptr;
-  const int m_pad = (int)round_up(l.m, 128);
+  const int m_pad = (int)round_up(l.m, 256);
   const int used = l.group == -1 ? 1 : (l.d + l.group - 1) / l.group;
   float2* grid2 = out ? cv.take<float2>((size_t)used * m_pad) : nullptr;
   float* u_tmp = low ? low : cv.take<float>((size_t)l.T * l.R);
@@ -1069,8 +1094,8 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
 
   CUtensorMap mx, mu, mc;
   if (!lt_map(&mx, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, xs,
-              ld, l.T, plan.BN) ||
-      !lt_map(&mu, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, parts, Rp, 2LL * l.T, plan.BN) ||
+              ld, l.T, plan.BN / 2) ||
+      !lt_map(&mu, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, parts, Rp, 2LL * l.T, plan.BN / 2) ||
       !lt_map(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, widen ? codes : l.packed, wpr4, l.m,
               forward ? 128 : 64, 64))
     GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "lora: tensor map failed");
@@ -1080,7 +1105,8 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   p.group_steps = l.group == -1 ? 0 : l.group / 128;
   p.grid = grid2;
   p.m_pad = m_pad;
-  p.mtiles = (M + 127) / 128;
+  p.used = used;
+  p.mtiles = (M + 255) / 256;
   p.ttiles = ttiles;
   p.splits = plan.splits;
   p.units = units;
@@ -1094,8 +1120,8 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   p.out = out;
   p.out_f32 = out_f32;
   p.part = fused ? nullptr : part;
-  p.idesc = tc::idesc_f32acc(bf ? 1u : 0u, !forward, false, 128, plan.BN);
-  p.idesc_tf32 = tc::idesc_f32acc(2u, false, false, 128, plan.BN);
+  p.idesc = tc::idesc_f32acc(bf ? 1u : 0u, !forward, false, 256, plan.BN);
+  p.idesc_tf32 = tc::idesc_f32acc(2u, false, false, 256, plan.BN);
   const int rc = forward ? launch_tc_any<true>(c, plan.BN, bf, mx, mu, mc, p)
                          : launch_tc_any<false>(c, plan.BN, bf, mx, mu, mc, p);
   if (rc || fused) return rc;
