@@ -30,7 +30,7 @@
 // The barriers' arrivals and waits are the plain ones, also across the pair: each CTA's shared memory is
 // written, fenced for the tensor core's proxy and read by that same SM's tensor core, and what crosses
 // the pair is the order alone.  With cluster-wide release and acquire a stage took 0.87 us for 0.53.
-// The grid is first turned column-major (k_lora_grid), so that the (Δ, z) of a unit's rows are one
+// The grid is first turned column-major (turn_grid), so that the (Δ, z) of a unit's rows are one
 // contiguous copy: read in place they are 128 scattered words per step, and loads of codes and grid
 // into the weight warps' registers, though issued two to four stages ahead, took as long as the
 // whole stage (0.74 us of 256 tokens; without them 0.45).
@@ -238,8 +238,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
   tc::cluster_sync();   // TMEM allocated in both before the first MMA
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  // The kernel right before (A X or B dY of this call) has itself waited for everything earlier, so
-  // the layer, X and dY may be read now; only its own results (slots, the split U) wait for it.
+  // The kernel right before (A X or B dY of this call) has itself waited for everything earlier, so X
+  // and dY may be read now; only its own results (the grid, slots, the split U) wait for it.
   pdl_release();
   // the leader's barriers
   const uint32_t lead_full_x = tc::map_to_rank(full_x, 0), lead_full_a = tc::map_to_rank(full_a, 0);
@@ -365,6 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       LtRing<NC> ring;
       int issued = 0;
       bool ok = true;
+      pdl_wait();   // the grid
       for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
         const LtTile t(p, i, BN, rank);
         for (int u = t.u0; u < t.u1; ++u) {
@@ -647,12 +648,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
 }
 
 // ------------------------------------------------------------------------------------------
-// U = s A X (or G = s B dY): 32 tokens per CTA, the features over its 8 warps and over a cluster's
-// CTAs, on mma.sync straight from global memory (16 bytes a lane; tokens and adapter rows share the
-// tensor instruction's free column order).  Every adapter among the 32 tokens takes a pass over the
-// tile's features; a token keeps its own adapter's.  Writes U [T, R], its two tf32 parts
-// [2, T_rows, Rp] (zero behind R), and the lists of adapters per tile of BN tokens.
-constexpr int LU_THREADS = 256;
+// U = s A X (or G = s B dY): 16 tokens per CTA, the features over its 16 warps (and, for few tokens, over
+// a cluster's CTAs) on mma.sync straight from global memory (16 bytes a lane; tokens and adapter rows
+// share the tensor instruction's free column order).  It is short and bound by the latency of its loads:
+// the warps take two steps of 64 features at once.  Every adapter among the 16 tokens takes a pass over
+// the tile's features; a token keeps its own adapter's.  Writes U [T, R], its two tf32 parts
+// [2, T_rows, Rp] (zero behind R), the lists of adapters per tile of BN tokens, and the layer's grid
+// column-major.
+constexpr int LU_THREADS = 512, LU_WARPS = LU_THREADS / 32, LU_TOKENS = 16;
 
 struct ShrinkParams {
   const void *x, *w;     // [T, F], [n, R, F]
@@ -664,7 +667,44 @@ struct ShrinkParams {
   int32_t* slots;        // or null
   int BN, ttiles;
   int shrink_ctas, cluster;
+  // the grid: grid[g, r] = (Δ[r, g], z[r, g]) for g < used, zero for r in [m, m_pad); limit > 0: |Δ| must
+  // be below it
+  const float* scales;
+  const int32_t* zeros;
+  float2* grid;
+  int m, ng, used, m_pad, grid_ctas;
+  float limit;
 };
+
+// 32 x 32 tile `i` of the grid, by the first 256 threads; every thread of the CTA calls it.
+__device__ __forceinline__ void turn_grid(const ShrinkParams& p, int i, DeviceStatus* st) {
+  __shared__ float2 tile[32][33];
+  const int across = (p.used + 31) / 32;
+  const int g0 = i % across * 32, r0 = i / across * 32, x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  bool bad = false;
+  if (y < 8) {
+#pragma unroll
+    for (int k = y; k < 32; k += 8) {
+      float2 v = make_float2(0.f, 0.f);
+      if (r0 + k < p.m && g0 + x < p.used) {
+        const long long at = (long long)(r0 + k) * p.ng + g0 + x;
+        const int z = p.zeros[at];
+        v = make_float2(p.scales[at], (float)z);
+        bad = bad || z < 0 || z > 15 || (p.limit > 0.f && !(fabsf(v.x) < p.limit));
+        if (z < 0 || z > 15) v.y = 0.f;
+      }
+      tile[k][x] = v;
+    }
+  }
+  if (bad) raise_error(st, GPTQ_ERR_ARG, r0);
+  __syncthreads();
+  if (y < 8) {
+#pragma unroll
+    for (int k = y; k < 32; k += 8)
+      if (g0 + k < p.used && r0 + x < p.m_pad)
+        p.grid[(long long)(g0 + k) * p.m_pad + r0 + x] = tile[x][k];
+  }
+}
 
 __device__ __forceinline__ void write_low_rank(const ShrinkParams& p, int t, int j, float u) {
   if (p.U && j < p.R) p.U[(long long)t * p.R + j] = u;
@@ -681,7 +721,7 @@ __device__ __forceinline__ void write_low_rank(const ShrinkParams& p, int t, int
 __device__ __forceinline__ void list_slots(const ShrinkParams& p, int nt) {
   __shared__ int ids[256];
   __shared__ int counts[8];
-  const int tid = threadIdx.x, t = nt * p.BN + tid;
+  const int tid = threadIdx.x & 255, t = nt * p.BN + tid;   // a second half of the threads does the same
   int a = (tid < p.BN && t < p.T) ? p.adapter[t] : -1;
   if (a < 0 || a >= p.n) a = -1;
   ids[tid] = a;
@@ -701,43 +741,33 @@ __device__ __forceinline__ void list_slots(const ShrinkParams& p, int nt) {
   if (tid == 0) out[0] = total;
 }
 
-// NTL: 8-rank tiles of a pass (16 or 32 ranks, so that the sums leave registers for two CTAs per SM)
+// NTL: 8-rank tiles of a pass (16 or 32 ranks)
 template <bool BF16, int NTL>
-__global__ void __launch_bounds__(LU_THREADS, 2) k_lora_shrink(ShrinkParams p, DeviceStatus* st) {
+__global__ void __launch_bounds__(LU_THREADS, 1) k_lora_shrink(ShrinkParams p, DeviceStatus* st) {
   pdl_wait();
   pdl_release();
-  __shared__ float sums[8][32][16 + 1];   // 16 ranks at a time, per warp
-  __shared__ float total[32 * 8 * NTL];
+  constexpr int COLS = 8 * NTL;
+  __shared__ float sums[LU_WARPS][LU_TOKENS][16 + 1];   // 16 ranks at a time
+  __shared__ float total[LU_TOKENS * COLS];
   const int cl = p.cluster, rank = blockIdx.x % cl;
-  if ((int)blockIdx.x >= p.shrink_ctas) {
-    if ((int)blockIdx.x - p.shrink_ctas < p.ttiles) list_slots(p, blockIdx.x - p.shrink_ctas);
-    return;   // whole clusters of list CTAs: no cluster barrier
+  if ((int)blockIdx.x >= p.shrink_ctas) {   // whole clusters: no cluster barrier
+    const int i = blockIdx.x - p.shrink_ctas;
+    if (i < p.ttiles) list_slots(p, i);
+    else if (i < p.ttiles + p.grid_ctas) turn_grid(p, i - p.ttiles, st);
+    return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const int t0 = (int)(blockIdx.x / cl) * 32;
-  int id = t0 + lane < p.T ? adapter_of(p.adapter, t0 + lane, p.n, st) : -1;
-  // features in steps of 64, spread over the cluster's CTAs and their warps in contiguous runs
-  const int steps = (p.F + 63) / 64, lanes = cl * 8, per = (steps + lanes - 1) / lanes;
-  const int s0 = min(steps, (rank * 8 + warp) * per), s1 = min(steps, s0 + per);
-  const uint16_t* xb = (const uint16_t*)p.x + (long long)t0 * p.F;
-  auto load_x = [&](uint4 (&xv)[2][2], int k) {
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 16 * mt + 8 * h + g;
-        xv[mt][h] = (k < p.F && t0 + row < p.T)
-                        ? *reinterpret_cast<const uint4*>(xb + (long long)row * p.F + k)
-                        : make_uint4(0, 0, 0, 0);
-      }
-  };
-  // the first 64 columns stay in registers: with the cluster's split most warps have no others
-  uint4 x0[2][2][2];
-#pragma unroll
-  for (int hh = 0; hh < 2; ++hh) load_x(x0[hh], s0 < s1 ? s0 * 64 + hh * 32 + t4 * 8 : p.F);
+  const int t0 = (int)(blockIdx.x / cl) * LU_TOKENS;
+  const int id = lane < LU_TOKENS && t0 + lane < p.T ? adapter_of(p.adapter, t0 + lane, p.n, st) : -1;
+  // steps of 64 features, spread over the cluster's CTAs and their warps in contiguous runs
+  const int steps = (p.F + 63) / 64, lanes = cl * LU_WARPS, per = (steps + lanes - 1) / lanes;
+  const int s0 = min(steps, (rank * LU_WARPS + warp) * per), s1 = min(steps, s0 + per);
+  // this lane's token rows g and g + 8 (clamped: a token outside is not kept)
+  const uint16_t* x0 = (const uint16_t*)p.x + (long long)min(t0 + g, p.T - 1) * p.F + 8 * t4;
+  const uint16_t* x1 = (const uint16_t*)p.x + (long long)min(t0 + g + 8, p.T - 1) * p.F + 8 * t4;
   // tokens without an adapter
   if (rank == 0)
-    for (int e = threadIdx.x; e < 32 * p.Rp; e += LU_THREADS) {
+    for (int e = threadIdx.x; e < LU_TOKENS * p.Rp; e += LU_THREADS) {
       const int t = t0 + e / p.Rp;
       if (t < p.T) {
         const int a = p.adapter[t];
@@ -749,74 +779,69 @@ __global__ void __launch_bounds__(LU_THREADS, 2) k_lora_shrink(ShrinkParams p, D
     const int a = __shfl_sync(0xffffffffu, id, __ffs(todo) - 1);
     const uint32_t mine = __ballot_sync(0xffffffffu, id == a);
     todo &= ~mine;
-    for (int j0 = 0; j0 < p.Rp; j0 += 8 * NTL) {
-      const int ntile = min(NTL, (p.R - j0 + 7) / 8);   // <= 0 behind R
-      float acc[2][NTL][4] = {};
-      const uint16_t* wb = (const uint16_t*)p.w + ((long long)a * p.R + j0) * p.F;
-      auto multiply = [&](const uint4 (&xv)[2][2], int k) {
+    const float scale = p.scaling[a];
+    for (int j0 = 0; j0 < p.Rp; j0 += COLS) {
+      float acc[NTL][4] = {};
+      // this lane's rank rows j0 + g + 8 n (clamped: what lies behind R is not kept)
+      const uint16_t* w[NTL];
 #pragma unroll
-        for (int nt = 0; nt < NTL; ++nt) {
-          if (nt >= ntile) break;
-          const int j = 8 * nt + g;
-          const uint4 wv = (k < p.F && j0 + j < p.R)
-                               ? *reinterpret_cast<const uint4*>(wb + (long long)j * p.F + k)
-                               : make_uint4(0, 0, 0, 0);
+      for (int nt = 0; nt < NTL; ++nt)
+        w[nt] = (const uint16_t*)p.w + ((long long)a * p.R + min(j0 + 8 * nt + g, p.R - 1)) * p.F + 8 * t4;
+      for (int s = s0; s < s1; s += 2) {
+        uint4 xv[4][2], wv[4][NTL];
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            mma16816<BF16>(acc[mt][nt], xv[mt][0].x, xv[mt][1].x, xv[mt][0].y, xv[mt][1].y, wv.x,
-                           wv.y);
-            mma16816<BF16>(acc[mt][nt], xv[mt][0].z, xv[mt][1].z, xv[mt][0].w, xv[mt][1].w, wv.z,
-                           wv.w);
-          }
+        for (int h = 0; h < 4; ++h) {   // 32 features each
+          const int k = s * 64 + h * 32;
+          const bool in = k + 8 * t4 < p.F && s + h / 2 < s1;
+          const uint4 none = make_uint4(0, 0, 0, 0);
+          xv[h][0] = in ? *reinterpret_cast<const uint4*>(x0 + k) : none;
+          xv[h][1] = in ? *reinterpret_cast<const uint4*>(x1 + k) : none;
+#pragma unroll
+          for (int nt = 0; nt < NTL; ++nt)
+            wv[h][nt] = in ? *reinterpret_cast<const uint4*>(w[nt] + k) : none;
         }
-      };
-      if (s0 < s1) {
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) multiply(x0[hh], s0 * 64 + hh * 32 + t4 * 8);
-      }
-      for (int s = s0 + 1; s < s1; ++s) {
-        uint4 xv[2][2][2];
+        for (int h = 0; h < 4; ++h)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) load_x(xv[hh], s * 64 + hh * 32 + t4 * 8);
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) multiply(xv[hh], s * 64 + hh * 32 + t4 * 8);
+          for (int nt = 0; nt < NTL; ++nt) {
+            mma16816<BF16>(acc[nt], xv[h][0].x, xv[h][1].x, xv[h][0].y, xv[h][1].y, wv[h][nt].x,
+                           wv[h][nt].y);
+            mma16816<BF16>(acc[nt], xv[h][0].z, xv[h][1].z, xv[h][0].w, xv[h][1].w, wv[h][nt].z,
+                           wv[h][nt].w);
+          }
       }
       // join the warps (fixed order), 16 ranks at a time
-      const int quarters = NTL / 2;
 #pragma unroll
-      for (int quarter = 0; quarter < NTL / 2; ++quarter) {
+      for (int half = 0; half < NTL / 2; ++half) {
         __syncthreads();
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int n2 = 0; n2 < 2; ++n2)
 #pragma unroll
-          for (int n2 = 0; n2 < 2; ++n2)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              sums[warp][16 * mt + 8 * (i >> 1) + g][8 * n2 + 2 * t4 + (i & 1)] =
-                  acc[mt][2 * quarter + n2][i];
+          for (int i = 0; i < 4; ++i)
+            sums[warp][8 * (i >> 1) + g][8 * n2 + 2 * t4 + (i & 1)] = acc[2 * half + n2][i];
         __syncthreads();
-        for (int e = threadIdx.x; e < 32 * 16; e += LU_THREADS) {
+        if (threadIdx.x < LU_TOKENS * 16) {
+          const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
           float v = 0.f;
 #pragma unroll
-          for (int w = 0; w < 8; ++w) v += sums[w][e >> 4][e & 15];
-          total[(e >> 4) * (8 * NTL) + 16 * quarter + (e & 15)] = v;
+          for (int k = 0; k < LU_WARPS; ++k) v += sums[k][row][col];
+          total[row * COLS + 16 * half + col] = v;
         }
       }
       if (cl > 1) tc::cluster_sync();
       else __syncthreads();
       // each CTA of the cluster finishes its share of the tokens
-      const float scale = p.scaling[a];
-      const int rows = 32 / cl, cols = 16 * quarters;
-      for (int e = threadIdx.x; e < rows * cols; e += LU_THREADS) {
-        const int row = rank * rows + e / cols, col = e % cols, j = j0 + col;
+      const int rows = LU_TOKENS / cl;
+      for (int e = threadIdx.x; e < rows * COLS; e += LU_THREADS) {
+        const int row = rank * rows + e / COLS, col = e % COLS, j = j0 + col;
         if (!((mine >> row) & 1u) || j >= p.Rp) continue;
         float v = 0.f;
         for (int c = 0; c < cl; ++c) {
-          float u = total[row * (8 * NTL) + col];
+          float u = total[row * COLS + col];
           if (cl > 1)
             asm volatile("ld.shared::cluster.f32 %0, [%1];"
                          : "=f"(u)
-                         : "r"(tc::map_to_rank(&total[row * (8 * NTL) + col], c))
+                         : "r"(tc::map_to_rank(&total[row * COLS + col], c))
                          : "memory");
           v += u;
         }
@@ -828,46 +853,19 @@ __global__ void __launch_bounds__(LU_THREADS, 2) k_lora_shrink(ShrinkParams p, D
   }
 }
 
-// The two parts and the lists from a U that another kernel has formed.
-__global__ void __launch_bounds__(256) k_lora_parts(ShrinkParams p, const float* __restrict__ U) {
+// The two parts, the lists and the grid for a U that another kernel has formed.
+__global__ void __launch_bounds__(256) k_lora_parts(ShrinkParams p, const float* __restrict__ U, DeviceStatus* st) {
   pdl_wait();
   pdl_release();
   if ((int)blockIdx.x >= p.shrink_ctas) {
-    list_slots(p, blockIdx.x - p.shrink_ctas);
+    const int i = blockIdx.x - p.shrink_ctas;
+    if (i < p.ttiles) list_slots(p, i);
+    else turn_grid(p, i - p.ttiles, st);
     return;
   }
   const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
   const int t = (int)(e / p.Rp), j = (int)(e % p.Rp);
   if (t < p.T) write_low_rank(p, t, j, j < p.R ? U[(long long)t * p.R + j] : 0.f);
-}
-
-// The grid column-major: out[g, r] = (Δ[r, g], z[r, g]), zero for r in [m, m_pad); limit > 0: |Δ| must be
-// below it.  32 x 32 tiles.
-__global__ void __launch_bounds__(256)
-    k_lora_grid(const float* __restrict__ scales, const int32_t* __restrict__ zeros, int m, int ng,
-                int used, int m_pad, float limit, float2* __restrict__ out, DeviceStatus* st) {
-  pdl_wait();
-  pdl_release();
-  __shared__ float2 tile[32][33];
-  const int g0 = blockIdx.y * 32, r0 = blockIdx.x * 32, x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  bool bad = false;
-#pragma unroll
-  for (int i = y; i < 32; i += 8) {
-    float2 v = make_float2(0.f, 0.f);
-    if (r0 + i < m && g0 + x < used) {
-      const long long at = (long long)(r0 + i) * ng + g0 + x;
-      const int z = zeros[at];
-      v = make_float2(scales[at], (float)z);
-      bad = bad || z < 0 || z > 15 || (limit > 0.f && !(fabsf(v.x) < limit));
-      if (z < 0 || z > 15) v.y = 0.f;
-    }
-    tile[i][x] = v;
-  }
-  if (bad) raise_error(st, GPTQ_ERR_ARG, r0);
-  __syncthreads();
-#pragma unroll
-  for (int i = y; i < 32; i += 8)
-    if (g0 + i < used && r0 + x < m_pad) out[(long long)(g0 + i) * m_pad + r0 + x] = tile[x][i];
 }
 
 // Codes of BITS bits -> 4-bit codes in rows of `wpr4` words (a multiple of 4; zeros behind d): 32
@@ -1030,9 +1028,6 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   float* part = cv.take<float>(0);
   const size_t part_floats = cv.ok() ? (c->ws_bytes - cv.off) / sizeof(float) : 0;
 
-  if (out)
-    GPTQ_LAUNCH(c, k_lora_grid, dim3(m_pad / 32, (used + 31) / 32), 256, 0, l.scales, l.zeros, l.m,
-                l.ng, used, m_pad, !forward && !bf ? 17.f : 0.f, grid2, c->status);
   if (widen) {
     // rows in the grid's y: in pieces, should there be more than it holds
     for (int r0 = 0; r0 < l.m; r0 += 65535) {
@@ -1067,18 +1062,23 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   s.slots = slots;
   s.BN = plan.BN;
   s.ttiles = fused && out ? ttiles : 0;
+  s.scales = l.scales;
+  s.zeros = l.zeros;
+  s.grid = grid2;
+  s.m = l.m; s.ng = l.ng; s.used = used; s.m_pad = m_pad;
+  s.grid_ctas = out ? (used + 31) / 32 * (m_pad / 32) : 0;
+  s.limit = !forward && !bf ? 17.f : 0.f;
   // the adapter's rows must be readable in 16-byte pieces; x's are (padded rows are longer than the
   // adapter's, so those go the other way)
   if (K % 8 == 0 && aligned16(w1)) {
     s.U = (low || !fused) ? u_tmp : nullptr;
-    const int tiles = (l.T + 31) / 32;
+    const int tiles = (l.T + LU_TOKENS - 1) / LU_TOKENS;
+    // few tokens: up to a CTA per SM, and two steps of 64 features at least per warp
     s.cluster = 1;
-    // up to about four CTAs per SM, and a step of 64 features at least per warp: a warp's steps follow
-    // one another at the latency of a load
-    while (s.cluster < 8 && tiles * s.cluster <= 2 * c->num_sms && (K + 63) / 64 > 8 * s.cluster)
+    while (s.cluster < 8 && 2 * tiles * s.cluster <= c->num_sms && (K + 63) / 64 > 2 * LU_WARPS * s.cluster)
       s.cluster *= 2;
     s.shrink_ctas = tiles * s.cluster;
-    const int grid = s.shrink_ctas + (int)round_up(s.ttiles, s.cluster);
+    const int grid = s.shrink_ctas + (int)round_up(s.ttiles + s.grid_ctas, s.cluster);
     auto kernel = l.R <= 16 ? (bf ? k_lora_shrink<true, 2> : k_lora_shrink<false, 2>)
                             : (bf ? k_lora_shrink<true, 4> : k_lora_shrink<false, 4>);
     GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, s.cluster, kernel, dim3(grid), dim3(LU_THREADS), 0, s,
@@ -1087,8 +1087,8 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
     const int rc = lora_shrink_any(c, l, x, K, w1, u_tmp);
     if (rc) return rc;
     s.shrink_ctas = s.parts ? (int)(((long long)l.T * Rp + 255) / 256) : 0;
-    if (s.shrink_ctas + s.ttiles)
-      GPTQ_LAUNCH(c, k_lora_parts, s.shrink_ctas + s.ttiles, 256, 0, s, (const float*)u_tmp);
+    const int ctas = s.shrink_ctas + s.ttiles + s.grid_ctas;
+    if (ctas) GPTQ_LAUNCH(c, k_lora_parts, ctas, 256, 0, s, (const float*)u_tmp, c->status);
   }
   if (!out) return GPTQ_OK;
 
