@@ -303,9 +303,9 @@ def gptq_lora_workspace_bytes(T: int, m: int, d: int, bits: int, n_adapters: int
 
 
 def _shaped(ctx: Context, t: torch.Tensor, shape, dtypes, name):
-    """A contiguous tensor of this shape, one of these dtypes, on the context's device."""
-    if not t.is_cuda or not t.is_contiguous() or t.shape != shape or t.dtype not in dtypes or \
-            t.device != ctx.device:
+    """The pointer of a contiguous tensor of this shape, one of these dtypes, on the context's device."""
+    if t.get_device() != ctx.device.index or t.dtype not in dtypes or t.shape != shape or \
+            not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of "
                          f"{' or '.join(map(str, dtypes))} on {ctx.device}, got {tuple(t.shape)} "
                          f"{t.dtype} on {t.device}")
@@ -371,7 +371,7 @@ def gptq_lora_backward(ctx: Context, dY, X, packed, d: int, bits: int, group: in
 
 def _rows(ctx: Context, t, shape, dtypes, name):
     """As _shaped, but the rows may lie further apart than they are long; also that distance."""
-    if not t.is_cuda or t.shape != shape or t.dtype not in dtypes or t.device != ctx.device or \
+    if t.get_device() != ctx.device.index or t.shape != shape or t.dtype not in dtypes or \
             (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
         raise ValueError(f"{name} must be a {tuple(shape)} tensor with contiguous rows of "
                          f"{' or '.join(map(str, dtypes))} on {ctx.device}, got {tuple(t.shape)} "

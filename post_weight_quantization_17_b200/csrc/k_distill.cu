@@ -182,8 +182,9 @@ struct DsList {
   float mass, cm, c;   // M, g w tau M, g w tau
 };
 
-// Reads the list (indices, the student's scaled logits there, the teacher's), and turns the
-// teacher's logits into probabilities.  Returns L; every thread of the CTA.
+// Reads the list (indices, the student's scaled logits there, the teacher's).  Without the teacher's
+// log-sum-exp the teacher's logits are taken relative to their largest, so that log p_k is a difference
+// of small numbers.  Returns L; every thread of the CTA.
 template <class T>
 __device__ __forceinline__ float ds_read_list(const DistillArgs& p, int t, const T* z, float it,
                                               DsList& l, float* red, DeviceStatus* st) {
@@ -208,8 +209,11 @@ __device__ __forceinline__ float ds_read_list(const DistillArgs& p, int t, const
     most = ds_block(most, true, red);
     float s = 0.f;
     for (int k = threadIdx.x; k < p.K; k += DS_THREADS)
-      s += l.pk[k] == -INFINITY ? 0.f : ds_exp2((l.pk[k] - most) * DS_LOG2E);
-    L = most + logf(ds_block(s, false, red));
+      if (l.pk[k] != -INFINITY) {
+        l.pk[k] -= most;
+        s += expf(l.pk[k]);
+      }
+    L = logf(ds_block(s, false, red));
   }
   return L;
 }
@@ -221,7 +225,7 @@ __device__ __forceinline__ void ds_finish_list(const DistillArgs& p, float L, fl
   float kl = 0.f, mass = 0.f;
   for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
     const float lp = l.pk[k] - L;
-    const float q = l.pk[k] == -INFINITY ? 0.f : ds_exp2(lp * DS_LOG2E);
+    const float q = l.pk[k] == -INFINITY ? 0.f : expf(lp);
     l.pk[k] = q;
     mass += q;
     if (q != 0.f) kl += q * (lp - (l.zk[k] - lse));

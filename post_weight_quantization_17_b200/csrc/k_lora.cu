@@ -242,9 +242,10 @@ static bool lora_tensor_format(const LoraLayer& l) {
 
 size_t lora_workspace_bytes(const LoraLayer& l) {
   size_t floats = (size_t)l.T * l.R;
-  if (l.T <= kLoraSmallTokens) floats = std::max(floats, lora_small_floats(l));
+  const bool tensor = l.dtype != GPTQ_F32 && l.bits <= 4;
+  if (tensor && l.T <= kLoraSmallTokens) floats = std::max(floats, lora_small_floats(l));
   size_t b = 256 * 2 + floats * sizeof(float);
-  if (l.dtype != GPTQ_F32 && l.bits <= 4)   // the backward pass keeps G in front
+  if (tensor)   // the backward pass keeps G in front
     b = std::max(b, 256 + (size_t)l.T * l.R * sizeof(float) + lora_tc_bytes(l));
   return kStatusBytes + b;
 }

@@ -5,8 +5,9 @@
 // mma.sync tf32 (16 x 8 x 8): x is exact in tf32, u goes in as two tf32 parts (22 bits), so the sums
 // are fp32 sums.  x is read straight into the tensor operand: a lane's 16 bytes are 8 features of
 // one token, and tile i of the warp's eight takes feature 8 n + i as its column n, so no
-// shared-memory pass is needed.  A CTA covers 128 features and 32 ranks; its four token warps, and
-// the CTAs of a cluster, take the 8-token groups in turn (adapters' runs spread evenly) and are
+// shared-memory pass is needed.  A CTA covers 128 features and 16 ranks (32 at once need twice the
+// registers: 169 us with one CTA per SM, 215 with two and spills, where two passes take 134: 4096 tokens,
+// 4 adapters of rank 32 on 4096 x 11008); its four token warps, and the CTAs of a cluster, take the 8-token groups in turn (adapters' runs spread evenly) and are
 // joined in a fixed order in (distributed) shared memory.  A cluster takes several adapters one after
 // the other (one in turn would leave most CTAs of a large adapter table with nothing to do); those
 // without a token are cleared.  Groups without a token of the adapter are skipped; in mixed groups the
@@ -20,15 +21,17 @@ namespace gptq {
 
 constexpr int LO_THREADS = 256;
 constexpr int LO_FEATS = 128, LO_PAD = 68;
-// Shared memory: the warps' sums [8][16 RT][64 + 4], the CTA's [16 RT][128], the adapters' bits.  Up to
-// rank 16 a tile of 16 ranks takes half of it, and more CTAs fit on an SM.
-constexpr int lo_smem(int rank_tiles) { return (8 * 16 * rank_tiles * LO_PAD + 16 * rank_tiles * LO_FEATS) * 4; }
+constexpr int LO_TOKENS = 8192;   // of a launch: their adapters (16 bits each) are kept in shared memory
+constexpr int LO_RANKS = 16;
+// the warps' sums [8][16][64 + 4] and the CTA's [16][128]; the adapters' bits and the tokens' adapters
+// follow
+constexpr int LO_SMEM = (8 * LO_RANKS * LO_PAD + LO_RANKS * LO_FEATS) * 4;
 
 struct OuterProblem {
   const float* u;          // [T, R]
   const void* x;           // [T, F]
   float* out;              // [n, R, F]
-  int F, wide;             // wide: x may be read in 16-byte pieces
+  int F, wide, u_wide;     // x may be read in 16-byte pieces, u in 8-byte ones
 };
 struct OuterParams {
   OuterProblem two[2];
@@ -48,15 +51,14 @@ __device__ __forceinline__ void mma_tf32_1688(float (&d)[4], const uint32_t (&a)
 }
 
 // Two groups of 8 tokens of a warp: a lane's 8 features of four of the tokens, and their ranks.
-template <int RT> struct OuterGroup {
+struct OuterGroup {
   uint32_t members;
   uint4 x[2][2];
-  float u[2][2][2 * RT];
+  float u[2][2][2];
 };
 
-template <int RT, bool BF16>
+template <bool BF16>
 __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_constant__ OuterParams p) {
-  constexpr int LO_RANKS = 16 * RT;
   pdl_wait();
   pdl_release();
   extern __shared__ __align__(16) float lo_smem_[];
@@ -70,10 +72,12 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
   const uint16_t* px = (const uint16_t*)(second ? p.two[1].x : p.two[0].x);
   float* const out = second ? p.two[1].out : p.two[0].out;
   const int F = second ? p.two[1].F : p.two[0].F, wide = second ? p.two[1].wide : p.two[0].wide;
+  const int u_wide = second ? p.two[1].u_wide : p.two[0].u_wide;
   const int fb = ((int)blockIdx.x - (second ? p.first_ctas : 0)) / cl * LO_FEATS;
   const int f0 = fb + wf * 64, j0 = blockIdx.y * LO_RANKS, f = f0 + 8 * g;
-  // which adapters have tokens
+  // the tokens' adapters (0xFFFF: none), and which adapters have tokens
   uint32_t* present = reinterpret_cast<uint32_t*>(total + LO_RANKS * LO_FEATS);
+  uint16_t* id_of = reinterpret_cast<uint16_t*>(present + (p.n + 31) / 32);
   for (int i = threadIdx.x; i < (p.n + 31) / 32; i += LO_THREADS) present[i] = 0;
   __syncthreads();
   for (int t = threadIdx.x; t < p.T; t += 8 * LO_THREADS) {
@@ -81,9 +85,12 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
 #pragma unroll
     for (int i = 0; i < 8; ++i) id[i] = t + i * LO_THREADS < p.T ? p.adapter[t + i * LO_THREADS] : -1;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (id[i] >= 0 && id[i] < p.n && !((present[id[i] >> 5] >> (id[i] & 31)) & 1u))
+    for (int i = 0; i < 8; ++i) {
+      const bool one = id[i] >= 0 && id[i] < p.n;
+      if (t + i * LO_THREADS < p.T) id_of[t + i * LO_THREADS] = one ? (uint16_t)id[i] : (uint16_t)0xFFFF;
+      if (one && !((present[id[i] >> 5] >> (id[i] & 31)) & 1u))
         atomicOr(&present[id[i] >> 5], 1u << (id[i] & 31));
+    }
   }
   __syncthreads();
   for (int a = blockIdx.z; a < p.n; a += gridDim.z) {
@@ -95,23 +102,28 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
       }
     continue;
   }
-  float acc[RT][8][4] = {};
-  // this warp's groups: i0, i0 + stride, ...; two at a time, the next two on their way
+  float acc[8][4] = {};
+  // this warp's groups: rank * 4 + wt, and every `stride`-th from there, taken in pairs
   const int groups = (p.T + 7) / 8, stride = 4 * cl;
-  auto ids = [&](int i) {
-    const int t = (i + ((lane >> 3) & 1) * stride) * 8 + (lane & 7);
-    return lane < 16 && i < groups && t < p.T ? p.adapter[t] : -1;
+  // the next pair at or behind i that has a token of the adapter (its members, and i), from shared memory
+  auto find = [&](int& i) -> uint32_t {
+    for (; i < groups; i += 2 * stride) {
+      const int t = (i + ((lane >> 3) & 1) * stride) * 8 + (lane & 7);
+      const uint32_t m = __ballot_sync(0xffffffffu, lane < 16 && t < p.T && id_of[t] == a);
+      if (m) return m;
+    }
+    return 0u;
   };
-  auto fetch = [&](OuterGroup<RT>& o, int i, int id) {
-    o.members = __ballot_sync(0xffffffffu, id == a);
-    if (!o.members) return;
+  auto fetch = [&](OuterGroup& o, int i, uint32_t members) {
+    o.members = members;
+    if (!members) return;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r8 = t4 + 4 * h;
         const long long t = (long long)(i + k * stride) * 8 + r8;
-        const bool in = (o.members >> (8 * k + r8)) & 1u;
+        const bool in = (members >> (8 * k + r8)) & 1u;
         o.x[k][h] = make_uint4(0, 0, 0, 0);
         if (in && wide) {
           if (f < F) o.x[k][h] = *reinterpret_cast<const uint4*>(px + t * F + f);
@@ -123,67 +135,70 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
             if (f + e < F) w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
           o.x[k][h] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-#pragma unroll
-        for (int r = 0; r < 2 * RT; ++r) {   // ranks g, g + 8, ...
-          const int j = j0 + g + 8 * r;
-          o.u[k][h][r] = (in && j < p.R) ? pu[t * p.R + j] : 0.f;
+        // ranks 2 g, 2 g + 1: the operand's row order is free, so a lane's ranks are adjacent
+        const int j = j0 + 2 * g;
+        o.u[k][h][0] = o.u[k][h][1] = 0.f;
+        if (in && u_wide && j < p.R) {
+          const float2 v = *reinterpret_cast<const float2*>(pu + t * p.R + j);
+          o.u[k][h][0] = v.x;
+          o.u[k][h][1] = v.y;
+        } else if (in) {
+          if (j < p.R) o.u[k][h][0] = pu[t * p.R + j];
+          if (j + 1 < p.R) o.u[k][h][1] = pu[t * p.R + j + 1];
         }
       }
     }
   };
-  auto multiply = [&](const OuterGroup<RT>& o) {
+  auto multiply = [&](const OuterGroup& o) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!((o.members >> (8 * k)) & 0xffu)) continue;
       const uint32_t x0[4] = {o.x[k][0].x, o.x[k][0].y, o.x[k][0].z, o.x[k][0].w};
       const uint32_t x1[4] = {o.x[k][1].x, o.x[k][1].y, o.x[k][1].z, o.x[k][1].w};
+      uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        uint32_t hi[4], lo[4];
+      for (int e = 0; e < 4; ++e) {   // rows g and g + 8 (ranks 2 g, 2 g + 1) of tokens t4 and t4 + 4
+        const float v = o.u[k][e >> 1][e & 1];
+        const bool finite = fabsf(v) <= 3.0e38f;   // the split is for finite values
+        const float h = finite ? tc::tf32_rna(v) : v;
+        hi[e] = __float_as_uint(h);
+        lo[e] = finite ? __float_as_uint(tc::tf32_rna(v - h)) : 0u;
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {   // (rank g, token t4), (g + 8, t4), (g, t4 + 4), (g + 8, t4 + 4)
-          const float v = o.u[k][e >> 1][2 * m + (e & 1)];
-          const bool finite = fabsf(v) <= 3.0e38f;   // the split is for finite values
-          const float h = finite ? tc::tf32_rna(v) : v;
-          hi[e] = __float_as_uint(h);
-          lo[e] = finite ? __float_as_uint(tc::tf32_rna(v - h)) : 0u;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 b0 = pair_f32<BF16>(x0[e]), b1 = pair_f32<BF16>(x1[e]);
-          mma_tf32_1688(acc[m][2 * e], hi, __float_as_uint(b0.x), __float_as_uint(b1.x));
-          mma_tf32_1688(acc[m][2 * e + 1], hi, __float_as_uint(b0.y), __float_as_uint(b1.y));
-          mma_tf32_1688(acc[m][2 * e], lo, __float_as_uint(b0.x), __float_as_uint(b1.x));
-          mma_tf32_1688(acc[m][2 * e + 1], lo, __float_as_uint(b0.y), __float_as_uint(b1.y));
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float2 b0 = pair_f32<BF16>(x0[e]), b1 = pair_f32<BF16>(x1[e]);
+        mma_tf32_1688(acc[2 * e], hi, __float_as_uint(b0.x), __float_as_uint(b1.x));
+        mma_tf32_1688(acc[2 * e + 1], hi, __float_as_uint(b0.y), __float_as_uint(b1.y));
+        mma_tf32_1688(acc[2 * e], lo, __float_as_uint(b0.x), __float_as_uint(b1.x));
+        mma_tf32_1688(acc[2 * e + 1], lo, __float_as_uint(b0.y), __float_as_uint(b1.y));
       }
     }
   };
   {
-    const int i0 = rank * 4 + wt;
-    OuterGroup<RT> one, other;
-    int id_next = ids(i0 + 2 * stride);
-    fetch(one, i0, ids(i0));
-    for (int i = i0; i < groups; i += 4 * stride) {
-      const int id_after = ids(i + 4 * stride);
-      fetch(other, i + 2 * stride, id_next);
+    int i = rank * 4 + wt;
+    OuterGroup one, other;
+    uint32_t m = find(i);
+    fetch(one, i, m);
+    while (one.members) {
+      i += 2 * stride;
+      m = find(i);
+      fetch(other, i, m);
       multiply(one);
-      id_next = ids(i + 6 * stride);
-      fetch(one, i + 4 * stride, id_after);
+      if (!m) break;
+      i += 2 * stride;
+      m = find(i);
+      fetch(one, i, m);
       multiply(other);
     }
   }
   // tile i's column n is feature 8 n + i: a lane holds features 16 t4 + (0..7) and + 8
   float* mine = sums + warp * LO_RANKS * LO_PAD;
 #pragma unroll
-  for (int m = 0; m < RT; ++m)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float4* dst = reinterpret_cast<float4*>(mine + (16 * m + 8 * (c >> 1) + g) * LO_PAD + 16 * t4 +
-                                              8 * (c & 1));
-      dst[0] = make_float4(acc[m][0][c], acc[m][1][c], acc[m][2][c], acc[m][3][c]);
-      dst[1] = make_float4(acc[m][4][c], acc[m][5][c], acc[m][6][c], acc[m][7][c]);
-    }
+  for (int c = 0; c < 4; ++c) {
+    float4* dst = reinterpret_cast<float4*>(mine + (2 * g + (c >> 1)) * LO_PAD + 16 * t4 + 8 * (c & 1));
+    dst[0] = make_float4(acc[0][c], acc[1][c], acc[2][c], acc[3][c]);
+    dst[1] = make_float4(acc[4][c], acc[5][c], acc[6][c], acc[7][c]);
+  }
   __syncthreads();
   for (int e = threadIdx.x; e < LO_RANKS * LO_FEATS; e += LO_THREADS) {
     const int j = e / LO_FEATS, ff = e % LO_FEATS;
@@ -222,34 +237,38 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
 }
 
 // dA from (G, X) and dB from (U, dY) in one launch (each alone is too short to fill the GPU); either may
-// be left out (null).
+// be left out (null).  Batches of more than LO_TOKENS tokens take several, which add up.
 int lora_outers(Ctx* c, const LoraLayer& l, const float* G, const void* X, float* dA, const float* U,
                 const void* dY, float* dB, int accumulate) {
-  OuterParams p{};
-  p.T = l.T; p.R = l.R; p.n = l.n;
-  p.adapter = l.adapter;
-  p.accumulate = accumulate;
+  const int ranks = (l.R + LO_RANKS - 1) / LO_RANKS;
   const int tiles = (dA ? (l.d + LO_FEATS - 1) / LO_FEATS : 0) + (dB ? (l.m + LO_FEATS - 1) / LO_FEATS : 0);
-  const int rt = l.R <= 16 ? 1 : 2, ranks = (l.R + 16 * rt - 1) / (16 * rt);
-  // tokens over a cluster until there is a CTA for every SM: joining a cluster costs an adapter about
-  // 4 us (of 4096 tokens, 4 adapters of rank 32 on 4096 x 11008: 272 us on clusters of 8, see below)
-  p.cluster = 1;
-  while (p.cluster < 8 && l.T > 32 * p.cluster && tiles * ranks * p.cluster < c->num_sms) p.cluster *= 2;
-  auto problem = [](const float* u, const void* x, float* out, int F) {
-    return OuterProblem{u, x, out, F, F % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0};
-  };
-  const int ca = dA ? (l.d + LO_FEATS - 1) / LO_FEATS * p.cluster : 0;
-  const int cb = dB ? (l.m + LO_FEATS - 1) / LO_FEATS * p.cluster : 0;
-  p.two[0] = problem(G, X, dA, l.d);
-  p.two[1] = problem(U, dY, dB, l.m);
-  p.first_ctas = ca;
-  const dim3 grid(ca + cb, ranks, std::max(1, std::min(l.n, 4 * c->num_sms / ((ca + cb) * ranks))));
-  const int smem = lo_smem(rt) + (l.n + 31) / 32 * 4;
-  const bool bf = l.dtype == GPTQ_BF16;
-  auto kernel = rt == 1 ? (bf ? k_lora_outer<1, true> : k_lora_outer<1, false>)
-                        : (bf ? k_lora_outer<2, true> : k_lora_outer<2, false>);
-  GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, p.cluster, kernel, grid, dim3(LO_THREADS), smem, p));
+  auto kernel = l.dtype == GPTQ_BF16 ? k_lora_outer<true> : k_lora_outer<false>;
+  for (int t0 = 0; t0 < l.T; t0 += LO_TOKENS) {
+    OuterParams p{};
+    p.T = std::min(LO_TOKENS, l.T - t0);
+    p.R = l.R; p.n = l.n;
+    p.adapter = l.adapter + t0;
+    p.accumulate = accumulate || t0 > 0;
+    // tokens over a cluster until there is a CTA for every SM: joining a cluster costs each adapter some
+    // microseconds (clusters of 8 took 272 us where clusters of 2 took 217, at the size above)
+    p.cluster = 1;
+    while (p.cluster < 8 && p.T > 32 * p.cluster && tiles * ranks * p.cluster < c->num_sms) p.cluster *= 2;
+    auto problem = [&](const float* u, const void* x, float* out, int F) {
+      const float* ut = u ? u + (size_t)t0 * l.R : nullptr;
+      const uint16_t* xt = x ? (const uint16_t*)x + (size_t)t0 * F : nullptr;
+      return OuterProblem{ut, xt, out, F, F % 8 == 0 && (reinterpret_cast<uintptr_t>(xt) & 15) == 0,
+                          l.R % 2 == 0 && (reinterpret_cast<uintptr_t>(ut) & 7) == 0};
+    };
+    const int ca = dA ? (l.d + LO_FEATS - 1) / LO_FEATS * p.cluster : 0;
+    const int cb = dB ? (l.m + LO_FEATS - 1) / LO_FEATS * p.cluster : 0;
+    p.two[0] = problem(G, X, dA, l.d);
+    p.two[1] = problem(U, dY, dB, l.m);
+    p.first_ctas = ca;
+    const dim3 grid(ca + cb, ranks, std::max(1, std::min(l.n, 4 * c->num_sms / ((ca + cb) * ranks))));
+    const int smem = LO_SMEM + (l.n + 31) / 32 * 4 + (p.T + 1) / 2 * 4;
+    GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, p.cluster, kernel, grid, dim3(LO_THREADS), smem, p));
+  }
   return GPTQ_OK;
 }
 

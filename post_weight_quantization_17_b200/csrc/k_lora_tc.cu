@@ -36,7 +36,7 @@
 // whole stage (0.74 us of 256 tokens; without them 0.45).
 // Few tokens: the contraction is split over CTAs and k_lora_join adds the splits and the adapter.
 #include <algorithm>
-#include <cstring>
+#include <type_traits>
 
 #include "lora_util.cuh"
 #include "tc_util.cuh"
@@ -648,14 +648,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
 }
 
 // ------------------------------------------------------------------------------------------
-// U = s A X (or G = s B dY): 16 tokens per CTA, the features over its 16 warps (and, for few tokens, over
+// U = s A X (or G = s B dY): 16 or 32 tokens per CTA, the features over its 16 warps (and, for few tokens, over
 // a cluster's CTAs) on mma.sync straight from global memory (16 bytes a lane; tokens and adapter rows
 // share the tensor instruction's free column order).  It is short and bound by the latency of its loads:
-// the warps take two steps of 64 features at once.  Every adapter among the 16 tokens takes a pass over
+// the warps take two steps of 64 features at once.  Every adapter among the tokens takes a pass over
 // the tile's features; a token keeps its own adapter's.  Writes U [T, R], its two tf32 parts
 // [2, T_rows, Rp] (zero behind R), the lists of adapters per tile of BN tokens, and the layer's grid
 // column-major.
-constexpr int LU_THREADS = 512, LU_WARPS = LU_THREADS / 32, LU_TOKENS = 16;
+constexpr int LU_THREADS = 512, LU_WARPS = LU_THREADS / 32;
 
 struct ShrinkParams {
   const void *x, *w;     // [T, F], [n, R, F]
@@ -676,11 +676,13 @@ struct ShrinkParams {
   float limit;
 };
 
-// 32 x 32 tile `i` of the grid, by the first 256 threads; every thread of the CTA calls it.
+// 32 x 32 tiles i, i + grid_ctas, ... of the grid; every thread of the CTA (at least 256).
 __device__ __forceinline__ void turn_grid(const ShrinkParams& p, int i, DeviceStatus* st) {
   __shared__ float2 tile[32][33];
-  const int across = (p.used + 31) / 32;
-  const int g0 = i % across * 32, r0 = i / across * 32, x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int across = (p.used + 31) / 32, tiles = across * (p.m_pad / 32);
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  for (; i < tiles; i += p.grid_ctas) {
+  const int g0 = i % across * 32, r0 = i / across * 32;
   bool bad = false;
   if (y < 8) {
 #pragma unroll
@@ -703,6 +705,8 @@ __device__ __forceinline__ void turn_grid(const ShrinkParams& p, int i, DeviceSt
     for (int k = y; k < 32; k += 8)
       if (g0 + k < p.used && r0 + x < p.m_pad)
         p.grid[(long long)(g0 + k) * p.m_pad + r0 + x] = tile[x][k];
+  }
+  __syncthreads();
   }
 }
 
@@ -741,13 +745,14 @@ __device__ __forceinline__ void list_slots(const ShrinkParams& p, int nt) {
   if (tid == 0) out[0] = total;
 }
 
-// NTL: 8-rank tiles of a pass (16 or 32 ranks)
-template <bool BF16, int NTL>
+// NTL: 8-rank tiles of a pass (16 or 32 ranks); MT: 16-token tiles of a CTA (two halve the reads of A
+// where there are tokens enough for every SM)
+template <bool BF16, int NTL, int MT>
 __global__ void __launch_bounds__(LU_THREADS, 1) k_lora_shrink(ShrinkParams p, DeviceStatus* st) {
   pdl_wait();
   pdl_release();
-  constexpr int COLS = 8 * NTL;
-  __shared__ float sums[LU_WARPS][LU_TOKENS][16 + 1];   // 16 ranks at a time
+  constexpr int COLS = 8 * NTL, LU_TOKENS = 16 * MT;
+  __shared__ float sums[LU_WARPS][16][16 + 1];   // 16 tokens x 16 ranks at a time
   __shared__ float total[LU_TOKENS * COLS];
   const int cl = p.cluster, rank = blockIdx.x % cl;
   if ((int)blockIdx.x >= p.shrink_ctas) {   // whole clusters: no cluster barrier
@@ -762,9 +767,11 @@ __global__ void __launch_bounds__(LU_THREADS, 1) k_lora_shrink(ShrinkParams p, D
   // steps of 64 features, spread over the cluster's CTAs and their warps in contiguous runs
   const int steps = (p.F + 63) / 64, lanes = cl * LU_WARPS, per = (steps + lanes - 1) / lanes;
   const int s0 = min(steps, (rank * LU_WARPS + warp) * per), s1 = min(steps, s0 + per);
-  // this lane's token rows g and g + 8 (clamped: a token outside is not kept)
-  const uint16_t* x0 = (const uint16_t*)p.x + (long long)min(t0 + g, p.T - 1) * p.F + 8 * t4;
-  const uint16_t* x1 = (const uint16_t*)p.x + (long long)min(t0 + g + 8, p.T - 1) * p.F + 8 * t4;
+  // this lane's token rows g + 8 i (clamped: a token outside is not kept)
+  const uint16_t* x[2 * MT];
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i)
+    x[i] = (const uint16_t*)p.x + (long long)min(t0 + g + 8 * i, p.T - 1) * p.F + 8 * t4;
   // tokens without an adapter
   if (rank == 0)
     for (int e = threadIdx.x; e < LU_TOKENS * p.Rp; e += LU_THREADS) {
@@ -781,53 +788,68 @@ __global__ void __launch_bounds__(LU_THREADS, 1) k_lora_shrink(ShrinkParams p, D
     todo &= ~mine;
     const float scale = p.scaling[a];
     for (int j0 = 0; j0 < p.Rp; j0 += COLS) {
-      float acc[NTL][4] = {};
+      float acc[MT][NTL][4] = {};
       // this lane's rank rows j0 + g + 8 n (clamped: what lies behind R is not kept)
       const uint16_t* w[NTL];
 #pragma unroll
       for (int nt = 0; nt < NTL; ++nt)
         w[nt] = (const uint16_t*)p.w + ((long long)a * p.R + min(j0 + 8 * nt + g, p.R - 1)) * p.F + 8 * t4;
-      for (int s = s0; s < s1; s += 2) {
-        uint4 xv[4][2], wv[4][NTL];
+      constexpr int H = MT == 1 ? 4 : 2;   // pieces of 32 features loaded at once
+      for (int k0 = s0 * 64; k0 < s1 * 64; k0 += 32 * H) {
+        uint4 xv[H][2 * MT], wv[H][NTL];
+        if (k0 + 32 * H <= min(s1 * 64, p.F)) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {   // 32 features each
-          const int k = s * 64 + h * 32;
-          const bool in = k + 8 * t4 < p.F && s + h / 2 < s1;
-          const uint4 none = make_uint4(0, 0, 0, 0);
-          xv[h][0] = in ? *reinterpret_cast<const uint4*>(x0 + k) : none;
-          xv[h][1] = in ? *reinterpret_cast<const uint4*>(x1 + k) : none;
+          for (int h = 0; h < H; ++h) {
 #pragma unroll
-          for (int nt = 0; nt < NTL; ++nt)
-            wv[h][nt] = in ? *reinterpret_cast<const uint4*>(w[nt] + k) : none;
-        }
+            for (int i = 0; i < 2 * MT; ++i) xv[h][i] = *reinterpret_cast<const uint4*>(x[i] + k0 + 32 * h);
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-#pragma unroll
-          for (int nt = 0; nt < NTL; ++nt) {
-            mma16816<BF16>(acc[nt], xv[h][0].x, xv[h][1].x, xv[h][0].y, xv[h][1].y, wv[h][nt].x,
-                           wv[h][nt].y);
-            mma16816<BF16>(acc[nt], xv[h][0].z, xv[h][1].z, xv[h][0].w, xv[h][1].w, wv[h][nt].z,
-                           wv[h][nt].w);
+            for (int nt = 0; nt < NTL; ++nt)
+              wv[h][nt] = *reinterpret_cast<const uint4*>(w[nt] + k0 + 32 * h);
           }
-      }
-      // join the warps (fixed order), 16 ranks at a time
+        } else {
 #pragma unroll
-      for (int half = 0; half < NTL / 2; ++half) {
-        __syncthreads();
+          for (int h = 0; h < H; ++h) {
+            const int k = k0 + 32 * h;
+            const bool in = k < s1 * 64 && k + 8 * t4 < p.F;
+            const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int n2 = 0; n2 < 2; ++n2)
+            for (int i = 0; i < 2 * MT; ++i) xv[h][i] = in ? *reinterpret_cast<const uint4*>(x[i] + k) : none;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sums[warp][8 * (i >> 1) + g][8 * n2 + 2 * t4 + (i & 1)] = acc[2 * half + n2][i];
-        __syncthreads();
-        if (threadIdx.x < LU_TOKENS * 16) {
-          const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
-          float v = 0.f;
-#pragma unroll
-          for (int k = 0; k < LU_WARPS; ++k) v += sums[k][row][col];
-          total[row * COLS + 16 * half + col] = v;
+            for (int nt = 0; nt < NTL; ++nt)
+              wv[h][nt] = in ? *reinterpret_cast<const uint4*>(w[nt] + k) : none;
+          }
         }
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NTL; ++nt) {
+              const uint4 &u = xv[h][2 * mt], &v = xv[h][2 * mt + 1], &b = wv[h][nt];
+              mma16816<BF16>(acc[mt][nt], u.x, v.x, u.y, v.y, b.x, b.y);
+              mma16816<BF16>(acc[mt][nt], u.z, v.z, u.w, v.w, b.z, b.w);
+            }
       }
+      // join the warps (fixed order), 16 tokens and 16 ranks at a time
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < NTL / 2; ++half) {
+          __syncthreads();
+#pragma unroll
+          for (int n2 = 0; n2 < 2; ++n2)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sums[warp][8 * (i >> 1) + g][8 * n2 + 2 * t4 + (i & 1)] = acc[mt][2 * half + n2][i];
+          __syncthreads();
+          if (threadIdx.x < 256) {
+            const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < LU_WARPS; ++k) v += sums[k][row][col];
+            total[(16 * mt + row) * COLS + 16 * half + col] = v;
+          }
+        }
       if (cl > 1) tc::cluster_sync();
       else __syncthreads();
       // each CTA of the cluster finishes its share of the tokens
@@ -1066,21 +1088,25 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   s.zeros = l.zeros;
   s.grid = grid2;
   s.m = l.m; s.ng = l.ng; s.used = used; s.m_pad = m_pad;
-  s.grid_ctas = out ? (used + 31) / 32 * (m_pad / 32) : 0;
+  s.grid_ctas = out ? std::min(64, (used + 31) / 32 * (m_pad / 32)) : 0;
   s.limit = !forward && !bf ? 17.f : 0.f;
   // the adapter's rows must be readable in 16-byte pieces; x's are (padded rows are longer than the
   // adapter's, so those go the other way)
   if (K % 8 == 0 && aligned16(w1)) {
     s.U = (low || !fused) ? u_tmp : nullptr;
-    const int tiles = (l.T + LU_TOKENS - 1) / LU_TOKENS;
+    const int mt = (l.T + 15) / 16 > c->num_sms ? 2 : 1, tiles = (l.T + 16 * mt - 1) / (16 * mt);
     // few tokens: up to a CTA per SM, and two steps of 64 features at least per warp
     s.cluster = 1;
     while (s.cluster < 8 && 2 * tiles * s.cluster <= c->num_sms && (K + 63) / 64 > 2 * LU_WARPS * s.cluster)
       s.cluster *= 2;
     s.shrink_ctas = tiles * s.cluster;
     const int grid = s.shrink_ctas + (int)round_up(s.ttiles + s.grid_ctas, s.cluster);
-    auto kernel = l.R <= 16 ? (bf ? k_lora_shrink<true, 2> : k_lora_shrink<false, 2>)
-                            : (bf ? k_lora_shrink<true, 4> : k_lora_shrink<false, 4>);
+    auto pick = [&](auto bf16) {
+      constexpr bool B = decltype(bf16)::value;
+      if (l.R <= 16) return mt == 1 ? k_lora_shrink<B, 2, 1> : k_lora_shrink<B, 2, 2>;
+      return mt == 1 ? k_lora_shrink<B, 4, 1> : k_lora_shrink<B, 4, 2>;
+    };
+    auto kernel = bf ? pick(std::true_type{}) : pick(std::false_type{});
     GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, s.cluster, kernel, dim3(grid), dim3(LU_THREADS), 0, s,
                                           c->status));
   } else {
