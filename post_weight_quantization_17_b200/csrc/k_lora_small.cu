@@ -21,15 +21,16 @@
 namespace gptq {
 
 constexpr int LS_THREADS = 256;
-// 16-row tiles per warp: two halve the reads of X per code; at 32 tokens the registers of their
-// sums leave room for one (two spilled).
-inline constexpr int ls_row_tiles(int token_tiles) { return token_tiles == 4 ? 1 : 2; }
-// steps of codes in the ring: 64 KB per CTA, two CTAs per SM
-__host__ __device__ constexpr int ls_depth(int token_tiles) { return token_tiles == 4 ? 8 : 4; }
-constexpr int LS_SMEM = 8 * 4 * 4 * 512;
-// rows per CTA: 4 row warps x 2 column warps
-constexpr int ls_rows(int token_tiles) { return 64 * ls_row_tiles(token_tiles); }
+constexpr int LS_MT = 2;                       // 16-row tiles per warp: two halve the reads of X per code
+constexpr int LS_ROWS = 4 * LS_MT * 16;        // rows per CTA: 4 row warps x 2 column warps
 constexpr int LS_KC = 4096;                    // columns per warp of A X
+// Up to 16 tokens two CTAs share an SM (128 registers a thread, 4 steps of codes in each ring); with 24
+// or 32 the sums take the registers of one, whose ring is twice as deep.  (One 16-row tile per warp and
+// two CTAs: L1 then delivers X twice as often, 8 KB per KB of codes, and 24 tokens of 11008 x 4096 took
+// 29 us instead of 21.)
+__host__ __device__ constexpr int ls_ctas(int token_tiles) { return token_tiles <= 2 ? 2 : 1; }
+__host__ __device__ constexpr int ls_depth(int token_tiles) { return token_tiles <= 2 ? 4 : 8; }
+__host__ __device__ constexpr int ls_smem(int token_tiles) { return 8 * ls_depth(token_tiles) * 2 * LS_MT * 512; }
 
 struct SmallParams {
   const void* X;
@@ -41,18 +42,19 @@ struct SmallParams {
   int steps, per, row_ctas;  // steps in all and per split, CTAs along the rows
   int wide;                  // rows of codes may be read in 8- or 16-byte pieces
   float* part;               // [splits, T, m]
-  int shrink_ctas, n, R, chunks;
+  int base_ctas, n, R, chunks;
+  int ranks;                 // rank indices per warp of A X
   const int32_t* adapter;
   const void* A;
   float* upart;              // [chunks, T, R]
 };
 
-// One piece (32 codes, BITS words) of a row into this lane's slot; zeros outside the row.
-template <int BITS>
+// One piece (32 codes, BITS words) of a row into this lane's slot; with CHECK zeros outside the row.
+template <int BITS, bool CHECK>
 __device__ __forceinline__ void copy_codes(const SmallParams& p, const uint32_t* src, int words_left,
                                            uint32_t dst) {
   if (p.wide && (BITS == 4 || BITS == 2)) {
-    const int n = words_left > 0 ? 4 * BITS : 0;
+    const int n = !CHECK || words_left > 0 ? 4 * BITS : 0;
     if (BITS == 4)
       asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
                    "l"(n ? src : p.packed), "r"(n)
@@ -64,7 +66,7 @@ __device__ __forceinline__ void copy_codes(const SmallParams& p, const uint32_t*
   } else {
 #pragma unroll
     for (int i = 0; i < BITS; ++i) {
-      const int n = i < words_left ? 4 : 0;
+      const int n = !CHECK || i < words_left ? 4 : 0;
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * i),
                    "l"(n ? src + i : p.packed), "r"(n)
                    : "memory");
@@ -72,51 +74,56 @@ __device__ __forceinline__ void copy_codes(const SmallParams& p, const uint32_t*
   }
 }
 
-// out[c, t, j] = Σ_{k in chunk c} X[t, k] A[a_t, j, k], one warp each.
+// out[c, t, j] = Σ_{k in chunk c} X[t, k] A[a_t, j, k]: a warp takes a chunk of a token and `ranks` rank
+// indices one after the other.
 template <bool BF16>
-__device__ __forceinline__ void small_shrink(const SmallParams& p, DeviceStatus* st) {
-  const int lane = threadIdx.x & 31;
-  const long long e = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (e >= (long long)p.chunks * p.T * p.R) return;
-  const int j = (int)(e % p.R), t = (int)(e / p.R % p.T), c = (int)(e / p.R / p.T);
+__device__ __forceinline__ void small_shrink(const SmallParams& p, int cta, DeviceStatus* st) {
+  const int lane = threadIdx.x & 31, runs = (p.R + p.ranks - 1) / p.ranks;
+  const long long e = (long long)cta * 8 + (threadIdx.x >> 5);
+  if (e >= (long long)p.chunks * p.T * runs) return;
+  const int j0 = (int)(e % runs) * p.ranks, t = (int)(e / runs % p.T), c = (int)(e / runs / p.T);
   const int a = adapter_of(p.adapter, t, p.n, st);
-  float s0 = 0.f, s1 = 0.f;
-  if (a >= 0) {
-    const uint4* x = reinterpret_cast<const uint4*>((const uint16_t*)p.X + (long long)t * p.d);
-    const uint4* w = reinterpret_cast<const uint4*>((const uint16_t*)p.A + ((long long)a * p.R + j) * p.d);
-    const int v1 = min(p.d, (c + 1) * LS_KC) / 8;
+  const uint4* x = reinterpret_cast<const uint4*>((const uint16_t*)p.X + (long long)t * p.d);
+  const int v1 = min(p.d, (c + 1) * LS_KC) / 8;
+  for (int j = j0; j < min(p.R, j0 + p.ranks); ++j) {
+    float s0 = 0.f, s1 = 0.f;
+    if (a >= 0) {
+      const uint4* w = reinterpret_cast<const uint4*>((const uint16_t*)p.A + ((long long)a * p.R + j) * p.d);
 #pragma unroll 4
-    for (int v = c * (LS_KC / 8) + lane; v < v1; v += 32) {
-      const uint4 xv = x[v], wv = w[v];
-      const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w}, ws[4] = {wv.x, wv.y, wv.z, wv.w};
+      for (int v = c * (LS_KC / 8) + lane; v < v1; v += 32) {
+        const uint4 xv = x[v], wv = w[v];
+        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w}, ws[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 xf = pair_f32<BF16>(xs[i]), wf = pair_f32<BF16>(ws[i]);
-        s0 = fmaf(xf.x, wf.x, s0);
-        s1 = fmaf(xf.y, wf.y, s1);
+        for (int i = 0; i < 4; ++i) {
+          const float2 xf = pair_f32<BF16>(xs[i]), wf = pair_f32<BF16>(ws[i]);
+          s0 = fmaf(xf.x, wf.x, s0);
+          s1 = fmaf(xf.y, wf.y, s1);
+        }
       }
     }
-  }
-  float s = s0 + s1;
+    float s = s0 + s1;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) p.upart[e] = s;
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) p.upart[((long long)c * p.T + t) * p.R + j] = s;
+  }
 }
 
 template <int BITS, int NT, bool BF16>
-__global__ void __launch_bounds__(LS_THREADS, 2) k_lora_small(SmallParams p, DeviceStatus* st) {
+__global__ void __launch_bounds__(LS_THREADS, ls_ctas(NT)) k_lora_small(SmallParams p, DeviceStatus* st) {
   pdl_wait();
   pdl_release();
-  if ((int)blockIdx.x < p.shrink_ctas) {
-    small_shrink<BF16>(p, st);
+  // the product's CTAs first: those of A X then fill what their wave leaves (put first, they pushed 124 of
+  // 288 long CTAs into a second wave: 8 tokens of 12288 x 49152 took 101 us instead of 93)
+  if ((int)blockIdx.x >= p.base_ctas) {
+    small_shrink<BF16>(p, blockIdx.x - p.base_ctas, st);
     return;
   }
-  constexpr int LS_MT = NT == 4 ? 1 : 2, DEPTH = ls_depth(NT), PIECES = 2 * LS_MT;
+  constexpr int DEPTH = ls_depth(NT), PIECES = 2 * LS_MT;
   extern __shared__ __align__(16) uint8_t ls_smem[];
-  const int bid = blockIdx.x - p.shrink_ctas;
+  const int bid = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wr = warp & 3, wk = warp >> 2, g = lane >> 2, t4 = lane & 3;
-  const int row0 = (bid % p.row_ctas) * (64 * LS_MT) + wr * (LS_MT * 16) + g, split = bid / p.row_ctas;
+  const int row0 = (bid % p.row_ctas) * LS_ROWS + wr * (LS_MT * 16) + g, split = bid / p.row_ctas;
   const int n = min(p.steps, (split + 1) * p.per) - split * p.per;
   const int s0 = split * p.per + (wk ? (n + 1) / 2 : 0), s1 = split * p.per + (wk ? n : (n + 1) / 2);
   float acc[LS_MT][NT][4] = {};
@@ -129,6 +136,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) k_lora_small(SmallParams p, Dev
   // This lane's slots: [DEPTH][PIECES] of 16 bytes, 32 lanes side by side.
   const uint8_t* const slot0 = ls_smem + warp * (DEPTH * PIECES * 512) + lane * 16;
   const uint32_t slot0_u = (uint32_t)__cvta_generic_to_shared(slot0);
+  const int ragged = p.d % 128 ? p.steps - 1 : -1;   // the step that ends before its last column
   const uint32_t* csrc[PIECES];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i)
@@ -136,12 +144,18 @@ __global__ void __launch_bounds__(LS_THREADS, 2) k_lora_small(SmallParams p, Dev
   int ahead = s0, put = 0;   // the next step to copy, and its place
   auto copy_step = [&] {
     if (ahead < s1) {
-      const int left = p.wpr - (ahead * 4 + t4) * BITS;
+      if (ahead != ragged) {
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        copy_codes<BITS>(p, csrc[i], left, slot0_u + (put * PIECES + i) * 512);
-        csrc[i] += 4 * BITS;
+        for (int i = 0; i < PIECES; ++i)
+          copy_codes<BITS, false>(p, csrc[i], 0, slot0_u + (put * PIECES + i) * 512);
+      } else {
+        const int left = p.wpr - (ahead * 4 + t4) * BITS;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+          copy_codes<BITS, true>(p, csrc[i], left, slot0_u + (put * PIECES + i) * 512);
       }
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) csrc[i] += 4 * BITS;
     }
     ++ahead;
     put = (put + 1) % DEPTH;
@@ -177,19 +191,26 @@ __global__ void __launch_bounds__(LS_THREADS, 2) k_lora_small(SmallParams p, Dev
   for (int nt = 0; nt < NT; ++nt)
     xrow[nt] = reinterpret_cast<const uint4*>((const uint16_t*)p.X + (long long)min(nt * 8 + g, p.T - 1) * p.d +
                                               s0 * 128 + t4 * 32);
-  const int ragged = p.d % 128 ? p.steps - 1 : -1;   // the step that ends before its last column
-  auto load_x = [&](int s, int q, uint4 (&x)[NT]) {   // q 4: the first of the next step
-    if ((s == ragged && s * 128 + t4 * 32 + 8 * q >= p.d && q < 4) ||
-        (q == 4 && (s + 1 >= s1 || (s + 1 == ragged && (s + 1) * 128 + t4 * 32 >= p.d)))) {
+  // The q-th 8 columns of step s, which is the one that `xrow` points to (q 4 and up: of the next, or of
+  // this one once more where there is no next).  Loaded XA pieces ahead: three for 8 tokens, where an
+  // L2 round trip is as long as the work on two, one where the registers hold more tokens.
+  constexpr int XA = NT == 1 ? 3 : 1, XB = XA + 1;
+  auto load_x = [&](int s, int q, uint4 (&x)[NT]) {
+    if (s + (q >> 2) == ragged) {
+      const bool in = s * 128 + t4 * 32 + (q >> 2) * 128 + 8 * (q & 3) < p.d;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt] = make_uint4(0, 0, 0, 0);
+      for (int nt = 0; nt < NT; ++nt) x[nt] = in ? xrow[nt][(q >> 2) * 16 + (q & 3)] : make_uint4(0, 0, 0, 0);
     } else {
+      const int at = q >= 4 && s + 1 < s1 ? 16 : 0;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt] = xrow[nt][q == 4 ? 16 : q];
+      for (int nt = 0; nt < NT; ++nt) x[nt] = xrow[nt][at + (q & 3)];
     }
   };
-  uint4 x[2][NT];
-  if (s0 < s1) load_x(s0, 0, x[0]);
+  uint4 x[XB][NT];
+  if (s0 < s1) {
+#pragma unroll
+    for (int q = 0; q < XA; ++q) load_x(s0, q, x[q]);
+  }
   int get = 0;
   for (int sb = s0; sb < s1; sb += 4) {
     float sn[PIECES];
@@ -223,12 +244,12 @@ __global__ void __launch_bounds__(LS_THREADS, 2) k_lora_small(SmallParams p, Dev
       float dd[LS_MT][NT][4] = {};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        load_x(s, q + 1, x[(q + 1) & 1]);
+        load_x(s, q + XA, x[(q + XA) % XB]);
         if (q == 3) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) xrow[nt] += 16;
         }
-        const uint4 (&xq)[NT] = x[q & 1];
+        const uint4 (&xq)[NT] = x[q % XB];
         // Eight tokens: codes two apart make a pair (one byte permute each, from the even and the odd
         // nibbles), and the activations are put in the same order; with more tokens that would cost
         // more than the pairs in column order do.
@@ -435,7 +456,7 @@ int lora_join(Ctx* c, const LoraLayer& l, const float* part, int splits, int F, 
 
 namespace {
 
-int token_tiles(int T) { return T <= 8 ? 1 : (T <= 16 ? 2 : 4); }
+int token_tiles(int T) { return (T + 7) / 8; }
 
 template <int BITS>
 int launch_small(Ctx* c, const SmallParams& p, int grid, bool bf) {
@@ -444,11 +465,12 @@ int launch_small(Ctx* c, const SmallParams& p, int grid, bool bf) {
   do {                                                                                              \
     auto kernel = bf ? k_lora_small<BITS, NT, true> : k_lora_small<BITS, NT, false>;                \
     GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(                                                        \
-                           kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LS_SMEM));          \
-    GPTQ_LAUNCH(c, kernel, grid, LS_THREADS, LS_SMEM, p, c->status);                                \
+                           kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ls_smem(NT)));       \
+    GPTQ_LAUNCH(c, kernel, grid, LS_THREADS, ls_smem(NT), p, c->status);                                \
   } while (0)
   if (nt == 1) GPTQ_SMALL(1);
   else if (nt == 2) GPTQ_SMALL(2);
+  else if (nt == 3) GPTQ_SMALL(3);
   else GPTQ_SMALL(4);
 #undef GPTQ_SMALL
   return GPTQ_OK;
@@ -456,10 +478,11 @@ int launch_small(Ctx* c, const SmallParams& p, int grid, bool bf) {
 
 int small_chunks(int d) { return (d + LS_KC - 1) / LS_KC; }
 
-// Splits of the columns so that the CTAs (two fit on an SM) fill whole waves: the smallest
-// waves x (steps of a warp + 2 for its start).
+// Splits of the columns so that the CTAs fill whole waves: the smallest waves x (steps of a warp + 2 for
+// its start).  (Those of A X are short and run alongside; counting them in cost 24 tokens of 11008 x 4096
+// 25 us instead of 21.)
 int small_splits(int m, int d, int T, int num_sms, size_t max_floats) {
-  const long long rows = (m + ls_rows(token_tiles(T)) - 1) / ls_rows(token_tiles(T)), steps = (d + 127) / 128, slots = 2LL * num_sms;
+  const long long rows = (m + LS_ROWS - 1) / LS_ROWS, steps = (d + 127) / 128, slots = (long long)ls_ctas(token_tiles(T)) * num_sms;
   long long best = -1;
   int splits = 1;
   for (int s = 1; s <= 64 && s <= steps; ++s) {
@@ -504,20 +527,23 @@ int lora_forward_small(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool 
   p.ng = l.ng;
   p.group_steps = l.group == -1 ? 0 : l.group / 128;
   p.steps = (l.d + 127) / 128;
+  p.n = l.n; p.R = l.R;
+  p.chunks = small_chunks(l.d);
+  // at most about 128 CTAs of A X, so that they run beside the product's first wave
+  const long long parts = (long long)p.chunks * l.T * l.R;
+  p.ranks = (int)std::min<long long>(l.R, (parts + 1023) / 1024);
+  const long long warps = (long long)p.chunks * l.T * ((l.R + p.ranks - 1) / p.ranks);
   const int splits = small_splits(l.m, l.d, l.T, c->num_sms, ws_floats - uf);
   p.per = (p.steps + splits - 1) / splits;
-  p.row_ctas = (l.m + ls_rows(token_tiles(l.T)) - 1) / ls_rows(token_tiles(l.T));
+  p.row_ctas = (l.m + LS_ROWS - 1) / LS_ROWS;
   const int piece = l.bits == 4 ? 4 : 2;   // words per load of codes
   p.wide = p.wpr % piece == 0 && (reinterpret_cast<uintptr_t>(l.packed) & (piece * 4 - 1)) == 0;
   p.upart = ws;
   p.part = ws + uf;
-  p.n = l.n; p.R = l.R;
-  p.chunks = small_chunks(l.d);
   p.adapter = l.adapter;
   p.A = l.A;
-  const long long warps = (long long)p.chunks * l.T * l.R;
-  p.shrink_ctas = (int)((warps + 7) / 8);
-  const int grid = p.shrink_ctas + p.row_ctas * splits;
+  p.base_ctas = p.row_ctas * splits;
+  const int grid = p.base_ctas + (int)((warps + 7) / 8);
   const bool bf = l.dtype == GPTQ_BF16;
   int rc;
   switch (l.bits) {

@@ -676,38 +676,35 @@ struct ShrinkParams {
   float limit;
 };
 
-// 32 x 32 tiles i, i + grid_ctas, ... of the grid; every thread of the CTA (at least 256).
+// The grid's share of CTA i of grid_ctas: a warp takes 32 rows x 8 groups at a time, a row per lane, whose
+// 16 loads are independent (a lane's next groups lie in the same sectors) and whose stores are contiguous
+// over the lanes.
 __device__ __forceinline__ void turn_grid(const ShrinkParams& p, int i, DeviceStatus* st) {
-  __shared__ float2 tile[32][33];
-  const int across = (p.used + 31) / 32, tiles = across * (p.m_pad / 32);
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  for (; i < tiles; i += p.grid_ctas) {
-  const int g0 = i % across * 32, r0 = i / across * 32;
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  const int across = (p.used + 7) / 8, tasks = across * (p.m_pad / 32);
   bool bad = false;
-  if (y < 8) {
+  for (int k = i * warps + (threadIdx.x >> 5); k < tasks; k += p.grid_ctas * warps) {
+    const int g0 = k % across * 8, r = k / across * 32 + lane;
+    const long long at = (long long)min(r, p.m - 1) * p.ng + g0;
+    float d[8];
+    int z[8];
 #pragma unroll
-    for (int k = y; k < 32; k += 8) {
-      float2 v = make_float2(0.f, 0.f);
-      if (r0 + k < p.m && g0 + x < p.used) {
-        const long long at = (long long)(r0 + k) * p.ng + g0 + x;
-        const int z = p.zeros[at];
-        v = make_float2(p.scales[at], (float)z);
-        bad = bad || z < 0 || z > 15 || (p.limit > 0.f && !(fabsf(v.x) < p.limit));
-        if (z < 0 || z > 15) v.y = 0.f;
+    for (int e = 0; e < 8; ++e) {
+      const bool in = r < p.m && g0 + e < p.used;
+      d[e] = in ? p.scales[at + e] : 0.f;
+      z[e] = in ? p.zeros[at + e] : 0;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (z[e] < 0 || z[e] > 15) {
+        bad = true;
+        z[e] = 0;
       }
-      tile[k][x] = v;
+      bad = bad || (p.limit > 0.f && !(fabsf(d[e]) < p.limit));
+      if (g0 + e < p.used) p.grid[(long long)(g0 + e) * p.m_pad + r] = make_float2(d[e], (float)z[e]);
     }
   }
-  if (bad) raise_error(st, GPTQ_ERR_ARG, r0);
-  __syncthreads();
-  if (y < 8) {
-#pragma unroll
-    for (int k = y; k < 32; k += 8)
-      if (g0 + k < p.used && r0 + x < p.m_pad)
-        p.grid[(long long)(g0 + k) * p.m_pad + r0 + x] = tile[x][k];
-  }
-  __syncthreads();
-  }
+  if (bad) raise_error(st, GPTQ_ERR_ARG, i);
 }
 
 __device__ __forceinline__ void write_low_rank(const ShrinkParams& p, int t, int j, float u) {
@@ -772,22 +769,20 @@ __global__ void __launch_bounds__(LU_THREADS, 1) k_lora_shrink(ShrinkParams p, D
 #pragma unroll
   for (int i = 0; i < 2 * MT; ++i)
     x[i] = (const uint16_t*)p.x + (long long)min(t0 + g + 8 * i, p.T - 1) * p.F + 8 * t4;
-  // tokens without an adapter
+  uint32_t todo = __ballot_sync(0xffffffffu, id >= 0);
+  // zeros: tokens without an adapter, and the ranks behind the last pass
+  const int passes = (p.R + COLS - 1) / COLS * COLS;
   if (rank == 0)
     for (int e = threadIdx.x; e < LU_TOKENS * p.Rp; e += LU_THREADS) {
-      const int t = t0 + e / p.Rp;
-      if (t < p.T) {
-        const int a = p.adapter[t];
-        if (a < 0 || a >= p.n) write_low_rank(p, t, e % p.Rp, 0.f);
-      }
+      const int row = e / p.Rp, j = e % p.Rp;
+      if (t0 + row < p.T && (j >= passes || !((todo >> row) & 1u))) write_low_rank(p, t0 + row, j, 0.f);
     }
-  uint32_t todo = __ballot_sync(0xffffffffu, id >= 0);
   while (todo) {
     const int a = __shfl_sync(0xffffffffu, id, __ffs(todo) - 1);
     const uint32_t mine = __ballot_sync(0xffffffffu, id == a);
     todo &= ~mine;
     const float scale = p.scaling[a];
-    for (int j0 = 0; j0 < p.Rp; j0 += COLS) {
+    for (int j0 = 0; j0 < p.R; j0 += COLS) {
       float acc[MT][NTL][4] = {};
       // this lane's rank rows j0 + g + 8 n (clamped: what lies behind R is not kept)
       const uint16_t* w[NTL];
@@ -1088,7 +1083,7 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   s.zeros = l.zeros;
   s.grid = grid2;
   s.m = l.m; s.ng = l.ng; s.used = used; s.m_pad = m_pad;
-  s.grid_ctas = out ? std::min(64, (used + 31) / 32 * (m_pad / 32)) : 0;
+  s.grid_ctas = out ? std::min(64, ((used + 7) / 8 * (m_pad / 32) + 7) / 8) : 0;
   s.limit = !forward && !bf ? 17.f : 0.f;
   // the adapter's rows must be readable in 16-byte pieces; x's are (padded rows are longer than the
   // adapter's, so those go the other way)
