@@ -272,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         const int k1 = FWD ? 2 * t.u1 : t.u1;
         for (int k = FWD ? 2 * t.u0 : t.u0; k < k1 && ok; ++k) stage(&tmX, k * 64, t.t0);
         if (!p.rank_chunks) continue;
-        if (!waited) pdl_wait();
+        if (!waited) pdl_wait();   // only now: the tokens' operand is the caller's
         waited = true;
         const int count = p.slots[t.nt * (BN + 1)];
         for (int s = 0; s < count && ok; ++s)
@@ -290,7 +290,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       // -------------------------------------------------------------- MMA issuer
       LtRing<NS> ring;
       LtRing<ND> dr;
-      bool ok = true, any = false, waited = false, ready = false;
+      bool ok = true, any = false, ready = false;
+      pdl_wait();   // the slots
       // The descriptors of stage 0; a stage or a k step on is an addition to the address field (in
       // 16-byte units; shared memory ends below its 14 bits).  Little else may stand between the
       // MMAs: this thread's own instructions are what would hold them up.
@@ -345,14 +346,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       };
       for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
         const LtTile t(p, i, BN, rank);
+        const int count = p.rank_chunks ? p.slots[t.nt * (BN + 1)] : 0;   // on its way meanwhile
         if (FWD)
           for (int u = t.u0; u < t.u1 && ok; ++u) partial(2, false);
         else
           partial(t.u1 - t.u0, false);
-        if (!p.rank_chunks) continue;
-        if (!waited) pdl_wait();
-        waited = true;
-        const int count = p.slots[t.nt * (BN + 1)];
         for (int s = 0; s < count && ok; ++s) partial(2 * p.rank_chunks, true);
       }
       // every MMA has completed before TMEM is freed
@@ -404,7 +402,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     const int tid = threadIdx.x;
     LtRing<NS> ring;
     LtRing<NC> cring;
-    bool ok = true, waited = false;
+    bool ok = true;
+    pdl_wait();   // the slots
     // A thread's piece is 16 bytes (32 codes) of a row: eight lanes with the same piece of eight rows
     // read eight different 16-byte columns of the 64-byte-swizzled codes, and store to eight
     // different ones of the 128-byte-swizzled operand.  Forward: 128 rows x 128 columns at a time,
@@ -414,7 +413,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     uint32_t pc = 0;   // partial sums so far
     for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
       const LtTile t(p, i, BN, rank);
+      // An adapter's rows go from global memory into registers (thread = feature and half of a chunk's
+      // 32 ranks) while the work before them is still going on: forward, the first during the last units.
+      const int32_t* slots = p.slots + t.nt * (BN + 1);
+      const int fr = tid & 127, jh = tid >> 7, f = t.f0 + fr;
+      const int chunks = p.rank_chunks ? slots[0] * p.rank_chunks : 0;
+      uint16_t next[16];
+      auto fetch = [&](int q) {
+        const int j0 = 32 * (q % p.rank_chunks) + 16 * jh;
+        const uint16_t* w = (const uint16_t*)p.w + (long long)slots[1 + q / p.rank_chunks] * p.R * p.M + f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          next[j] = f < p.M && j0 + j < p.R ? w[(long long)(j0 + j) * p.M] : (uint16_t)0;
+      };
       for (int k = t.u0; k < t.u1; ++k) {
+        if (FWD && k == max(t.u0, t.u1 - 2) && chunks) fetch(0);
         LtRing<NS> second = ring;
         second.next();
         if (!__all_sync(0xffffffffu,
@@ -504,43 +517,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         cring.next();
         ++pc;
       }
-      if (!p.rank_chunks || !ok) continue;
-      if (!waited) pdl_wait();
-      waited = true;
-      const int32_t* slots = p.slots + t.nt * (BN + 1);
-      // thread = feature and half of a chunk's 32 ranks
-      const int count = slots[0], fr = tid & 127, jh = tid >> 7, f = t.f0 + fr;
-      for (int s = 0; s < count && ok; ++s) {
-        const uint16_t* w = (const uint16_t*)p.w + (long long)slots[1 + s] * p.R * p.M + f;
-        ++pc;
-        for (int c = 0; c < p.rank_chunks && ok; ++c) {
-          const int j0 = 32 * c + 16 * jh;
-          uint32_t v[8];   // 16 ranks of this feature, two to a word
+      if (!FWD && chunks) fetch(0);   // (inside the loop its registers cost the backward units 5 %)
+      for (int q = 0; q < chunks && ok; ++q) {
+        if (q % p.rank_chunks == 0) ++pc;
+        uint32_t v[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint32_t e = (f < p.M && j0 + j < p.R) ? w[(long long)(j0 + j) * p.M] : 0u;
-            if (j & 1) v[j / 2] |= e << 16;
-            else v[j / 2] = e;
+        for (int j = 0; j < 8; ++j) v[j] = next[2 * j] | ((uint32_t)next[2 * j + 1] << 16);
+        if (q + 1 < chunks) fetch(q + 1);
+        for (int half = 0; half < 2; ++half) {   // against U's high and low parts
+          if (!lt_wait_warp(&empty[ring.i], ring.phase ^ 1u, budget)) {
+            raise_error(st, GPTQ_ERR_TIMEOUT, 77);
+            *abort_flag = 1;
+            ok = false;
+            break;
           }
-          for (int half = 0; half < 2; ++half) {   // against U's high and low parts
-            if (!lt_wait_warp(&empty[ring.i], ring.phase ^ 1u, budget)) {
-              raise_error(st, GPTQ_ERR_TIMEOUT, 77);
-              *abort_flag = 1;
-              ok = false;
-              break;
-            }
-            uint8_t* dst = smem + ring.i * Cfg::STAGE + fr * 128;
+          uint8_t* dst = smem + ring.i * Cfg::STAGE + fr * 128;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 a = pair_f32<BF16>(v[2 * e]), b = pair_f32<BF16>(v[2 * e + 1]);
-              *reinterpret_cast<float4*>(dst + (((4 * jh + e) ^ (fr & 7)) << 4)) =
-                  make_float4(a.x, a.y, b.x, b.y);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) lt_arrive_remote(lead_full_a + 8u * ring.i);
-            ring.next();
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = pair_f32<BF16>(v[2 * e]), b = pair_f32<BF16>(v[2 * e + 1]);
+            *reinterpret_cast<float4*>(dst + (((4 * jh + e) ^ (fr & 7)) << 4)) =
+                make_float4(a.x, a.y, b.x, b.y);
           }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) lt_arrive_remote(lead_full_a + 8u * ring.i);
+          ring.next();
         }
       }
     }
