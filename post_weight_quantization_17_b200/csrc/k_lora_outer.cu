@@ -58,7 +58,7 @@ struct OuterGroup {
 };
 
 template <bool BF16>
-__global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_constant__ OuterParams p) {
+__global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_constant__ OuterParams p, DeviceStatus* st) {
   pdl_wait();
   pdl_release();
   extern __shared__ __align__(16) float lo_smem_[];
@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const bool one = id[i] >= 0 && id[i] < p.n;
+      if (id[i] < -1 || id[i] >= p.n) raise_error(st, GPTQ_ERR_ARG, t + i * LO_THREADS);
       if (t + i * LO_THREADS < p.T) id_of[t + i * LO_THREADS] = one ? (uint16_t)id[i] : (uint16_t)0xFFFF;
       if (one && !((present[id[i] >> 5] >> (id[i] & 31)) & 1u))
         atomicOr(&present[id[i] >> 5], 1u << (id[i] & 31));
@@ -267,7 +268,8 @@ int lora_outers(Ctx* c, const LoraLayer& l, const float* G, const void* X, float
     const dim3 grid(ca + cb, ranks, std::max(1, std::min(l.n, 4 * c->num_sms / ((ca + cb) * ranks))));
     const int smem = LO_SMEM + (l.n + 31) / 32 * 4 + (p.T + 1) / 2 * 4;
     GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, p.cluster, kernel, grid, dim3(LO_THREADS), smem, p));
+    GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, p.cluster, kernel, grid, dim3(LO_THREADS), smem, p,
+                                          c->status));
   }
   return GPTQ_OK;
 }

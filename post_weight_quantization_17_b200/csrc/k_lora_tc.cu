@@ -989,7 +989,7 @@ int launch_tc(Ctx* c, const CUtensorMap& mx, const CUtensorMap& mu,
                                           LtCfg<FWD, BN>::SMEM));
   const int grid = 2 * std::min(c->num_sms / 2, p.mtiles * p.ttiles * p.splits);
   GPTQ_LAUNCH(c, (k_lora_tc<FWD, BN, BF16>), grid, LT_THREADS, LtCfg<FWD, BN>::SMEM, mx, mu, mc, p, c->status,
-              c->timeout_cycles);
+              kDefaultWaitCycles);   // as every kernel on CTA pairs
   return GPTQ_OK;
 }
 

@@ -210,6 +210,25 @@ def test_gradient_against_differences(ctx):
     assert ((num * dl.double() - got).abs() <= bound).all()
 
 
+def test_offsets_beyond_32_bits(ctx):
+    """More than 2^31 logits, the gradient in place: every 997th token against the formula."""
+    T, V, K = 17000, 128000, 8
+    assert T * V > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(4)
+    z = torch.empty(T, V, dtype=BF, device="cuda").normal_(generator=g)
+    val = torch.randn(T, K, device="cuda", generator=g)
+    idx = (torch.randint(0, V // K, (T, K), device="cuda", generator=g) +
+           torch.arange(K, device="cuda") * (V // K)).to(torch.int32)
+    w, dl = torch.ones(T, device="cuda"), torch.rand(T, device="cuda", generator=g)
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    rows = torch.arange(T - 1, 0, -997, device="cuda")
+    want = _formula(z[rows], val[rows], idx[rows], 1.0, w[rows], dl[rows], None)
+    G.gptq_distill_topk(ctx, z, val, idx, 1.0, loss, lse, dloss=dl, dlogits=z)
+    G.gptq_sync_status(ctx)
+    _near(loss[rows], want[0], want[3], F32, "loss")
+    _near(z[rows], want[2], want[5], BF, "dlogits")
+
+
 def test_captured_and_replayed():
     s = torch.cuda.Stream()
     z, val, idx, w, dl, _ = _inputs(6, 5003, 16, BF, 12)

@@ -33,6 +33,13 @@ SHAPES = {
     "t300_odd_length": (300, 131, 333, 4, 128, 12, 3, BF, BF, "runs", {}),
     "t640_m_odd": (640, 2049, 512, 2, 128, 16, 4, HF, HF, "runs", {"offset": 1}),
     "rank_200": (40, 128, 256, 4, 128, 200, 2, BF, BF, "mixed", {}),
+    "t300_300_adapters": (300, 128, 256, 4, 128, 8, 300, BF, F32, "mixed", {}),
+    "t8300_many_tokens": (8300, 40, 128, 4, 128, 4, 3, BF, BF, "mixed", {}),
+    "t40_one_row_of_8": (40, 1, 8, 4, 128, 3, 2, HF, F32, "mixed", {}),
+    "t40_one_column": (40, 9, 1, 4, -1, 2, 2, BF, BF, "mixed", {}),
+    "t24": (24, 200, 384, 4, 128, 16, 24, HF, HF, "mixed", {}),
+    "t32_fc2_like": (32, 256, 6144, 4, 128, 32, 8, BF, BF, "mixed", {}),
+    "t129_wide_grid": (129, 300, 8192, 4, 128, 16, 2, BF, F32, "runs", {}),
     "any_fp32": (11, 70, 130, 4, 128, 8, 3, F32, F32, "mixed", {}),
     "any_8bit": (9, 65, 96, 8, -1, 5, 2, BF, BF, "mixed", {}),
     "any_g32": (12, 80, 200, 4, 32, 8, 2, HF, F32, "runs", {}),
@@ -177,6 +184,35 @@ def test_other_requests_do_not_leak(ctx, T):
     G.gptq_sync_status(ctx)
 
 
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements of Y and of dY: every 997th token against the formulas."""
+    T, m, d, R, n = 66000, 33000, 64, 4, 3
+    assert T * m > 2 ** 31
+    c = Case(8, m, d, 4, -1, R, n, BF, "mixed", 12)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    c.T = T
+    c.X = torch.randn(T, d, device="cuda", generator=g).to(BF)
+    c.adapter = torch.randint(-1, n, (T,), device="cuda", generator=g, dtype=torch.int32)
+    big = G.Context(1, 1, workspace_bytes=G.gptq_lora_workspace_bytes(T, m, d, 4, n, R, BF))
+    try:
+        Y, U = torch.empty(T, m, dtype=BF, device="cuda"), torch.empty(T, R, device="cuda")
+        G.gptq_lora_matmul(big, c.X, *c.layer(), Y, U=U)
+        dX = torch.empty_like(c.X)
+        G.gptq_lora_backward(big, Y, c.X, *c.layer(), U, dX=dX)
+        G.gptq_sync_status(big)
+        rows = torch.arange(T - 1, 0, -997, device="cuda")
+        few = Case.__new__(Case)
+        few.__dict__.update(c.__dict__)
+        few.T, few.X, few.dY, few.adapter = len(rows), c.X[rows], Y[rows], c.adapter[rows]
+        want, bound, u, ubound = few.forward(BF)
+        within(U[rows], u, ubound, "U")
+        within(Y[rows], want, bound, "Y")
+        dx, dx_bound = few.backward(u, True)[0]
+        within(dX[rows], dx, dx_bound, "dX")
+    finally:
+        big.close()
+
+
 def test_empty_batch(ctx):
     c = Case(1, 64, 128, 4, 128, 8, 2, BF)
     none = lambda *s, dt=BF: torch.empty(*s, dtype=dt, device="cuda")  # noqa: E731
@@ -206,12 +242,30 @@ def test_bad_ids_and_zeros_are_reported(ctx):
         with pytest.raises(G.GPTQError) as e:
             G.gptq_sync_status(ctx)
         assert e.value.code == G.GPTQ_ERR_ARG and torch.equal(Y, want)
-    c.adapter.copy_(good)
-    c.zeros[5, 1] = 16
-    G.gptq_lora_matmul(ctx, c.X, *c.layer(), Y)
-    with pytest.raises(G.GPTQError) as e:
+        for out in (dict(dX=torch.empty_like(c.X)), dict(dB=torch.empty_like(c.B, dtype=F32))):
+            G.gptq_lora_backward(ctx, c.dY, None, *c.layer(), torch.zeros(8, 8, device="cuda"), **out)
+            with pytest.raises(G.GPTQError) as e:
+                G.gptq_sync_status(ctx)
+            assert e.value.code == G.GPTQ_ERR_ARG
+    for T in (8, 80):
+        c = Case(T, 64, 256, 4, 128, 8, 2, HF, "mixed", 9)
+        Y, dX = torch.empty(T, 64, device="cuda"), torch.empty_like(c.X)
+        calls = [lambda: G.gptq_lora_matmul(ctx, c.X, *c.layer(), Y),
+                 lambda: G.gptq_lora_backward(ctx, c.dY, None, *c.layer(), None, dX=dX)]
+        c.zeros[5, 1] = 16
+        for call in calls:
+            call()
+            with pytest.raises(G.GPTQError) as e:
+                G.gptq_sync_status(ctx)
+            assert e.value.code == G.GPTQ_ERR_ARG
+        c.zeros[5, 1] = 15
+        c.scales[3, 0] = 17.5              # fp16 weights of 255 and more: the backward pass only
+        calls[0]()
         G.gptq_sync_status(ctx)
-    assert e.value.code == G.GPTQ_ERR_ARG
+        calls[1]()
+        with pytest.raises(G.GPTQError) as e:
+            G.gptq_sync_status(ctx)
+        assert e.value.code == G.GPTQ_ERR_ARG
 
 
 def test_refusals(ctx):
@@ -270,6 +324,17 @@ def test_workspace_as_asked_for_suffices(T):
         _backward(own, c, U)
     finally:
         own.close()
+
+
+def test_stage_timing_counts_the_calls(ctx):
+    c = Case(80, 256, 512, 4, 128, 16, 2, BF, "runs", 14)
+    plain, _ = _forward(ctx, c, F32)
+    G.gptq_timing_enable(ctx, True)
+    timed, U = _forward(ctx, c, F32)
+    _backward(ctx, c, U)
+    ms, launches = G.gptq_timing_read(ctx)["lora"]
+    G.gptq_timing_enable(ctx, False)
+    assert launches >= 5 and ms > 0 and torch.equal(plain, timed)
 
 
 @pytest.mark.parametrize("T", [4, 200])
