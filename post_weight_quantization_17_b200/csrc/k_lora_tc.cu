@@ -286,8 +286,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         if (!lt_wait(&full_x[j % NS], (uint32_t)(j / NS) & 1u, kDrainCycles))
           raise_error(st, GPTQ_ERR_TIMEOUT, 72);
       }
-    } else if (warp == 17 && lane == 0 && rank == 0) {
+    } else if (warp == 17 && rank == 0) {
       // -------------------------------------------------------------- MMA issuer
+      // (the whole warp runs the loop, so that descriptors and addresses stay in uniform registers, and
+      // one lane issues)
+      uint32_t elected;
+      asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                   : "=r"(elected));
       LtRing<NS> ring;
       LtRing<ND> dr;
       bool ok = true, any = false, ready = false;
@@ -302,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       // one partial sum of `stages` stages
       auto partial = [&](int stages, bool tf32) {
         if (!ok) return;
-        if (!lt_wait(&d_empty[dr.i], dr.phase ^ 1u, budget)) {
+        if (!lt_wait_warp(&d_empty[dr.i], dr.phase ^ 1u, budget)) {
           raise_error(st, GPTQ_ERR_TIMEOUT, 73);
           *abort_flag = 1;
           ok = false;
@@ -310,7 +315,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         }
         const uint32_t d = tmem + dr.i * BN;
         for (int s = 0; s < stages; ++s) {
-          if (!ready && !lt_wait2(&full_x[ring.i], ring.phase, &full_a[ring.i], ring.phase, budget)) {
+          if (!ready && !__all_sync(0xffffffffu, lt_wait2(&full_x[ring.i], ring.phase, &full_a[ring.i],
+                                                          ring.phase, budget))) {
             raise_error(st, GPTQ_ERR_TIMEOUT, 74);
             *abort_flag = 1;
             ok = false;
@@ -323,25 +329,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
           next.next();
           if (tf32) {
             const uint64_t da = dk0 + at;
+            if (elected) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_tf32_pair(d, da + 2 * kk, db + 2 * kk, p.idesc_tf32, (s | kk) ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_tf32_pair(d, da + 2 * kk, db + 2 * kk, p.idesc_tf32, (s | kk) ? 1u : 0u);
+              tc::mma_commit_pair(&empty[ring.i]);
+            }
             ready = false;
           } else {
             const uint64_t da = da0 + at;
+            if (elected) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              tc::mma_f16_pair(d, da + A_STEP * kk, db + 2 * kk, p.idesc, (s | kk) ? 1u : 0u);
-              // the next stage's barriers, while MMAs are still queued behind this one
-              if (kk == 1)
-                ready = lt_test(&full_x[next.i], next.phase) && lt_test(&full_a[next.i], next.phase);
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_f16_pair(d, da + A_STEP * kk, db + 2 * kk, p.idesc, (s | kk) ? 1u : 0u);
+              tc::mma_commit_pair(&empty[ring.i]);
             }
+            // the next stage's barriers, while these MMAs are still being worked on
+            ready = __all_sync(0xffffffffu, lt_test(&full_x[next.i], next.phase) &&
+                                                lt_test(&full_a[next.i], next.phase));
           }
           any = true;
-          tc::mma_commit_pair(&empty[ring.i]);
           ring = next;
         }
-        tc::mma_commit_pair(&d_full[dr.i]);
+        if (elected) tc::mma_commit_pair(&d_full[dr.i]);
         dr.next();
       };
       for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
@@ -355,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       }
       // every MMA has completed before TMEM is freed
       if (any) {
-        tc::mma_commit_pair(drain);
+        if (elected) tc::mma_commit_pair(drain);
         if (!lt_wait(drain, 0, kDrainCycles)) raise_error(st, GPTQ_ERR_TIMEOUT, 75);
       }
     } else if (warp == 18 && lane == 0) {
