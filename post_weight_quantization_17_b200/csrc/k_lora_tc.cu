@@ -104,8 +104,11 @@ __device__ __forceinline__ bool lt_test(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ void lt_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// `count` arrivals on a barrier of either CTA (a shared::cluster address; this CTA's shared::cta
+// addresses are among them).
+__device__ __forceinline__ void lt_arrive_remote(uint32_t cluster_addr, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr), "r"(count)
+               : "memory");
 }
 // Waits for a phase, suspended in hardware between tries; false after `budget` cycles.
 __device__ __forceinline__ bool lt_wait(uint64_t* bar, uint32_t parity, long long budget) {
@@ -418,9 +421,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     // read eight different 16-byte columns of the 64-byte-swizzled codes, and store to eight
     // different ones of the 128-byte-swizzled operand.  Forward: 128 rows x 128 columns at a time,
     // two stages (pieces 0, 1 and 2, 3).  Backward: 64 rows x 128 columns, one stage.
-    const int q = (tid >> 3) & 3, brow = (tid & 7) + 8 * (tid >> 5);
-    constexpr int PIECES = FWD ? 2 : 1;
+    // The units alternate between two groups of four warps, so that one's waits and fences overlap the
+    // other's arithmetic; each arrives for two on the barriers, which count eight warps.
+    const int group = warp >> 2, q = (tid >> 3) & 3, brow = (tid & 7) + 8 * (warp & 3);
+    constexpr int PIECES = FWD ? 4 : 2;
     uint32_t pc = 0;   // partial sums so far
+    int turn = 0;      // whose unit it is
     for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
       const LtTile t(p, i, BN, rank);
       // An adapter's rows go from global memory into registers (thread = feature and half of a chunk's
@@ -440,6 +446,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         if (FWD && k == max(t.u0, t.u1 - 2) && chunks) fetch(0);
         LtRing<NS> second = ring;
         second.next();
+        const bool mine = turn == group;
+        turn ^= 1;
+        if (!mine) {
+          ring.next();
+          if (FWD) ring.next();
+          cring.next();
+          ++pc;
+          continue;
+        }
         if (!__all_sync(0xffffffffu,
                         lt_wait(&full_c[cring.i], cring.phase, budget) &&
                             (FWD ? lt_wait2(&empty[ring.i], ring.phase ^ 1u, &empty[second.i],
@@ -454,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         float2 dz[PIECES];
 #pragma unroll
         for (int h = 0; h < PIECES; ++h) {
-          const int row = brow + 64 * h;
+          const int row = brow + 32 * h;
           code[h] = *reinterpret_cast<const uint4*>(codes + cring.i * Cfg::C_BYTES + row * 64 +
                                                     ((q ^ ((row >> 1) & 3)) << 4));
           dz[h] = grids[cring.i * (Cfg::G_BYTES / 8) + row];
@@ -464,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         // two partials on, have released the stages that were just waited for
         if (FWD && q == 0) {
 #pragma unroll
-          for (int h = 0; h < PIECES; ++h) deltas[(pc % LT_DELTAS) * 128 + brow + 64 * h] = dz[h].x;
+          for (int h = 0; h < PIECES; ++h) deltas[(pc % LT_DELTAS) * 128 + brow + 32 * h] = dz[h].x;
         }
 #pragma unroll
         for (int h = 0; h < PIECES; ++h) {
@@ -487,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
               lo2 = *reinterpret_cast<const uint32_t*>(&b);
             }
           }
-          const int row = brow + 64 * h;
+          const int row = brow + 32 * h;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t v[4];
@@ -518,9 +533,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          lt_arrive_remote(lead_full_a + 8u * ring.i);
-          if (FWD) lt_arrive_remote(lead_full_a + 8u * second.i);
-          tc::mbar_arrive(&empty_c[cring.i]);
+          lt_arrive_remote(lead_full_a + 8u * ring.i, 2);
+          if (FWD) lt_arrive_remote(lead_full_a + 8u * second.i, 2);
+          lt_arrive_remote(tc::smem_u32(&empty_c[cring.i]), 2);
         }
         ring.next();
         if (FWD) ring.next();
@@ -550,7 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) lt_arrive_remote(lead_full_a + 8u * ring.i);
+          if (lane == 0) lt_arrive_remote(lead_full_a + 8u * ring.i, 1);
           ring.next();
         }
       }
