@@ -77,7 +77,7 @@ struct LtParams {
   const void* w;            // [n, R, M] 16-bit
   const int32_t* slots;     // per token tile: count, then the adapters that occur in it
   void* out;                // [T, M]
-  int out_f32;
+  int out_f32, wide_out;    // wide_out: 16-bit, M a multiple of 4, 8-byte aligned
   float* part;              // [splits, T, M] or null
   uint32_t idesc, idesc_tf32;
 };
@@ -157,6 +157,16 @@ __device__ __forceinline__ void fma_f32x2(float& a0, float& a1, uint64_t f, uint
       "mov.b64 {%0, %1}, a;\n\t}"
       : "+f"(a0), "+f"(a1)
       : "l"(f), "r"(v0), "r"(v1));
+}
+
+// Two values rounded to the 16-bit type, the first in the low half.
+template <bool BF16> __device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // A position in a ring of N stages or buffers.
@@ -430,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
       const LtTile t(p, i, BN, rank);
       // An adapter's rows go from global memory into registers (thread = feature and half of a chunk's
-      // 32 ranks) while the work before them is still going on: forward, the first during the last units.
+      // 32 ranks) while the stage before them still waits for its place.
       const int32_t* slots = p.slots + t.nt * (BN + 1);
       const int fr = tid & 127, jh = tid >> 7, f = t.f0 + fr;
       const int chunks = p.rank_chunks ? slots[0] * p.rank_chunks : 0;
@@ -443,7 +453,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
           next[j] = f < p.M && j0 + j < p.R ? w[(long long)(j0 + j) * p.M] : (uint16_t)0;
       };
       for (int k = t.u0; k < t.u1; ++k) {
-        if (FWD && k == max(t.u0, t.u1 - 2) && chunks) fetch(0);
         LtRing<NS> second = ring;
         second.next();
         const bool mine = turn == group;
@@ -465,24 +474,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
           ok = false;
           break;
         }
-        uint4 code[PIECES];
-        float2 dz[PIECES];
+        uint8_t* dst = smem + (FWD && q >= 2 ? second.i : ring.i) * Cfg::STAGE;
 #pragma unroll
-        for (int h = 0; h < PIECES; ++h) {
-          const int row = brow + 32 * h;
+        for (int h0 = 0; h0 < PIECES; h0 += 2) {
+        uint4 code[2];
+        float2 dz[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = brow + 32 * (h0 + h);
           code[h] = *reinterpret_cast<const uint4*>(codes + cring.i * Cfg::C_BYTES + row * 64 +
                                                     ((q ^ ((row >> 1) & 3)) << 4));
           dz[h] = grids[cring.i * (Cfg::G_BYTES / 8) + row];
-        }
-        uint8_t* dst = smem + (FWD && q >= 2 ? second.i : ring.i) * Cfg::STAGE;
-        // the partial that last used this slot of deltas has been taken out: its MMAs' successors,
-        // two partials on, have released the stages that were just waited for
-        if (FWD && q == 0) {
-#pragma unroll
-          for (int h = 0; h < PIECES; ++h) deltas[(pc % LT_DELTAS) * 128 + brow + 32 * h] = dz[h].x;
+          // the partial that last used this slot of deltas has been taken out: its MMAs' successors,
+          // two partials on, have released the stages that were just waited for
+          if (FWD && q == 0) deltas[(pc % LT_DELTAS) * 128 + row] = dz[h].x;
         }
 #pragma unroll
-        for (int h = 0; h < PIECES; ++h) {
+        for (int h = 0; h < 2; ++h) {
           const uint32_t zz = zero_pair<BF16>((int)dz[h].y);
           const uint32_t words[4] = {code[h].x, code[h].y, code[h].z, code[h].w};
           uint32_t hi2 = 0, lo2 = 0;
@@ -502,7 +510,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
               lo2 = *reinterpret_cast<const uint32_t*>(&b);
             }
           }
-          const int row = brow + 32 * h;
+          const int row = brow + 32 * (h0 + h);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t v[4];
@@ -530,6 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
                 make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
@@ -542,7 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         cring.next();
         ++pc;
       }
-      if (!FWD && chunks) fetch(0);   // (inside the loop its registers cost the backward units 5 %)
+      if (chunks) fetch(0);   // (inside the loop above its registers cost the units more than they gain)
       for (int q = 0; q < chunks && ok; ++q) {
         if (q % p.rank_chunks == 0) ++pc;
         uint32_t v[8];
@@ -577,10 +586,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * EBN;
     LtRing<ND> dr;
     uint32_t pc = 0;
-    bool ok = true, waited = false;
+    bool ok = true;
+    pdl_wait();   // the slots
     for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
       const LtTile t(p, i, BN, rank);
       const int f = t.f0 + r, tok = t.t0 + half * EBN;
+      // the tile's slots and this half's adapters are on their way while the base partials come in
+      const int32_t* slots = p.slots + t.nt * (BN + 1);
+      const int count = p.rank_chunks ? slots[0] : 0;
+      int ids[EBN / 32];
+#pragma unroll
+      for (int c = 0; c < EBN / 32; ++c)
+        ids[c] = count && tok + 32 * c + lane < p.T ? p.adapter[tok + 32 * c + lane] : -1;
       float acc[EBN];
 #pragma unroll
       for (int e = 0; e < EBN; ++e) acc[e] = 0.f;
@@ -626,23 +643,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         for (int u = t.u0; u < t.u1 && ok; ++u) take(true, nullptr);
       else
         take(false, nullptr);
-      if (p.rank_chunks && ok) {
-        if (!waited) pdl_wait();
-        waited = true;
-        const int32_t* slots = p.slots + t.nt * (BN + 1);
-        const int count = slots[0];
-        for (int s = 0; s < count && ok; ++s) {
-          const int a = slots[1 + s];
-          uint32_t mask[EBN / 32];
+      for (int s = 0; s < count && ok; ++s) {
+        const int a = slots[1 + s];
+        uint32_t mask[EBN / 32];
 #pragma unroll
-          for (int c = 0; c < EBN / 32; ++c) {
-            const int tt = tok + 32 * c + lane;
-            mask[c] = __ballot_sync(0xffffffffu, tt < p.T && p.adapter[tt] == a);
-          }
-          take(false, mask);
-        }
+        for (int c = 0; c < EBN / 32; ++c) mask[c] = __ballot_sync(0xffffffffu, ids[c] == a);
+        take(false, mask);
       }
-      if (!ok || f >= p.M) continue;
+      if (!ok) continue;
+      if (p.wide_out) {
+        // 16-bit rows that can be written four features at a time: two exchanges turn four tokens of one
+        // feature per lane into four features of one token (a 16-bit store per token and lane took 4 us
+        // of a tile's 38)
+        using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+        const bool odd = lane & 1, upper = lane & 2;
+        uint2* o = reinterpret_cast<uint2*>((T16*)p.out + (long long)(tok + (lane & 3)) * p.M + (f & ~3));
+        const long long step = p.M;   // four tokens on, in units of four values
+#pragma unroll
+        for (int e = 0; e < EBN; e += 4) {
+          const uint32_t p0 = pack16<BF16>(acc[e], acc[e + 1]), p1 = pack16<BF16>(acc[e + 2], acc[e + 3]);
+          const uint32_t o0 = __shfl_xor_sync(0xffffffffu, p0, 1), o1 = __shfl_xor_sync(0xffffffffu, p1, 1);
+          // features 2 k, 2 k + 1 of tokens e + odd and e + 2 + odd
+          const uint32_t w0 = odd ? __byte_perm(o0, p0, 0x7632) : __byte_perm(p0, o0, 0x5410);
+          const uint32_t w1 = odd ? __byte_perm(o1, p1, 0x7632) : __byte_perm(p1, o1, 0x5410);
+          const uint32_t r2 = __shfl_xor_sync(0xffffffffu, upper ? w0 : w1, 2);
+          if (tok + e + (lane & 3) < p.T && f < p.M) *o = upper ? make_uint2(r2, w1) : make_uint2(w0, r2);
+          o += step;
+        }
+        continue;
+      }
+      if (f >= p.M) continue;
       if (p.part) {
         float* o = p.part + ((long long)t.split * p.T + tok) * p.M + f;
 #pragma unroll
@@ -1166,6 +1196,7 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   p.slots = slots;
   p.out = out;
   p.out_f32 = out_f32;
+  p.wide_out = fused && !out_f32 && M % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 7) == 0;
   p.part = fused ? nullptr : part;
   p.idesc = tc::idesc_f32acc(bf ? 1u : 0u, !forward, false, 256, plan.BN);
   p.idesc_tf32 = tc::idesc_f32acc(2u, false, false, 256, plan.BN);
