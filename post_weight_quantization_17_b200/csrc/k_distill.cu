@@ -20,7 +20,7 @@ namespace gptq {
 
 constexpr int DS_THREADS = 256;
 constexpr int DS_WARPS = DS_THREADS / 32;
-constexpr int DS_PIECES = 4;                     // bulk copies (and barriers) of a CTA's part
+constexpr int DS_PIECES = 2;                     // bulk copies (and barriers) of a CTA's part
 constexpr int DS_PART = 64 * 1024;               // a CTA's part of a row, where rows allow it
 constexpr int DS_PART_MAX = 160 * 1024;
 constexpr float DS_LOG2E = 1.4426950408889634f, DS_LN2 = 0.6931471805599453f;
@@ -175,82 +175,101 @@ __device__ __forceinline__ void ds_join(float& m, float& s, float m2, float s2, 
   m = mm;
 }
 
-// The teacher's list of one row in shared memory, and what follows from it.
-struct DsList {
-  float *pk, *zk;
-  int32_t* ik;
-  float mass, cm, c;   // M, g w tau M, g w tau
-};
-
-// Reads the list (indices, the student's scaled logits there, the teacher's).  Without the teacher's
-// log-sum-exp the teacher's logits are taken relative to their largest, so that log p_k is a difference
-// of small numbers.  Returns L; every thread of the CTA.
-template <class T>
-__device__ __forceinline__ float ds_read_list(const DistillArgs& p, int t, const T* z, float it,
-                                              DsList& l, float* red, DeviceStatus* st) {
-  float most = -INFINITY;
-  bool bad = false;
-  for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
-    int i = p.indices[(long long)t * p.K + k];
-    if (i < -1 || i >= p.V) {
-      bad = true;
-      i = -1;
-    }
-    l.ik[k] = i;
-    l.pk[k] = i < 0 ? -INFINITY : p.values[(long long)t * p.K + k] * it;
-    l.zk[k] = i < 0 ? 0.f : to_f32<T>(z[i]) * it;
-    most = fmaxf(most, l.pk[k]);
+// The same over the eight warps' (m, s) in shared memory, or a cluster's: n, a power of two up to 8, of
+// them; every lane of the calling warp gets the result.
+__device__ __forceinline__ void ds_join_all(const float2* ms, int n, float& m, float& s, float k) {
+  const float2 v = ms[threadIdx.x & (n - 1)];
+  m = v.x;
+  s = v.y;
+  for (int o = n >> 1; o; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    ds_join(m, s, m2, s2, k);
   }
-  if (bad) raise_error(st, GPTQ_ERR_ARG, t);
-  float L;
-  if (p.teacher_lse) {
-    L = p.teacher_lse[t];
-  } else {
-    most = ds_block(most, true, red);
-    float s = 0.f;
-    for (int k = threadIdx.x; k < p.K; k += DS_THREADS)
-      if (l.pk[k] != -INFINITY) {
-        l.pk[k] -= most;
-        s += expf(l.pk[k]);
-      }
-    L = logf(ds_block(s, false, red));
-  }
-  return L;
 }
 
-// log p - log q summed over the list into *kl where asked for, the probabilities into l.pk and
-// their sum into l.mass.
-__device__ __forceinline__ void ds_finish_list(const DistillArgs& p, float L, float lse, DsList& l,
-                                               float* kl_out, float* red) {
-  float kl = 0.f, mass = 0.f;
-  for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
-    const float lp = l.pk[k] - L;
-    const float q = l.pk[k] == -INFINITY ? 0.f : expf(lp);
-    l.pk[k] = q;
-    mass += q;
-    if (q != 0.f) kl += q * (lp - (l.zk[k] - lse));
+// The teacher's list of one row in shared memory, and what follows from it.  log p_k is taken relative
+// to `base`, the teacher's log-sum-exp or, without one, its largest kept logit, so that it is a
+// difference of small numbers: log p_k = (v_k - base) - logs.
+struct DsList {
+  float *v, *z;   // the teacher's and the student's scaled logits
+  int32_t* i;
+  float base, logs, mass;   // mass: M
+  float cm, c;              // g w tau M, g w tau
+  __device__ __forceinline__ DsList(uint8_t* at, int K)
+      : v(reinterpret_cast<float*>(at)), z(v + K), i(reinterpret_cast<int32_t*>(z + K)) {}
+  __device__ __forceinline__ float logp(int k) const { return (v[k] - base) - logs; }
+  __device__ __forceinline__ float p(int k) const { return v[k] == -INFINITY ? 0.f : expf(logp(k)); }
+};
+
+// Reads the list; the warp's (base, sum of exp(v - base)) into part[warp].  Called by every thread;
+// warps behind the list's end do next to nothing.
+template <class T>
+__device__ __forceinline__ void ds_read_list(const DistillArgs& p, int t, const T* z, float it,
+                                             const DsList& l, float2* part, DeviceStatus* st) {
+  const bool given = p.teacher_lse != nullptr;
+  float most = given ? p.teacher_lse[t] : -INFINITY, s = 0.f;
+  if ((int)(threadIdx.x & ~31u) < p.K) {
+    bool bad = false;
+    for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
+      int i = p.indices[(long long)t * p.K + k];
+      if (i < -1 || i >= p.V) {
+        bad = true;
+        i = -1;
+      }
+      const float v = i < 0 ? -INFINITY : p.values[(long long)t * p.K + k] * it;
+      l.i[k] = i;
+      l.v[k] = v;
+      l.z[k] = i < 0 ? 0.f : to_f32<T>(z[i]) * it;
+      if (!given) most = fmaxf(most, v);
+    }
+    if (bad) raise_error(st, GPTQ_ERR_ARG, t);
+    if (!given) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    for (int k = threadIdx.x; k < p.K; k += DS_THREADS)
+      if (l.v[k] != -INFINITY) s += expf(l.v[k] - most);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   }
-  l.mass = ds_block(mass, false, red);
-  if (kl_out) *kl_out = ds_block(kl, false, red);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(most, s);
+}
+// After a barrier.  (Without the teacher's log-sum-exp the p_k sum to one.)
+__device__ __forceinline__ void ds_join_list(const DistillArgs& p, DsList& l, const float2* part) {
+  float s;
+  ds_join_all(part, DS_WARPS, l.base, s, DS_LOG2E);
+  l.logs = p.teacher_lse ? 0.f : logf(s);
+  l.mass = p.teacher_lse || !(s > 0.f) ? s : 1.f;
+}
+// The loss of the row, by warp 0.
+__device__ __forceinline__ float ds_loss(const DistillArgs& p, const DsList& l, float lse) {
+  float kl = 0.f;
+  for (int k = threadIdx.x; k < p.K; k += 32) {
+    const float q = l.p(k);
+    if (q != 0.f) kl += q * (l.logp(k) - (l.z[k] - lse));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) kl += __shfl_xor_sync(0xffffffffu, kl, o);
+  return kl;
 }
 
 // The gradient at the listed entries inside [lo, hi), over what the dense pass wrote there: the
-// first listing of an index writes the sum of all its listings, rounded once.  After a
-// __syncthreads that follows the dense pass.
+// first listing of an index writes the sum of all its listings, rounded once.  After a barrier that
+// follows the dense pass.
 template <class T>
 __device__ __forceinline__ void ds_listed(const DistillArgs& p, T* dz, const DsList& l, float lse,
                                           long long lo, long long hi) {
   for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
-    const int i = l.ik[k];
+    const int i = l.i[k];
     if (i < lo || i >= hi) continue;
     bool first = true;
     float sum = 0.f;
     for (int j = 0; j < p.K; ++j)
-      if (l.ik[j] == i) {
+      if (l.i[j] == i) {
         first = first && j >= k;
-        sum += l.pk[j];
+        sum += l.p(j);
       }
-    if (first) dz[i] = ds_round<T>(fmaf(l.cm, ds_exp2((l.zk[k] - lse) * DS_LOG2E), -l.c * sum));
+    if (first) dz[i] = ds_round<T>(fmaf(l.cm, ds_exp2((l.z[k] - lse) * DS_LOG2E), -l.c * sum));
   }
 }
 
@@ -262,18 +281,15 @@ __device__ __forceinline__ void ds_store_remote(uint32_t addr, float v) {
 // formed (else lse is given); GRAD: the gradient is written.
 template <class T, bool LOSS, bool GRAD>
 __global__ void __launch_bounds__(DS_THREADS)
-    k_distill(DistillArgs p, int part, DeviceStatus* st, long long budget) {
+    k_distill(DistillArgs p, int part, int log2c, DeviceStatus* st, long long budget) {
   constexpr int N = DsVec<T>::N;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar[DS_PIECES];
-  __shared__ float red[33], joined[2 * 8];
+  __shared__ float2 row_part[DS_WARPS], list_part[DS_WARPS], joined[8];
   uint4* row = reinterpret_cast<uint4*>(smem);
-  DsList l;
-  l.pk = reinterpret_cast<float*>(smem + (size_t)part * 16);
-  l.zk = l.pk + p.K;
-  l.ik = reinterpret_cast<int32_t*>(l.zk + p.K);
-  const int C = (int)(gridDim.x / p.T);
-  const int t = blockIdx.x / C, rank = blockIdx.x % C;
+  DsList l(smem + (size_t)part * 16, p.K);
+  const int C = 1 << log2c;
+  const int t = blockIdx.x >> log2c, rank = blockIdx.x & (C - 1);
   const T* z = (const T*)p.logits + (long long)t * p.ld;
   T* dz = GRAD ? (T*)p.dlogits + (long long)t * p.ld_grad : nullptr;
   // the row as `head` scalars, nvec aligned vectors and `tail` scalars
@@ -323,7 +339,7 @@ __global__ void __launch_bounds__(DS_THREADS)
       edge = tail0 + threadIdx.x - 16;
   }
   const float edge_z = edge >= 0 ? to_f32<T>(z[edge]) : -INFINITY;
-  const float L = ds_read_list<T>(p, t, z, it, l, red, st);
+  ds_read_list<T>(p, t, z, it, l, list_part, st);
   float lse;
   if (LOSS) {
     float m = edge_z, s = edge_z == -INFINITY ? 0.f : 1.f;
@@ -366,36 +382,32 @@ __global__ void __launch_bounds__(DS_THREADS)
       const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
       ds_join(m, s, m2, s2, k2);
     }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
-      red[2 * (threadIdx.x >> 5)] = m;
-      red[2 * (threadIdx.x >> 5) + 1] = s;
-    }
-    __syncthreads();
-    m = red[0];
-    s = red[1];
-#pragma unroll
-    for (int i = 1; i < DS_WARPS; ++i) ds_join(m, s, red[2 * i], red[2 * i + 1], k2);
+    if ((threadIdx.x & 31) == 0) row_part[threadIdx.x >> 5] = make_float2(m, s);
+    __syncthreads();   // also: the list
+    ds_join_all(row_part, DS_WARPS, m, s, k2);
     if (C > 1) {
       asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every CTA has started
       if ((int)threadIdx.x < C) {
-        ds_store_remote(tc::map_to_rank(&joined[2 * rank], threadIdx.x), m);
-        ds_store_remote(tc::map_to_rank(&joined[2 * rank + 1], threadIdx.x), s);
+        const uint32_t to = tc::map_to_rank(&joined[rank], threadIdx.x);
+        ds_store_remote(to, m);
+        ds_store_remote(to + 4, s);
       }
       tc::cluster_sync();   // also: every listed logit was read before any gradient is written
-      m = joined[0];
-      s = joined[1];
-      for (int i = 1; i < C; ++i) ds_join(m, s, joined[2 * i], joined[2 * i + 1], k2);
+      ds_join_all(joined, C, m, s, k2);
     }
     lse = fmaf(m, it, logf(s));
   } else {
     lse = p.lse_in[t];
+    __syncthreads();   // the list
   }
-  float kl;
-  ds_finish_list(p, L, lse, l, LOSS ? &kl : nullptr, red);
-  if (LOSS && rank == 0 && threadIdx.x == 0) {
-    p.loss[t] = w * p.tau * p.tau * kl;
-    p.lse_out[t] = lse;
+  ds_join_list(p, l, list_part);
+  if (LOSS && !GRAD && rank) return;
+  if (LOSS && rank == 0 && threadIdx.x < 32) {
+    const float kl = ds_loss(p, l, lse);
+    if (threadIdx.x == 0) {
+      p.loss[t] = w * p.tau * p.tau * kl;
+      p.lse_out[t] = lse;
+    }
   }
   if (!GRAD) return;
   l.c = p.dloss[t] * w * p.tau;
@@ -428,35 +440,43 @@ __global__ void __launch_bounds__(DS_THREADS)
       }
     }
   }
-  // The listed entries of this CTA's own part, over what was just written there.  Their slots in
-  // the row's shared memory, no longer needed, find indices that are listed twice: every listing
-  // leaves its number, one of each index's listings finds its own again and writes the sum over
-  // all of them (in list order, whichever listing it is).
-  __syncthreads();
+  // The listed entries of this CTA's own part, over what was just written there, by the warps that
+  // the list reaches.  Their slots in the row's shared memory, no longer needed, find indices that
+  // are listed twice: every listing leaves its number, one of each index's listings finds its own
+  // again and writes the sum over all of them (in list order, whichever listing it is).
+  const int listers = min(DS_THREADS, (p.K + 31) & ~31);
+  if ((int)threadIdx.x >= listers) {
+    asm volatile("bar.arrive 1, %0;" ::"n"(DS_THREADS) : "memory");
+    return;
+  }
+  asm volatile("bar.sync 1, %0;" ::"n"(DS_THREADS) : "memory");
+  auto sync = [&] { asm volatile("bar.sync 2, %0;" ::"r"(listers) : "memory"); };
   const int lo = head + v0 * N, hi = lo + nv * N;
   uint16_t* tag = reinterpret_cast<uint16_t*>(row);
   constexpr int TS = sizeof(T) / 2;
   for (int k = threadIdx.x; k < p.K; k += DS_THREADS)
-    if (l.ik[k] >= lo && l.ik[k] < hi) tag[(l.ik[k] - lo) * TS] = (uint16_t)k;
-  __syncthreads();
+    if (l.i[k] >= lo && l.i[k] < hi) tag[(l.i[k] - lo) * TS] = (uint16_t)k;
+  sync();
   constexpr int kTwice = 1 << 30;
   for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
-    const int i = l.ik[k] & ~kTwice;
-    if (l.ik[k] < 0 || i < lo || i >= hi) continue;
+    const int i = l.i[k] & ~kTwice;
+    if (l.i[k] < 0 || i < lo || i >= hi) continue;
     const int winner = tag[(i - lo) * TS];
-    if (winner != k) atomicOr(&l.ik[winner], kTwice);
+    if (winner != k) atomicOr(&l.i[winner], kTwice);
   }
-  __syncthreads();
+  sync();
   for (int k = threadIdx.x; k < p.K; k += DS_THREADS) {
-    const int i = l.ik[k] & ~kTwice;
-    if (l.ik[k] < 0 || i < lo || i >= hi || tag[(i - lo) * TS] != k) continue;
-    float sum = l.pk[k];
-    if (l.ik[k] & kTwice) {
+    const int i = l.i[k] & ~kTwice;
+    if (l.i[k] < 0 || i < lo || i >= hi || tag[(i - lo) * TS] != k) continue;
+    float sum;
+    if (l.i[k] & kTwice) {
       sum = 0.f;
       for (int j = 0; j < p.K; ++j)
-        if (l.ik[j] >= 0 && (l.ik[j] & ~kTwice) == i) sum += l.pk[j];
+        if (l.i[j] >= 0 && (l.i[j] & ~kTwice) == i) sum += l.p(j);
+    } else {
+      sum = l.p(k);
     }
-    dz[i] = ds_round<T>(fmaf(l.cm, ds_exp2((l.zk[k] - lse) * DS_LOG2E), -l.c * sum));
+    dz[i] = ds_round<T>(fmaf(l.cm, ds_exp2((l.z[k] - lse) * DS_LOG2E), -l.c * sum));
   }
   if (rank == 0) {   // the row's ends
     ds_listed<T>(p, dz, l, lse, 0, head);
@@ -471,10 +491,8 @@ __global__ void __launch_bounds__(DS_THREADS) k_distill_long(DistillArgs p, Devi
   pdl_release();
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[33];
-  DsList l;
-  l.pk = reinterpret_cast<float*>(smem);
-  l.zk = l.pk + p.K;
-  l.ik = reinterpret_cast<int32_t*>(l.zk + p.K);
+  __shared__ float2 list_part[DS_WARPS];
+  DsList l(smem, p.K);
   const int t = blockIdx.x;
   const T* z = (const T*)p.logits + (long long)t * p.ld;
   const float w = p.weight ? p.weight[t] : 1.f;
@@ -489,7 +507,7 @@ __global__ void __launch_bounds__(DS_THREADS) k_distill_long(DistillArgs p, Devi
     return;
   }
   const float it = 1.f / p.tau, k2 = it * DS_LOG2E;
-  const float L = ds_read_list<T>(p, t, z, it, l, red, st);
+  ds_read_list<T>(p, t, z, it, l, list_part, st);
   float lse;
   if (p.lse_in) {
     lse = p.lse_in[t];
@@ -497,16 +515,19 @@ __global__ void __launch_bounds__(DS_THREADS) k_distill_long(DistillArgs p, Devi
     float mx = -INFINITY;
     for (int i = threadIdx.x; i < p.V; i += DS_THREADS) mx = fmaxf(mx, to_f32<T>(z[i]));
     mx = ds_block(mx, true, red);
+    const float mk = mx == -INFINITY ? 0.f : mx * k2;
     float s = 0.f;
-    for (int i = threadIdx.x; i < p.V; i += DS_THREADS)
-      s += ds_exp2(fmaf(to_f32<T>(z[i]), k2, -mx * k2));
+    for (int i = threadIdx.x; i < p.V; i += DS_THREADS) s += ds_exp2(fmaf(to_f32<T>(z[i]), k2, -mk));
     lse = fmaf(mx, it, logf(ds_block(s, false, red)));
   }
-  float kl;
-  ds_finish_list(p, L, lse, l, &kl, red);
-  if (p.loss && threadIdx.x == 0) {
-    p.loss[t] = w * p.tau * p.tau * kl;
-    p.lse_out[t] = lse;
+  __syncthreads();   // the list; every listed logit was read before any gradient is written
+  ds_join_list(p, l, list_part);
+  if (p.loss && threadIdx.x < 32) {
+    const float kl = ds_loss(p, l, lse);
+    if (threadIdx.x == 0) {
+      p.loss[t] = w * p.tau * p.tau * kl;
+      p.lse_out[t] = lse;
+    }
   }
   if (!dz) return;
   l.c = p.dloss[t] * w * p.tau;
@@ -520,12 +541,12 @@ __global__ void __launch_bounds__(DS_THREADS) k_distill_long(DistillArgs p, Devi
 namespace {
 
 template <class T, bool LOSS, bool GRAD>
-int launch_distill(Ctx* c, const DistillArgs& p, int C, int part, size_t smem) {
+int launch_distill(Ctx* c, const DistillArgs& p, int log2c, int part, size_t smem) {
   GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(k_distill<T, LOSS, GRAD>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, LOSS ? C : 1, k_distill<T, LOSS, GRAD>,
-                                        dim3((unsigned)(p.T * C)), dim3(DS_THREADS), smem, p, part,
-                                        c->status, c->timeout_cycles));
+  GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, LOSS ? 1 << log2c : 1, k_distill<T, LOSS, GRAD>,
+                                        dim3((unsigned)p.T << log2c), dim3(DS_THREADS), smem, p,
+                                        part, log2c, c->status, c->timeout_cycles));
   return GPTQ_OK;
 }
 
@@ -535,18 +556,19 @@ int distill_as(Ctx* c, const DistillArgs& p) {
   const long long nvec = std::max<long long>(1, (long long)p.V / DsVec<T>::N);
   // CTAs per row: parts of at most DS_PART bytes; with few rows more, down to 8 KB parts, so that
   // the SMs share the work (the loss of 5 rows of 32000 fp32 logits: {SMALL}).
-  int C = 1;
-  while (C < 8 && nvec * 16 > (long long)C * DS_PART) C *= 2;
-  while (C < 8 && (long long)p.T * C * 2 <= c->num_sms && nvec * 16 > (long long)C * 8192) C *= 2;
-  const long long part = (nvec + C - 1) / C;
-  if (part * 16 > DS_PART_MAX || (long long)p.T * C > INT32_MAX) {
+  int log2c = 0;
+  while (log2c < 3 && (nvec * 16 > (long long)DS_PART << log2c ||
+                       (((long long)p.T << log2c) * 2 <= c->num_sms && nvec * 16 > 8192LL << log2c)))
+    ++log2c;
+  const long long part = (nvec + (1 << log2c) - 1) >> log2c;
+  if (part * 16 > DS_PART_MAX || ((long long)p.T << log2c) > INT32_MAX) {
     GPTQ_LAUNCH(c, k_distill_long<T>, p.T, DS_THREADS, list, p, c->status);
     return GPTQ_OK;
   }
   const size_t smem = (size_t)part * 16 + list;
-  if (!p.loss) return launch_distill<T, false, true>(c, p, C, (int)part, smem);
-  if (!p.dlogits) return launch_distill<T, true, false>(c, p, C, (int)part, smem);
-  return launch_distill<T, true, true>(c, p, C, (int)part, smem);
+  if (!p.loss) return launch_distill<T, false, true>(c, p, log2c, (int)part, smem);
+  if (!p.dlogits) return launch_distill<T, true, false>(c, p, log2c, (int)part, smem);
+  return launch_distill<T, true, true>(c, p, log2c, (int)part, smem);
 }
 
 }  // namespace
