@@ -11,7 +11,7 @@
 // formed in one pass, the cluster joins them through distributed shared memory, and the gradient is
 // formed from the same shared memory.  Several CTAs per SM let one load while another computes (a copy
 // in two or four parts, each waited for by itself, was slower: the list, the barriers and the joins are
-// what a row costs beyond its elements).  4096 x 128000 bf16 with the gradient: 429 us, 75 % of the copy
+// what a row costs beyond its elements).  4096 x 128000 bf16 with the gradient: 416 us, 77 % of the copy
 // rate; 32 KB parts 460.
 // Rows too long for 8 CTAs' shared memory take k_distill_long, which reads them again instead.
 #include <algorithm>
@@ -282,7 +282,7 @@ __device__ __forceinline__ void ds_store_remote(uint32_t addr, float v) {
 // One cluster per token; `part`: 16-byte vectors of the row per CTA.  LOSS: the loss and lse are
 // formed (else lse is given); GRAD: the gradient is written.
 template <class T, bool LOSS, bool GRAD>
-__global__ void __launch_bounds__(DS_THREADS)
+__global__ void __launch_bounds__(DS_THREADS, 3)
     k_distill(DistillArgs p, int part, int log2c, DeviceStatus* st, long long budget) {
   constexpr int N = DsVec<T>::N;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(DS_THREADS)
 #pragma unroll
     for (int e = 0; e < N; e += 2) ds_split(ds_mul2(ds_pair(x[e], x[e + 1]), cc), x[e], x[e + 1]);
     if (wide) {
-      __stcs(reinterpret_cast<uint4*>(out) + i, ds_pack<T>(x));
+      reinterpret_cast<uint4*>(out)[i] = ds_pack<T>(x);
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) out[(long long)i * N + e] = ds_round<T>(x[e]);
