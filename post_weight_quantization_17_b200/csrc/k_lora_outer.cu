@@ -77,8 +77,10 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
   const int f0 = fb + wf * 64, j0 = blockIdx.y * LO_RANKS, f = f0 + 8 * g;
   // the tokens' adapters (0xFFFF: none), and which adapters have tokens
   uint32_t* present = reinterpret_cast<uint32_t*>(total + LO_RANKS * LO_FEATS);
-  uint16_t* id_of = reinterpret_cast<uint16_t*>(present + (p.n + 31) / 32);
+  uint16_t* id_of = reinterpret_cast<uint16_t*>(present + (p.n + 127) / 128 * 4);
   for (int i = threadIdx.x; i < (p.n + 31) / 32; i += LO_THREADS) present[i] = 0;
+  const int groups = (p.T + 7) / 8;
+  if ((int)threadIdx.x < 8 * groups - p.T) id_of[p.T + threadIdx.x] = 0xFFFF;   // behind the last token
   __syncthreads();
   for (int t = threadIdx.x; t < p.T; t += 8 * LO_THREADS) {
     int id[8];
@@ -104,16 +106,32 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
     continue;
   }
   float acc[8][4] = {};
-  // this warp's groups: rank * 4 + wt, and every `stride`-th from there, taken in pairs
-  const int groups = (p.T + 7) / 8, stride = 4 * cl;
-  // the next pair at or behind i that has a token of the adapter (its members, and i), from shared memory
+  // this warp's groups: rank * 4 + wt, and every `stride`-th from there, taken in pairs.  `word`: which of
+  // 32 pairs, a lane looking at one pair's 16 adapters, have a token of this adapter and are still to come
+  // (looking at one pair after the other cost a fourth of the instructions with four adapters).
+  const int stride = 4 * cl, start = rank * 4 + wt;
+  const uint32_t aa = (uint32_t)a * 0x10001u;
+  int next = start;
+  uint32_t word = 0;
+  // the next pair with a token of the adapter: its members, and its first group i
   auto find = [&](int& i) -> uint32_t {
-    for (; i < groups; i += 2 * stride) {
-      const int t = (i + ((lane >> 3) & 1) * stride) * 8 + (lane & 7);
-      const uint32_t m = __ballot_sync(0xffffffffu, lane < 16 && t < p.T && id_of[t] == a);
-      if (m) return m;
+    while (!word) {
+      if (next >= groups) return 0u;
+      const int mine = next + lane * 2 * stride;
+      uint32_t hit = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (mine + k * stride < groups) {
+          const uint4 v = *reinterpret_cast<const uint4*>(id_of + (mine + k * stride) * 8);
+          hit |= __vcmpeq2(v.x, aa) | __vcmpeq2(v.y, aa) | __vcmpeq2(v.z, aa) | __vcmpeq2(v.w, aa);
+        }
+      word = __ballot_sync(0xffffffffu, hit != 0);
+      next += 64 * stride;
     }
-    return 0u;
+    i = next + (__ffs(word) - 33) * 2 * stride;
+    word &= word - 1;
+    const int of = i + ((lane >> 3) & 1) * stride;
+    return __ballot_sync(0xffffffffu, lane < 16 && of < groups && id_of[of * 8 + (lane & 7)] == a);
   };
   auto fetch = [&](OuterGroup& o, int i, uint32_t members) {
     o.members = members;
@@ -165,28 +183,32 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
         hi[e] = __float_as_uint(h);
         lo[e] = finite ? __float_as_uint(tc::tf32_rna(v - h)) : 0u;
       }
+      // all the high parts, then all the low ones: eight products lie between two of one sum
+      float2 b0[4], b1[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 b0 = pair_f32<BF16>(x0[e]), b1 = pair_f32<BF16>(x1[e]);
-        mma_tf32_1688(acc[2 * e], hi, __float_as_uint(b0.x), __float_as_uint(b1.x));
-        mma_tf32_1688(acc[2 * e + 1], hi, __float_as_uint(b0.y), __float_as_uint(b1.y));
-        mma_tf32_1688(acc[2 * e], lo, __float_as_uint(b0.x), __float_as_uint(b1.x));
-        mma_tf32_1688(acc[2 * e + 1], lo, __float_as_uint(b0.y), __float_as_uint(b1.y));
+        b0[e] = pair_f32<BF16>(x0[e]);
+        b1[e] = pair_f32<BF16>(x1[e]);
+        mma_tf32_1688(acc[2 * e], hi, __float_as_uint(b0[e].x), __float_as_uint(b1[e].x));
+        mma_tf32_1688(acc[2 * e + 1], hi, __float_as_uint(b0[e].y), __float_as_uint(b1[e].y));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        mma_tf32_1688(acc[2 * e], lo, __float_as_uint(b0[e].x), __float_as_uint(b1[e].x));
+        mma_tf32_1688(acc[2 * e + 1], lo, __float_as_uint(b0[e].y), __float_as_uint(b1[e].y));
       }
     }
   };
   {
-    int i = rank * 4 + wt;
+    int i = 0;
     OuterGroup one, other;
     uint32_t m = find(i);
     fetch(one, i, m);
     while (one.members) {
-      i += 2 * stride;
       m = find(i);
       fetch(other, i, m);
       multiply(one);
       if (!m) break;
-      i += 2 * stride;
       m = find(i);
       fetch(one, i, m);
       multiply(other);
@@ -265,8 +287,8 @@ int lora_outers(Ctx* c, const LoraLayer& l, const float* G, const void* X, float
     p.two[0] = problem(G, X, dA, l.d);
     p.two[1] = problem(U, dY, dB, l.m);
     p.first_ctas = ca;
-    const dim3 grid(ca + cb, ranks, std::max(1, std::min(l.n, 4 * c->num_sms / ((ca + cb) * ranks))));
-    const int smem = LO_SMEM + (l.n + 31) / 32 * 4 + (p.T + 1) / 2 * 4;
+    const dim3 grid(ca + cb, ranks, std::max(1, std::min(l.n, 8 * c->num_sms / ((ca + cb) * ranks))));
+    const int smem = LO_SMEM + (l.n + 127) / 128 * 16 + (p.T + 7) / 8 * 16;
     GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, p.cluster, kernel, grid, dim3(LO_THREADS), smem, p,
                                           c->status));
