@@ -798,8 +798,9 @@ __device__ __forceinline__ void list_slots(const ShrinkParams& p, int nt) {
   if (tid == 0) out[0] = total;
 }
 
-// NTL: 8-rank tiles of a pass (16 or 32 ranks); MT: 16-token tiles of a CTA (two halve the reads of A
-// where there are tokens enough for every SM)
+// NTL: 8-rank tiles of a pass; MT: 16-token tiles of a CTA (two halve the reads of A where there are tokens
+// enough for every SM).  At rank 64, d = 4096, 64 ranks in one pass took 22 us for 1024 tokens, 32 in two
+// 26; with two tiles the registers do not hold it (4096 tokens: 58 us, 45 in two passes).
 template <bool BF16, int NTL, int MT>
 __global__ void __launch_bounds__(LU_THREADS, 1) k_lora_shrink(ShrinkParams p, DeviceStatus* st) {
   pdl_wait();
@@ -845,7 +846,7 @@ __global__ void __launch_bounds__(LU_THREADS, 1) k_lora_shrink(ShrinkParams p, D
 #pragma unroll
       for (int nt = 0; nt < NTL; ++nt)
         w[nt] = (const uint16_t*)p.w + ((long long)a * p.R + min(j0 + 8 * nt + g, p.R - 1)) * p.F + 8 * t4;
-      constexpr int H = MT == 1 ? 4 : 2;   // pieces of 32 features loaded at once
+      constexpr int H = MT == 1 && NTL < 8 ? 4 : 2;   // pieces of 32 features loaded at once
       for (int k0 = s0 * 64; k0 < s1 * 64; k0 += 32 * H) {
         uint4 xv[H][2 * MT], wv[H][NTL];
         if (k0 + 32 * H <= min(s1 * 64, p.F)) {
@@ -1155,7 +1156,8 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
     auto pick = [&](auto bf16) {
       constexpr bool B = decltype(bf16)::value;
       if (l.R <= 16) return mt == 1 ? k_lora_shrink<B, 2, 1> : k_lora_shrink<B, 2, 2>;
-      return mt == 1 ? k_lora_shrink<B, 4, 1> : k_lora_shrink<B, 4, 2>;
+      if (mt == 2) return k_lora_shrink<B, 4, 2>;
+      return l.R <= 32 ? k_lora_shrink<B, 4, 1> : k_lora_shrink<B, 8, 1>;
     };
     auto kernel = bf ? pick(std::true_type{}) : pick(std::false_type{});
     GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, s.cluster, kernel, dim3(grid), dim3(LU_THREADS), 0, s,
