@@ -35,6 +35,11 @@
 // into the weight warps' registers, though issued two to four stages ahead, took as long as the
 // whole stage (0.74 us of 256 tokens; without them 0.45).
 // Few tokens: the contraction is split over CTAs and k_lora_join adds the splits and the adapter.
+//
+// 4096 tokens, 11008 x 4096, rank 64, forward: 355 us (1.04 PFLOP/s of 1.67 measured); 4096 x 11008, rank
+// 32, backward: 323 us (1.14).  Both run at the power limit.  Of the forward's 375 us before its rows
+// were written four features at a time, the adapters' partial sums were 48 us, the output 40, the fp32
+// additions of the base partials 40.
 #include <algorithm>
 #include <type_traits>
 
@@ -62,7 +67,7 @@ struct LtCfg {
 };
 
 struct LtParams {
-  int M, K;                 // features out, contraction length
+  int M;                    // features out
   int T;
   int group_steps;          // groups in 128-column steps; 0: one grid per row
   const float2* grid;       // [n_g, m_pad] (Δ, z), zero behind m
@@ -477,67 +482,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         uint8_t* dst = smem + (FWD && q >= 2 ? second.i : ring.i) * Cfg::STAGE;
 #pragma unroll
         for (int h0 = 0; h0 < PIECES; h0 += 2) {
-        uint4 code[2];
-        float2 dz[2];
+          uint4 code[2];
+          float2 dz[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = brow + 32 * (h0 + h);
-          code[h] = *reinterpret_cast<const uint4*>(codes + cring.i * Cfg::C_BYTES + row * 64 +
-                                                    ((q ^ ((row >> 1) & 3)) << 4));
-          dz[h] = grids[cring.i * (Cfg::G_BYTES / 8) + row];
-          // the partial that last used this slot of deltas has been taken out: its MMAs' successors,
-          // two partials on, have released the stages that were just waited for
-          if (FWD && q == 0) deltas[(pc % LT_DELTAS) * 128 + row] = dz[h].x;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t zz = zero_pair<BF16>((int)dz[h].y);
-          const uint32_t words[4] = {code[h].x, code[h].y, code[h].z, code[h].w};
-          uint32_t hi2 = 0, lo2 = 0;
-          if (!FWD) {
-            if (BF16) {
-              const __nv_bfloat16 hi = __float2bfloat16_rn(dz[h].x);
-              const __nv_bfloat16 lo = __float2bfloat16_rn(dz[h].x - __bfloat162float(hi));
-              const __nv_bfloat162 a = __halves2bfloat162(hi, hi), b = __halves2bfloat162(lo, lo);
-              hi2 = *reinterpret_cast<const uint32_t*>(&a);
-              lo2 = *reinterpret_cast<const uint32_t*>(&b);
-            } else {
-              const float ds = dz[h].x * LT_F16_SCALE;
-              const __half hi = __float2half_rn(ds);
-              const __half lo = __float2half_rn(ds - __half2float(hi));
-              const __half2 a = __halves2half2(hi, hi), b = __halves2half2(lo, lo);
-              hi2 = *reinterpret_cast<const uint32_t*>(&a);
-              lo2 = *reinterpret_cast<const uint32_t*>(&b);
-            }
+          for (int h = 0; h < 2; ++h) {
+            const int row = brow + 32 * (h0 + h);
+            code[h] = *reinterpret_cast<const uint4*>(codes + cring.i * Cfg::C_BYTES + row * 64 +
+                                                      ((q ^ ((row >> 1) & 3)) << 4));
+            dz[h] = grids[cring.i * (Cfg::G_BYTES / 8) + row];
+            // the partial that last used this slot of deltas has been taken out: its MMAs' successors,
+            // two partials on, have released the stages that were just waited for
+            if (FWD && q == 0) deltas[(pc % LT_DELTAS) * 128 + row] = dz[h].x;
           }
-          const int row = brow + 32 * (h0 + h);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t v[4];
-            centered8<BF16>(words[w], zz, v);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t zz = zero_pair<BF16>((int)dz[h].y);
+            const uint32_t words[4] = {code[h].x, code[h].y, code[h].z, code[h].w};
+            uint32_t hi2 = 0, lo2 = 0;
             if (!FWD) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (BF16) {
-                  const __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&v[e]);
-                  const __nv_bfloat162 r =
-                      __hfma2(c, *reinterpret_cast<const __nv_bfloat162*>(&hi2),
-                              __hmul2(c, *reinterpret_cast<const __nv_bfloat162*>(&lo2)));
-                  v[e] = *reinterpret_cast<const uint32_t*>(&r);
-                } else {
-                  const __half2 c = *reinterpret_cast<const __half2*>(&v[e]);
-                  const __half2 r = __hfma2(c, *reinterpret_cast<const __half2*>(&hi2),
-                                            __hmul2(c, *reinterpret_cast<const __half2*>(&lo2)));
-                  v[e] = *reinterpret_cast<const uint32_t*>(&r);
-                }
+              if (BF16) {
+                const __nv_bfloat16 hi = __float2bfloat16_rn(dz[h].x);
+                const __nv_bfloat16 lo = __float2bfloat16_rn(dz[h].x - __bfloat162float(hi));
+                const __nv_bfloat162 a = __halves2bfloat162(hi, hi), b = __halves2bfloat162(lo, lo);
+                hi2 = *reinterpret_cast<const uint32_t*>(&a);
+                lo2 = *reinterpret_cast<const uint32_t*>(&b);
+              } else {
+                const float ds = dz[h].x * LT_F16_SCALE;
+                const __half hi = __float2half_rn(ds);
+                const __half lo = __float2half_rn(ds - __half2float(hi));
+                const __half2 a = __halves2half2(hi, hi), b = __halves2half2(lo, lo);
+                hi2 = *reinterpret_cast<const uint32_t*>(&a);
+                lo2 = *reinterpret_cast<const uint32_t*>(&b);
               }
             }
-            const int chunk = 4 * (q & 1) + w;
-            *reinterpret_cast<uint4*>(dst + (FWD ? 0 : (q >> 1) * 8192) + row * 128 +
-                                      ((chunk ^ (row & 7)) << 4)) =
-                make_uint4(v[0], v[1], v[2], v[3]);
+            const int row = brow + 32 * (h0 + h);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              uint32_t v[4];
+              centered8<BF16>(words[w], zz, v);
+              if (!FWD) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (BF16) {
+                    const __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&v[e]);
+                    const __nv_bfloat162 r =
+                        __hfma2(c, *reinterpret_cast<const __nv_bfloat162*>(&hi2),
+                                __hmul2(c, *reinterpret_cast<const __nv_bfloat162*>(&lo2)));
+                    v[e] = *reinterpret_cast<const uint32_t*>(&r);
+                  } else {
+                    const __half2 c = *reinterpret_cast<const __half2*>(&v[e]);
+                    const __half2 r = __hfma2(c, *reinterpret_cast<const __half2*>(&hi2),
+                                              __hmul2(c, *reinterpret_cast<const __half2*>(&lo2)));
+                    v[e] = *reinterpret_cast<const uint32_t*>(&r);
+                  }
+                }
+              }
+              const int chunk = 4 * (q & 1) + w;
+              *reinterpret_cast<uint4*>(dst + (FWD ? 0 : (q >> 1) * 8192) + row * 128 +
+                                        ((chunk ^ (row & 7)) << 4)) =
+                  make_uint4(v[0], v[1], v[2], v[3]);
+            }
           }
-        }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -1179,7 +1184,7 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
               forward ? 128 : 64, 64))
     GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "lora: tensor map failed");
   LtParams p{};
-  p.M = M; p.K = K;
+  p.M = M;
   p.T = l.T;
   p.group_steps = l.group == -1 ? 0 : l.group / 128;
   p.grid = grid2;
