@@ -23,6 +23,7 @@ constexpr int LO_THREADS = 256;
 constexpr int LO_FEATS = 128, LO_PAD = 68;
 constexpr int LO_TOKENS = 8192;   // of a launch: their adapters (16 bits each) are kept in shared memory
 constexpr int LO_RANKS = 16;
+constexpr int LO_RUN = 8;       // pairs of token groups (16 tokens) that the tensor cores add up by themselves
 // the warps' sums [8][16][64 + 4] and the CTA's [16][128]; the adapters' bits and the tokens' adapters
 // follow
 constexpr int LO_SMEM = (8 * LO_RANKS * LO_PAD + LO_RANKS * LO_FEATS) * 4;
@@ -199,8 +200,30 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
       }
     }
   };
+  // The tensor cores' own additions round towards zero, so that a long run of them drifts (2.4e-6 of dA
+  // after 36 pairs); LO_RUN pairs on, the sums go to the warp's place in shared memory, by IEEE additions.
+  // Tile i's column n is feature 8 n + i: a lane holds features 16 t4 + (0..7) and + 8.
+  float* mine = sums + warp * LO_RANKS * LO_PAD;
+  bool fresh = true;
+  auto flush = [&] {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float4* dst = reinterpret_cast<float4*>(mine + (2 * g + (c >> 1)) * LO_PAD + 16 * t4 + 8 * (c & 1));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 v = fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : dst[h];
+        dst[h] = make_float4(v.x + acc[4 * h][c], v.y + acc[4 * h + 1][c], v.z + acc[4 * h + 2][c],
+                             v.w + acc[4 * h + 3][c]);
+      }
+    }
+    fresh = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
+  };
   {
-    int i = 0;
+    int i = 0, run = 0;
     OuterGroup one, other;
     uint32_t m = find(i);
     fetch(one, i, m);
@@ -212,16 +235,13 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
       m = find(i);
       fetch(one, i, m);
       multiply(other);
+      if ((run += 2) == LO_RUN) {
+        flush();
+        run = 0;
+      }
     }
   }
-  // tile i's column n is feature 8 n + i: a lane holds features 16 t4 + (0..7) and + 8
-  float* mine = sums + warp * LO_RANKS * LO_PAD;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float4* dst = reinterpret_cast<float4*>(mine + (2 * g + (c >> 1)) * LO_PAD + 16 * t4 + 8 * (c & 1));
-    dst[0] = make_float4(acc[0][c], acc[1][c], acc[2][c], acc[3][c]);
-    dst[1] = make_float4(acc[4][c], acc[5][c], acc[6][c], acc[7][c]);
-  }
+  flush();
   __syncthreads();
   for (int e = threadIdx.x; e < LO_RANKS * LO_FEATS; e += LO_THREADS) {
     const int j = e / LO_FEATS, ff = e % LO_FEATS;

@@ -716,7 +716,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
 // the tile's features; a token keeps its own adapter's.  Writes U [T, R], its two tf32 parts
 // [2, T_rows, Rp] (zero behind R), the lists of adapters per tile of BN tokens, and the layer's grid
 // column-major.
-constexpr int LU_THREADS = 512, LU_WARPS = LU_THREADS / 32;
+// The tensor cores' own additions round towards zero, so that a long run of them drifts (6.7e-7 of U after
+// 768 features): a warp takes LU_RUN features at a time, and the runs' sums meet in IEEE additions.
+constexpr int LU_THREADS = 512, LU_WARPS = LU_THREADS / 32, LU_RUN = 512;
 
 struct ShrinkParams {
   const void *x, *w;     // [T, F], [n, R, F]
@@ -845,68 +847,71 @@ __global__ void __launch_bounds__(LU_THREADS, 1) k_lora_shrink(ShrinkParams p, D
     todo &= ~mine;
     const float scale = p.scaling[a];
     for (int j0 = 0; j0 < p.R; j0 += COLS) {
-      float acc[MT][NTL][4] = {};
       // this lane's rank rows j0 + g + 8 n (clamped: what lies behind R is not kept)
       const uint16_t* w[NTL];
 #pragma unroll
       for (int nt = 0; nt < NTL; ++nt)
         w[nt] = (const uint16_t*)p.w + ((long long)a * p.R + min(j0 + 8 * nt + g, p.R - 1)) * p.F + 8 * t4;
       constexpr int H = MT == 1 && NTL < 8 ? 4 : 2;   // pieces of 32 features loaded at once
-      for (int k0 = s0 * 64; k0 < s1 * 64; k0 += 32 * H) {
-        uint4 xv[H][2 * MT], wv[H][NTL];
-        if (k0 + 32 * H <= min(s1 * 64, p.F)) {
+      for (int run = 0; run < per * 64; run += LU_RUN) {
+        float acc[MT][NTL][4] = {};
+        for (int k0 = s0 * 64 + run; k0 < min(s1 * 64, s0 * 64 + run + LU_RUN); k0 += 32 * H) {
+          uint4 xv[H][2 * MT], wv[H][NTL];
+          if (k0 + 32 * H <= min(s1 * 64, p.F)) {
 #pragma unroll
-          for (int h = 0; h < H; ++h) {
+            for (int h = 0; h < H; ++h) {
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) xv[h][i] = *reinterpret_cast<const uint4*>(x[i] + k0 + 32 * h);
+              for (int i = 0; i < 2 * MT; ++i) xv[h][i] = *reinterpret_cast<const uint4*>(x[i] + k0 + 32 * h);
 #pragma unroll
-            for (int nt = 0; nt < NTL; ++nt)
-              wv[h][nt] = *reinterpret_cast<const uint4*>(w[nt] + k0 + 32 * h);
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            const int k = k0 + 32 * h;
-            const bool in = k < s1 * 64 && k + 8 * t4 < p.F;
-            const uint4 none = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) xv[h][i] = in ? *reinterpret_cast<const uint4*>(x[i] + k) : none;
-#pragma unroll
-            for (int nt = 0; nt < NTL; ++nt)
-              wv[h][nt] = in ? *reinterpret_cast<const uint4*>(w[nt] + k) : none;
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NTL; ++nt) {
-              const uint4 &u = xv[h][2 * mt], &v = xv[h][2 * mt + 1], &b = wv[h][nt];
-              mma16816<BF16>(acc[mt][nt], u.x, v.x, u.y, v.y, b.x, b.y);
-              mma16816<BF16>(acc[mt][nt], u.z, v.z, u.w, v.w, b.z, b.w);
+              for (int nt = 0; nt < NTL; ++nt)
+                wv[h][nt] = *reinterpret_cast<const uint4*>(w[nt] + k0 + 32 * h);
             }
-      }
-      // join the warps (fixed order), 16 tokens and 16 ranks at a time
+          } else {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+            for (int h = 0; h < H; ++h) {
+              const int k = k0 + 32 * h;
+              const bool in = k < s1 * 64 && k + 8 * t4 < p.F;
+              const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int half = 0; half < NTL / 2; ++half) {
-          __syncthreads();
+              for (int i = 0; i < 2 * MT; ++i) xv[h][i] = in ? *reinterpret_cast<const uint4*>(x[i] + k) : none;
 #pragma unroll
-          for (int n2 = 0; n2 < 2; ++n2)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              sums[warp][8 * (i >> 1) + g][8 * n2 + 2 * t4 + (i & 1)] = acc[mt][2 * half + n2][i];
-          __syncthreads();
-          if (threadIdx.x < 256) {
-            const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
-            float v = 0.f;
-#pragma unroll
-            for (int k = 0; k < LU_WARPS; ++k) v += sums[k][row][col];
-            total[(16 * mt + row) * COLS + 16 * half + col] = v;
+              for (int nt = 0; nt < NTL; ++nt)
+                wv[h][nt] = in ? *reinterpret_cast<const uint4*>(w[nt] + k) : none;
+            }
           }
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int nt = 0; nt < NTL; ++nt) {
+                const uint4 &u = xv[h][2 * mt], &v = xv[h][2 * mt + 1], &b = wv[h][nt];
+                mma16816<BF16>(acc[mt][nt], u.x, v.x, u.y, v.y, b.x, b.y);
+                mma16816<BF16>(acc[mt][nt], u.z, v.z, u.w, v.w, b.z, b.w);
+              }
         }
+        // join the warps (fixed order), 16 tokens and 16 ranks at a time
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int half = 0; half < NTL / 2; ++half) {
+            __syncthreads();
+#pragma unroll
+            for (int n2 = 0; n2 < 2; ++n2)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                sums[warp][8 * (i >> 1) + g][8 * n2 + 2 * t4 + (i & 1)] = acc[mt][2 * half + n2][i];
+            __syncthreads();
+            if (threadIdx.x < 256) {
+              const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
+              float v = 0.f;
+#pragma unroll
+              for (int k = 0; k < LU_WARPS; ++k) v += sums[k][row][col];
+              float& sum = total[(16 * mt + row) * COLS + 16 * half + col];
+              sum = run ? sum + v : v;
+            }
+          }
+      }
       if (cl > 1) tc::cluster_sync();
       else __syncthreads();
       // each CTA of the cluster finishes its share of the tokens

@@ -35,6 +35,7 @@ SHAPES = {
     "rank_200": (40, 128, 256, 4, 128, 200, 2, BF, BF, "mixed", {}),
     "t300_300_adapters": (300, 128, 256, 4, 128, 8, 300, BF, F32, "mixed", {}),
     "t8300_many_tokens": (8300, 40, 128, 4, 128, 4, 3, BF, BF, "mixed", {}),
+    "t2500_rank40": (2500, 68, 256, 4, 128, 40, 3, HF, HF, "runs", {}),
     "t40_one_row_of_8": (40, 1, 8, 4, 128, 3, 2, HF, F32, "mixed", {}),
     "t40_one_column": (40, 9, 1, 4, -1, 2, 2, BF, BF, "mixed", {}),
     "t24": (24, 200, 384, 4, 128, 16, 24, HF, HF, "mixed", {}),
