@@ -6,9 +6,10 @@
 // are fp32 sums.  x is read straight into the tensor operand: a lane's 16 bytes are 8 features of
 // one token, and tile i of the warp's eight takes feature 8 n + i as its column n, so no
 // shared-memory pass is needed.  A CTA covers 128 features and 16 ranks (32 at once need twice the
-// registers: 169 us with one CTA per SM, 215 with two and spills, where two passes take 134: 4096 tokens,
-// 4 adapters of rank 32 on 4096 x 11008); its four token warps, and the CTAs of a cluster, take the 8-token groups in turn (adapters' runs spread evenly) and are
-// joined in a fixed order in (distributed) shared memory.  A cluster takes several adapters one after
+// registers: 169 us with one CTA per SM, 215 with two and spills, where two passes took 134: 4096 tokens,
+// 4 adapters of rank 32 on 4096 x 11008, now 114); its four token warps, and the CTAs of a cluster, take
+// the 8-token groups in turn (adapters' runs spread evenly) and are joined in a fixed order in
+// (distributed) shared memory.  A cluster takes several adapters one after
 // the other (one in turn would leave most CTAs of a large adapter table with nothing to do); those
 // without a token are cleared.  Groups without a token of the adapter are skipped; in mixed groups the
 // others' rows are replaced by zeros, not multiplied.
@@ -134,9 +135,28 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
     const int of = i + ((lane >> 3) & 1) * stride;
     return __ballot_sync(0xffffffffu, lane < 16 && of < groups && id_of[of * 8 + (lane & 7)] == a);
   };
+  // this lane's first token, features and ranks, for pairs whose 16 tokens are all the adapter's (features
+  // and ranks behind the end are read from before it and not kept); with the general reads alone 129 us
+  // for 114
+  const bool plain = wide && u_wide;
+  const uint16_t* const x_lane = px + (long long)t4 * F + (plain ? min(f, F - 8) : 0);
+  const float* const u_lane = pu + (long long)t4 * p.R + (plain ? min(j0 + 2 * g, p.R - 2) : 0);
   auto fetch = [&](OuterGroup& o, int i, uint32_t members) {
     o.members = members;
     if (!members) return;
+    if (plain && members == 0xFFFFu) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const long long t = (i + k * stride) * 8 + 4 * h;
+          o.x[k][h] = *reinterpret_cast<const uint4*>(x_lane + t * F);
+          const float2 v = *reinterpret_cast<const float2*>(u_lane + t * p.R);
+          o.u[k][h][0] = v.x;
+          o.u[k][h][1] = v.y;
+        }
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
