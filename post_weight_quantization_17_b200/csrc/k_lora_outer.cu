@@ -7,7 +7,7 @@
 // one token, and tile i of the warp's eight takes feature 8 n + i as its column n, so no
 // shared-memory pass is needed.  A CTA covers 128 features and 16 ranks (32 at once need twice the
 // registers: 169 us with one CTA per SM, 215 with two and spills, where two passes took 134: 4096 tokens,
-// 4 adapters of rank 32 on 4096 x 11008, now 114); its four token warps, and the CTAs of a cluster, take
+// 4 adapters of rank 32 on 4096 x 11008, now 119); its four token warps, and the CTAs of a cluster, take
 // the 8-token groups in turn (adapters' runs spread evenly) and are joined in a fixed order in
 // (distributed) shared memory.  A cluster takes several adapters one after
 // the other (one in turn would leave most CTAs of a large adapter table with nothing to do); those
@@ -24,7 +24,7 @@ constexpr int LO_THREADS = 256;
 constexpr int LO_FEATS = 128, LO_PAD = 68;
 constexpr int LO_TOKENS = 8192;   // of a launch: their adapters (16 bits each) are kept in shared memory
 constexpr int LO_RANKS = 16;
-constexpr int LO_RUN = 8;       // pairs of token groups (16 tokens) that the tensor cores add up by themselves
+constexpr int LO_RUN = 4;       // pairs of token groups (16 tokens) that the tensor cores add up by themselves
 // the warps' sums [8][16][64 + 4] and the CTA's [16][128]; the adapters' bits and the tokens' adapters
 // follow
 constexpr int LO_SMEM = (8 * LO_RANKS * LO_PAD + LO_RANKS * LO_FEATS) * 4;
@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
     return __ballot_sync(0xffffffffu, lane < 16 && of < groups && id_of[of * 8 + (lane & 7)] == a);
   };
   // this lane's first token, features and ranks, for pairs whose 16 tokens are all the adapter's (features
-  // and ranks behind the end are read from before it and not kept); with the general reads alone 129 us
-  // for 114
+  // and ranks behind the end are read from before it and not kept); with the general reads alone 15 us
+  // more of 114
   const bool plain = wide && u_wide;
   const uint16_t* const x_lane = px + (long long)t4 * F + (plain ? min(f, F - 8) : 0);
   const float* const u_lane = pu + (long long)t4 * p.R + (plain ? min(j0 + 2 * g, p.R - 2) : 0);
@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
     }
   };
   // The tensor cores' own additions round towards zero, so that a long run of them drifts (2.4e-6 of dA
-  // after 36 pairs); LO_RUN pairs on, the sums go to the warp's place in shared memory, by IEEE additions.
+  // after 36 pairs); LO_RUN pairs on, the sums go to the warp's place in shared memory, by IEEE additions
+  // (every 8 pairs 8.9e-7 and 114 us, every 4 6.4e-7 and 119).
   // Tile i's column n is feature 8 n + i: a lane holds features 16 t4 + (0..7) and + 8.
   float* mine = sums + warp * LO_RANKS * LO_PAD;
   bool fresh = true;
