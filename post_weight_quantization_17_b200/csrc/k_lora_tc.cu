@@ -11,10 +11,11 @@
 //
 //   Forward: the stage holds (c - z), exact in 16 bits; the group's Δ multiplies each 128-column
 //   partial sum in fp32 as it is taken out of TMEM, so Ŵ is never rounded.
-//   Backward: Δ differs along the contraction, so it has to be in the operand: Δ (c - z) is rounded
-//   once to the 16-bit type, as (c - z) Δ_hi + (c - z) Δ_lo with Δ split in two 16-bit parts.  Its
-//   error is that of a 16-bit weight, half a step, the same size as the rounding of dX itself.  (fp16
-//   operands carry a factor of 256, taken out at the end, so that small Δ stay normal numbers.)
+//   Backward: Δ differs along the contraction, so it has to be in the operand.  Δ (c - z) enters as two
+//   16-bit parts, a stage each against the same tokens, and keeps 14 bits of bf16 (16 in the mean) or 19
+//   of fp16, far below half a step of dX; as one 16-bit number it made dX 1.41 times as far from the
+//   exact sum as its own rounding, for half the products.  (fp16 operands carry a factor of 256, taken
+//   out at the end, so that small Δ stay normal numbers.)
 //   Adapters: each adapter that occurs among the tile's tokens ("slot") adds one more partial sum,
 //   whose operands are the adapter's 16-bit rows and U in two tf32 parts (22 bits), both fp32 in
 //   shared memory (kind::tf32); the epilogue adds it to that adapter's tokens only, so one request's
@@ -73,8 +74,8 @@ struct LtParams {
   const float2* grid;       // [n_g, m_pad] (Δ, z), zero behind m
   int m_pad, used;          // its columns, and how many n_g there are
   int mtiles, ttiles, splits;
-  int units, per;           // the contraction in 128-column steps (forward) or 64-row stages
-                            // (backward): in all and per split
+  int units, per;           // the contraction in 128-column (forward) or 64-row (backward) units of two
+                            // stages: in all and per split
   int T_rows;               // rows of one part of the split U
   int rank_chunks;          // 32-rank chunks; 0: no adapter partials (split contraction)
   int R, n;
@@ -173,6 +174,40 @@ template <bool BF16> __device__ __forceinline__ uint32_t pack16(float a, float b
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+
+// Δ of a row, and with it (c - z) Δ as a sum of two 16-bit numbers.  With Δ = H + L (each rounded once)
+// and H' a little below H, hi = round((c - z) H') is always smaller in magnitude than (c - z) Δ: the
+// margin of 5/4 half steps (2^-8 of bf16, 2^-11 of fp16) covers its rounding and that of L.  What is
+// left, ((c - z) H - hi) + (c - z) L, has an exact first term (at most 158 units of hi's last place, of
+// the 256 that the type holds) and is rounded once, to within 2^-14 of the weight (2^-19 for fp16).  It is
+// never zero and never of the other sign unless c = z, so that an infinite gradient stays infinite in
+// the sum of both products.
+template <bool BF16> struct WeightParts {
+  using T2 = typename std::conditional<BF16, __nv_bfloat162, __half2>::type;
+  T2 h, l, under;
+  __device__ __forceinline__ WeightParts() {}
+  __device__ __forceinline__ explicit WeightParts(float d) {
+    if constexpr (BF16) {
+      const __nv_bfloat16 H = __float2bfloat16_rn(d);
+      h = __bfloat162bfloat162(H);
+      l = __bfloat162bfloat162(__float2bfloat16_rn(d - __bfloat162float(H)));
+      under = __bfloat162bfloat162(__float2bfloat16_rz(d * (1.f - 0x5p-10f)));
+    } else {
+      const __half H = __float2half_rn(d);
+      h = __half2half2(H);
+      l = __half2half2(__float2half_rn(d - __half2float(H)));
+      under = __half2half2(__float2half_rz(d * (1.f - 0x5p-13f)));
+    }
+  }
+  // v: two values of (c - z), replaced by the high parts
+  __device__ __forceinline__ void split(uint32_t& v, uint32_t& low) const {
+    const T2 c = *reinterpret_cast<const T2*>(&v);
+    const T2 hi = __hmul2(c, under);
+    const T2 lo = __hfma2(c, l, __hfma2(c, h, __hneg2(hi)));
+    v = *reinterpret_cast<const uint32_t*>(&hi);
+    low = *reinterpret_cast<const uint32_t*>(&lo);
+  }
+};
 
 // A position in a ring of N stages or buffers.
 template <int N> struct LtRing {
@@ -287,8 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       };
       for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
         const LtTile t(p, i, BN, rank);
-        const int k1 = FWD ? 2 * t.u1 : t.u1;
-        for (int k = FWD ? 2 * t.u0 : t.u0; k < k1 && ok; ++k) stage(&tmX, k * 64, t.t0);
+        for (int k = 2 * t.u0; k < 2 * t.u1 && ok; ++k) stage(&tmX, (FWD ? k : k >> 1) * 64, t.t0);
         if (!p.rank_chunks) continue;
         if (!waited) pdl_wait();   // only now: the tokens' operand is the caller's
         waited = true;
@@ -378,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         if (FWD)
           for (int u = t.u0; u < t.u1 && ok; ++u) partial(2, false);
         else
-          partial(t.u1 - t.u0, false);
+          partial(2 * (t.u1 - t.u0), false);
         for (int s = 0; s < count && ok; ++s) partial(2 * p.rank_chunks, true);
       }
       // every MMA has completed before TMEM is freed
@@ -435,7 +469,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     // A thread's piece is 16 bytes (32 codes) of a row: eight lanes with the same piece of eight rows
     // read eight different 16-byte columns of the 64-byte-swizzled codes, and store to eight
     // different ones of the 128-byte-swizzled operand.  Forward: 128 rows x 128 columns at a time,
-    // two stages (pieces 0, 1 and 2, 3).  Backward: 64 rows x 128 columns, one stage.
+    // two stages (pieces 0, 1 and 2, 3).  Backward: 64 rows x 128 columns, the two parts of a weight in two
+    // stages.
     // The units alternate between two groups of four warps, so that one's waits and fences overlap the
     // other's arithmetic; each arrives for two on the barriers, which count eight warps.
     const int group = warp >> 2, q = (tid >> 3) & 3, brow = (tid & 7) + 8 * (warp & 3);
@@ -464,16 +499,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         turn ^= 1;
         if (!mine) {
           ring.next();
-          if (FWD) ring.next();
+          ring.next();
           cring.next();
           ++pc;
           continue;
         }
         if (!__all_sync(0xffffffffu,
                         lt_wait(&full_c[cring.i], cring.phase, budget) &&
-                            (FWD ? lt_wait2(&empty[ring.i], ring.phase ^ 1u, &empty[second.i],
-                                            second.phase ^ 1u, budget)
-                                 : lt_wait(&empty[ring.i], ring.phase ^ 1u, budget)))) {
+                            lt_wait2(&empty[ring.i], ring.phase ^ 1u, &empty[second.i], second.phase ^ 1u,
+                                     budget))) {
           raise_error(st, GPTQ_ERR_TIMEOUT, 76);
           *abort_flag = 1;
           ok = false;
@@ -498,49 +532,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
           for (int h = 0; h < 2; ++h) {
             const uint32_t zz = zero_pair<BF16>((int)dz[h].y);
             const uint32_t words[4] = {code[h].x, code[h].y, code[h].z, code[h].w};
-            uint32_t hi2 = 0, lo2 = 0;
-            if (!FWD) {
-              if (BF16) {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(dz[h].x);
-                const __nv_bfloat16 lo = __float2bfloat16_rn(dz[h].x - __bfloat162float(hi));
-                const __nv_bfloat162 a = __halves2bfloat162(hi, hi), b = __halves2bfloat162(lo, lo);
-                hi2 = *reinterpret_cast<const uint32_t*>(&a);
-                lo2 = *reinterpret_cast<const uint32_t*>(&b);
-              } else {
-                const float ds = dz[h].x * LT_F16_SCALE;
-                const __half hi = __float2half_rn(ds);
-                const __half lo = __float2half_rn(ds - __half2float(hi));
-                const __half2 a = __halves2half2(hi, hi), b = __halves2half2(lo, lo);
-                hi2 = *reinterpret_cast<const uint32_t*>(&a);
-                lo2 = *reinterpret_cast<const uint32_t*>(&b);
-              }
-            }
+            WeightParts<BF16> parts;
+            if (!FWD) parts = WeightParts<BF16>(BF16 ? dz[h].x : dz[h].x * LT_F16_SCALE);
             const int row = brow + 32 * (h0 + h);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               uint32_t v[4];
               centered8<BF16>(words[w], zz, v);
-              if (!FWD) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if (BF16) {
-                    const __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&v[e]);
-                    const __nv_bfloat162 r =
-                        __hfma2(c, *reinterpret_cast<const __nv_bfloat162*>(&hi2),
-                                __hmul2(c, *reinterpret_cast<const __nv_bfloat162*>(&lo2)));
-                    v[e] = *reinterpret_cast<const uint32_t*>(&r);
-                  } else {
-                    const __half2 c = *reinterpret_cast<const __half2*>(&v[e]);
-                    const __half2 r = __hfma2(c, *reinterpret_cast<const __half2*>(&hi2),
-                                              __hmul2(c, *reinterpret_cast<const __half2*>(&lo2)));
-                    v[e] = *reinterpret_cast<const uint32_t*>(&r);
-                  }
-                }
-              }
               const int chunk = 4 * (q & 1) + w;
-              *reinterpret_cast<uint4*>(dst + (FWD ? 0 : (q >> 1) * 8192) + row * 128 +
-                                        ((chunk ^ (row & 7)) << 4)) =
-                  make_uint4(v[0], v[1], v[2], v[3]);
+              const int at = (FWD ? 0 : (q >> 1) * 8192) + row * 128 + ((chunk ^ (row & 7)) << 4);
+              if (!FWD) {
+                uint32_t low[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) parts.split(v[e], low[e]);
+                *reinterpret_cast<uint4*>(smem + second.i * Cfg::STAGE + at) =
+                    make_uint4(low[0], low[1], low[2], low[3]);
+              }
+              *reinterpret_cast<uint4*>(dst + at) = make_uint4(v[0], v[1], v[2], v[3]);
             }
           }
         }
@@ -548,11 +556,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         __syncwarp();
         if (lane == 0) {
           lt_arrive_remote(lead_full_a + 8u * ring.i, 2);
-          if (FWD) lt_arrive_remote(lead_full_a + 8u * second.i, 2);
+          lt_arrive_remote(lead_full_a + 8u * second.i, 2);
           lt_arrive_remote(tc::smem_u32(&empty_c[cring.i]), 2);
         }
         ring.next();
-        if (FWD) ring.next();
+        ring.next();
         cring.next();
         ++pc;
       }
@@ -1022,7 +1030,7 @@ long long round_up(long long x, long long a) { return (x + a - 1) / a * a; }
 // tokens, 128 at 256), so 128 tokens are for batches that fit in them; an item costs about 3000 cycles
 // besides, a split's sums their traffic.
 struct LtPlan { int BN, splits, per; };
-LtPlan lt_plan(int M, int T, int units, int stages_per_unit, int num_sms, size_t part_floats) {
+LtPlan lt_plan(int M, int T, int units, int num_sms, size_t part_floats) {
   const int BN = T <= 128 ? 128 : 256;
   const long long tiles = ((M + 255) / 256) * (long long)((T + BN - 1) / BN), pairs = num_sms / 2;
   LtPlan best{BN, 1, units};
@@ -1031,7 +1039,7 @@ LtPlan lt_plan(int M, int T, int units, int stages_per_unit, int num_sms, size_t
     const int per = (units + s - 1) / s, splits = (units + per - 1) / per;
     if (splits > 1 && (T > 1024 || (size_t)splits * T * M > part_floats)) break;
     const long long waves = (tiles * splits + pairs - 1) / pairs;
-    const double cost = waves * ((double)per * stages_per_unit * 700 + 3000) +
+    const double cost = waves * ((double)per * 2 * 700 + 3000) +
                         (splits > 1 ? 6000 + splits * (double)T * M * 8 / 3000 : 0);
     if (s == 1 || cost < best_cost) {
       best = {BN, splits, per};
@@ -1132,7 +1140,7 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   const void* xs = pad ? xp : x;
 
   const int units = forward ? (K + 127) / 128 : (K + 63) / 64;
-  const LtPlan plan = lt_plan(M, l.T, units, forward ? 2 : 1, c->num_sms, part_floats);
+  const LtPlan plan = lt_plan(M, l.T, units, c->num_sms, part_floats);
   const bool fused = plan.splits == 1;
   const int ttiles = (l.T + plan.BN - 1) / plan.BN;
 
