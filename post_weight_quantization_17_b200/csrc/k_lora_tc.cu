@@ -44,6 +44,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "lora_rings.h"
 #include "lora_util.cuh"
 #include "tc_util.cuh"
 
@@ -61,10 +62,12 @@ struct LtCfg {
   static constexpr int NS = BN == 256 ? 6 : 8;
   // a unit of codes and grid: 128 rows x 128 columns forward, 64 rows backward
   static constexpr int C_BYTES = FWD ? 8192 : 4096, G_BYTES = FWD ? 1024 : 512;
-  static constexpr int NC = FWD ? 3 : 6;
+  static constexpr int NC = FWD ? kLoraCodeSlotsForward : kLoraCodeSlotsBackward;
+  static constexpr int NB = lora_code_barriers(NC);   // their barriers
   static constexpr int SMEM = NS * STAGE + NC * (C_BYTES + G_BYTES) + LT_DELTAS * 128 * 4 + 1024 + 512;
   static constexpr int EBN = BN / 2;       // tokens per epilogue thread
   static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(NB % 2 == 0 && NB % NC == 0, "a barrier of code units belongs to one group of weight warps");
 };
 
 struct LtParams {
@@ -246,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int NC = Cfg::NC;
+  constexpr int NC = Cfg::NC, NB = Cfg::NB;
   uint8_t* codes = smem + NS * Cfg::STAGE;               // NC units of codes, then of grid
   float2* grids = reinterpret_cast<float2*>(codes + NC * Cfg::C_BYTES);
   float* deltas = reinterpret_cast<float*>(codes + NC * (Cfg::C_BYTES + Cfg::G_BYTES));
@@ -256,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
   uint64_t* d_full = empty + NS;
   uint64_t* d_empty = d_full + ND;
   uint64_t* full_c = d_empty + ND;
-  uint64_t* empty_c = full_c + NC;
+  uint64_t* empty_c = full_c + NB;
   uint64_t* drain = empty_c + NC;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -274,10 +277,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       tc::mbar_init(&d_full[b], 1);
       tc::mbar_init(&d_empty[b], 16);
     }
-    for (int b = 0; b < NC; ++b) {
-      tc::mbar_init(&full_c[b], 1);
-      tc::mbar_init(&empty_c[b], 8);
-    }
+    for (int b = 0; b < NB; ++b) tc::mbar_init(&full_c[b], 1);
+    for (int b = 0; b < NC; ++b) tc::mbar_init(&empty_c[b], 8);
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
     tc::mbar_fence_init();
@@ -422,7 +423,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       }
     } else if (warp == 18 && lane == 0) {
       // -------------------------------------------------------------- codes and grid
-      LtRing<NC> ring;
+      LtRing<NC> ring;   // the slots
+      LtRing<NB> bar;    // and their barriers
       int issued = 0;
       bool ok = true;
       pdl_wait();   // the grid
@@ -438,23 +440,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
           // (the second CTA's columns may lie behind the last group: they are not stored)
           const int g = p.group_steps ? min((FWD ? u : t.f0 / 128) / p.group_steps, p.used - 1) : 0;
           const int row = FWD ? t.f0 : 64 * u;
-          tc::mbar_expect_tx(&full_c[ring.i], Cfg::C_BYTES + Cfg::G_BYTES);
-          tc::tma_load_2d(codes + ring.i * Cfg::C_BYTES, &tmC, &full_c[ring.i],
+          tc::mbar_expect_tx(&full_c[bar.i], Cfg::C_BYTES + Cfg::G_BYTES);
+          tc::tma_load_2d(codes + ring.i * Cfg::C_BYTES, &tmC, &full_c[bar.i],
                           FWD ? 16 * u : t.f0 / 8, row);
           asm volatile(
               "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
               "[%3];" ::"r"(tc::smem_u32(grids) + ring.i * Cfg::G_BYTES),
               "l"(p.grid + (long long)g * p.m_pad + row), "r"(Cfg::G_BYTES),
-              "r"(tc::smem_u32(&full_c[ring.i]))
+              "r"(tc::smem_u32(&full_c[bar.i]))
               : "memory");
           ring.next();
+          bar.next();
           ++issued;
         }
       }
-      const int left = min(issued, NC);
+      const int left = min(issued, NB);
       for (int s = 0; s < left; ++s) {
         const int j = issued - left + s;
-        if (!lt_wait(&full_c[j % NC], (uint32_t)(j / NC) & 1u, kDrainCycles))
+        if (!lt_wait(&full_c[j % NB], (uint32_t)(j / NB) & 1u, kDrainCycles))
           raise_error(st, GPTQ_ERR_TIMEOUT, 80);
       }
     }
@@ -463,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     // ---------------------------------------------------------------- weight operand
     const int tid = threadIdx.x;
     LtRing<NS> ring;
-    LtRing<NC> cring;
+    LtRing<NB> cring;   // the units' barriers; their slots are cring.i % NC
     bool ok = true;
     pdl_wait();   // the slots
     // A thread's piece is 16 bytes (32 codes) of a row: eight lanes with the same piece of eight rows
@@ -472,7 +475,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     // two stages (pieces 0, 1 and 2, 3).  Backward: 64 rows x 128 columns, the two parts of a weight in two
     // stages.
     // The units alternate between two groups of four warps, so that one's waits and fences overlap the
-    // other's arithmetic; each arrives for two on the barriers, which count eight warps.
+    // other's arithmetic; each arrives for two on the barriers, which count eight warps.  (The stages need
+    // no barriers of their own per group: MMAs complete in order, and a warp that has seen a stage within
+    // the last ring released finds no barrier two phases behind.)
     const int group = warp >> 2, q = (tid >> 3) & 3, brow = (tid & 7) + 8 * (warp & 3);
     constexpr int PIECES = FWD ? 4 : 2;
     uint32_t pc = 0;   // partial sums so far
@@ -513,6 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
           ok = false;
           break;
         }
+        const int slot = cring.i < NC ? cring.i : cring.i - NC;
         uint8_t* dst = smem + (FWD && q >= 2 ? second.i : ring.i) * Cfg::STAGE;
 #pragma unroll
         for (int h0 = 0; h0 < PIECES; h0 += 2) {
@@ -521,9 +527,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int row = brow + 32 * (h0 + h);
-            code[h] = *reinterpret_cast<const uint4*>(codes + cring.i * Cfg::C_BYTES + row * 64 +
+            code[h] = *reinterpret_cast<const uint4*>(codes + slot * Cfg::C_BYTES + row * 64 +
                                                       ((q ^ ((row >> 1) & 3)) << 4));
-            dz[h] = grids[cring.i * (Cfg::G_BYTES / 8) + row];
+            dz[h] = grids[slot * (Cfg::G_BYTES / 8) + row];
             // the partial that last used this slot of deltas has been taken out: its MMAs' successors,
             // two partials on, have released the stages that were just waited for
             if (FWD && q == 0) deltas[(pc % LT_DELTAS) * 128 + row] = dz[h].x;
@@ -557,7 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         if (lane == 0) {
           lt_arrive_remote(lead_full_a + 8u * ring.i, 2);
           lt_arrive_remote(lead_full_a + 8u * second.i, 2);
-          lt_arrive_remote(tc::smem_u32(&empty_c[cring.i]), 2);
+          lt_arrive_remote(tc::smem_u32(&empty_c[slot]), 2);
         }
         ring.next();
         ring.next();
