@@ -16,6 +16,7 @@
 // products end.
 #include <algorithm>
 
+#include "lora_small_x.h"
 #include "lora_util.cuh"
 
 namespace gptq {
@@ -191,20 +192,14 @@ __global__ void __launch_bounds__(LS_THREADS, ls_ctas(NT)) k_lora_small(SmallPar
   for (int nt = 0; nt < NT; ++nt)
     xrow[nt] = reinterpret_cast<const uint4*>((const uint16_t*)p.X + (long long)min(nt * 8 + g, p.T - 1) * p.d +
                                               s0 * 128 + t4 * 32);
-  // The q-th 8 columns of step s, which is the one that `xrow` points to (q 4 and up: of the next, or of
-  // this one once more where there is no next).  Loaded XA pieces ahead: three for 8 tokens, where an
-  // L2 round trip is as long as the work on two, one where the registers hold more tokens.
+  // The q-th 8 columns of step s, which is the one that `xrow` points to (q 4 and up: of the next one).
+  // Loaded XA pieces ahead: three for 8 tokens, where an L2 round trip is as long as the work on two, one
+  // where the registers hold more tokens.
   constexpr int XA = NT == 1 ? 3 : 1, XB = XA + 1;
   auto load_x = [&](int s, int q, uint4 (&x)[NT]) {
-    if (s + (q >> 2) == ragged) {
-      const bool in = s * 128 + t4 * 32 + (q >> 2) * 128 + 8 * (q & 3) < p.d;
+    const int at = small_x_piece(p.d, s, q, s1, ragged, t4);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt] = in ? xrow[nt][(q >> 2) * 16 + (q & 3)] : make_uint4(0, 0, 0, 0);
-    } else {
-      const int at = q >= 4 && s + 1 < s1 ? 16 : 0;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt] = xrow[nt][at + (q & 3)];
-    }
+    for (int nt = 0; nt < NT; ++nt) x[nt] = at >= 0 ? xrow[nt][at] : make_uint4(0, 0, 0, 0);
   };
   uint4 x[XB][NT];
   if (s0 < s1) {
