@@ -345,8 +345,9 @@ __global__ void __launch_bounds__(DS_THREADS, 3)
   ds_read_list<T>(p, t, z, it, l, list_part, st);
   float lse;
   if (LOSS) {
-    float m = edge_z, s = edge_z == -INFINITY ? 0.f : 1.f;
-    if (edge_z != edge_z) s = edge_z;   // NaN: fmaxf drops it from the maximum, not from the sum
+    // an end's own sum: 1, 0 for -inf, NaN for +inf (as inf - inf among the vectors) and NaN (which fmaxf
+    // drops from the maximum, not from the sum)
+    float m = edge_z, s = edge_z == -INFINITY ? 0.f : edge_z - edge_z + 1.f;
     landed();
     for (int i = threadIdx.x; i < nv; i += 2 * DS_THREADS) {
       const uint4 v0 = row[i];
