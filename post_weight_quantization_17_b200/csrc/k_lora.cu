@@ -155,13 +155,17 @@ __global__ void __launch_bounds__(128)
 }
 
 // fp32 x: out[a, j, f] (+)= Σ_{t: a_t = a} u[t, j] x[t, f] for 8 rank indices: one feature per thread.
-// A token of another adapter is skipped, not multiplied by zero, so its non-finite values stay out.
+// A token of another adapter is skipped, not multiplied by zero, so its non-finite values stay out.  (The
+// first CTA checks the ids: dB alone needs no other kernel.)
 __global__ void __launch_bounds__(128)
-    k_lora_outer_f32(const float* __restrict__ u, const float* __restrict__ x, int T, int F, int R,
-                     const int32_t* __restrict__ adapter, int accumulate, float* __restrict__ out) {
+    k_lora_outer_f32(const float* __restrict__ u, const float* __restrict__ x, int T, int F, int n, int R,
+                     const int32_t* __restrict__ adapter, int accumulate, float* __restrict__ out,
+                     DeviceStatus* st) {
   pdl_wait();
   pdl_release();
   const int f = blockIdx.x * 128 + threadIdx.x, j0 = blockIdx.y * 8, a = blockIdx.z;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    for (int t = threadIdx.x; t < T; t += 128) adapter_of(adapter, t, n, st);
   if (f >= F) return;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int t = 0; t < T; ++t) {
@@ -212,7 +216,7 @@ int forward_any(Ctx* c, const LoraLayer& l, const TX* X, void* Y, bool y_f32, fl
 int outer_f32(Ctx* c, const LoraLayer& l, const float* u, const float* x, int F, int accumulate,
               float* out) {
   GPTQ_LAUNCH(c, k_lora_outer_f32, dim3((F + 127) / 128, (l.R + 7) / 8, l.n), 128, 0, u, x, l.T, F,
-              l.R, l.adapter, accumulate, out);
+              l.n, l.R, l.adapter, accumulate, out, c->status);
   return GPTQ_OK;
 }
 
