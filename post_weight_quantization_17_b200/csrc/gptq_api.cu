@@ -74,12 +74,10 @@ bool aligned_to(const void* p, int dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == GPTQ_F32 ? 3 : 1)) == 0;
 }
 
-constexpr int64_t kLoraMaxRank = 1024, kLoraMaxAdapters = 65535;
-
 bool lora_sizes_ok(int64_t T, int64_t m, int64_t d, int bits, int64_t n, int64_t rank) {
   return T >= 0 && T <= 65535LL * 8 && m >= 1 && m <= (1 << 24) && d >= 1 && d <= (1 << 24) &&
-         bits >= 1 && bits <= 8 && n >= 1 && n <= kLoraMaxAdapters && rank >= 1 &&
-         rank <= kLoraMaxRank;
+         bits >= 1 && bits <= 8 && n >= 1 && n <= gptq::kLoraMaxAdapters && rank >= 1 &&
+         rank <= gptq::kLoraMaxRank;
 }
 
 bool make_lora_layer(gptq::LoraLayer* l, int64_t T, int64_t m, int64_t d, int bits, int group,
@@ -100,13 +98,11 @@ bool make_lora_layer(gptq::LoraLayer* l, int64_t T, int64_t m, int64_t d, int bi
   return true;
 }
 
-constexpr int64_t kDistillMaxK = 2048;
-
 bool distill_ok(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
                 const float* values, const int32_t* indices, int64_t K, float tau,
                 const float* weight, const float* teacher_lse) {
   return (T == 0 || (logits && values && indices)) && valid_dtype(dtype) && T >= 0 && T <= INT32_MAX && V >= 1 &&
-         V <= (1 << 24) && ld >= V && ld <= (1LL << 32) && K >= 1 && K <= kDistillMaxK &&
+         V <= (1 << 24) && ld >= V && ld <= (1LL << 32) && K >= 1 && K <= gptq::kDistillMaxK &&
          tau >= 1e-6f && tau <= 1e6f && aligned_to(logits, dtype) && aligned_to(values, GPTQ_F32) &&
          aligned_to(indices, GPTQ_F32) && aligned_to(weight, GPTQ_F32) &&
          aligned_to(teacher_lse, GPTQ_F32);

@@ -25,6 +25,7 @@ constexpr int DS_THREADS = 256;
 constexpr int DS_WARPS = DS_THREADS / 32;
 constexpr int DS_PART = 64 * 1024;               // a CTA's part of a row, where rows allow it
 constexpr int DS_PART_MAX = 160 * 1024;
+constexpr int DS_ENTRY = 12;                     // bytes of shared memory per entry of the list
 constexpr float DS_LOG2E = 1.4426950408889634f, DS_LN2 = 0.6931471805599453f;
 
 template <class T> __device__ __forceinline__ T ds_round(float v);
@@ -531,8 +532,11 @@ namespace {
 
 template <class T, bool LOSS, bool GRAD>
 int launch_distill(Ctx* c, const DistillArgs& p, int log2c, int part, size_t smem) {
+  // the kernel's limit, not this call's size: the attribute is the device's, and another thread's call may
+  // set it between this one's attribute and its launch
   GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(k_distill<T, LOSS, GRAD>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          DS_PART_MAX + kDistillMaxK * DS_ENTRY));
   GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, LOSS ? 1 << log2c : 1, k_distill<T, LOSS, GRAD>,
                                         dim3((unsigned)p.T << log2c), dim3(DS_THREADS), smem, p,
                                         part, log2c, c->status, c->timeout_cycles));
@@ -541,7 +545,7 @@ int launch_distill(Ctx* c, const DistillArgs& p, int log2c, int part, size_t sme
 
 template <class T>
 int distill_as(Ctx* c, const DistillArgs& p) {
-  const size_t list = (size_t)p.K * 12;
+  const size_t list = (size_t)p.K * DS_ENTRY;
   const long long nvec = std::max<long long>(1, (long long)p.V / DsVec<T>::N);
   // CTAs per row: parts of at most DS_PART bytes; with few rows more, down to 8 KB parts, so that
   // the SMs share the work (the loss of 5 rows of 32000 fp32 logits: 4.5 us, without 5.1).

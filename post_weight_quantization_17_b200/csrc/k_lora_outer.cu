@@ -28,6 +28,7 @@ constexpr int LO_RUN = 4;       // pairs of token groups (16 tokens) that the te
 // the warps' sums [8][16][64 + 4] and the CTA's [16][128]; the adapters' bits and the tokens' adapters
 // follow
 constexpr int LO_SMEM = (8 * LO_RANKS * LO_PAD + LO_RANKS * LO_FEATS) * 4;
+constexpr int lo_smem(int n, int T) { return LO_SMEM + (n + 127) / 128 * 16 + (T + 7) / 8 * 16; }
 
 struct OuterProblem {
   const float* u;          // [T, R]
@@ -329,9 +330,10 @@ int lora_outers(Ctx* c, const LoraLayer& l, const float* G, const void* X, float
     p.two[1] = problem(U, dY, dB, l.m);
     p.first_ctas = ca;
     const dim3 grid(ca + cb, ranks, std::max(1, std::min(l.n, 8 * c->num_sms / ((ca + cb) * ranks))));
-    const int smem = LO_SMEM + (l.n + 127) / 128 * 16 + (p.T + 7) / 8 * 16;
-    GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, p.cluster, kernel, grid, dim3(LO_THREADS), smem, p,
+    // the kernel's limit, not this call's size: other threads' calls set the same attribute
+    GPTQ_CUDA_CHECK(c, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            lo_smem(kLoraMaxAdapters, LO_TOKENS)));
+    GPTQ_CUDA_CHECK(c, launch_pdl_cluster(c, p.cluster, kernel, grid, dim3(LO_THREADS), lo_smem(l.n, p.T), p,
                                           c->status));
   }
   return GPTQ_OK;

@@ -98,6 +98,7 @@ int dequant_matmul_tiled(Ctx* c, const void* X, int x_dtype, int T, int d,
                          const int32_t* zeros, float* Y, float* part_ws, size_t part_floats);
 
 // ---- the packed layer with low-rank adapters (k_lora.cu)
+constexpr int kLoraMaxRank = 1024, kLoraMaxAdapters = 65535;
 struct LoraLayer {
   int T, m, d, bits, group, ng;
   const uint32_t* packed;
@@ -138,6 +139,7 @@ int lora_outers(Ctx* c, const LoraLayer& l, const float* G, const void* X, float
                 const void* dY, float* dB, int accumulate);
 
 // ---- distillation from a teacher's top logits (k_distill.cu)
+constexpr int kDistillMaxK = 2048;   // entries of a teacher's list
 struct DistillArgs {
   const void* logits;
   int dtype, T, V, K;
