@@ -199,11 +199,10 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {   // rows g and g + 8 (ranks 2 g, 2 g + 1) of tokens t4 and t4 + 4
-        const float v = o.u[k][e >> 1][e & 1];
-        const bool finite = fabsf(v) <= 3.0e38f;   // the split is for finite values
-        const float h = finite ? tc::tf32_rna(v) : v;
+        float h, l;
+        tc::tf32_parts(o.u[k][e >> 1][e & 1], h, l);
         hi[e] = __float_as_uint(h);
-        lo[e] = finite ? __float_as_uint(tc::tf32_rna(v - h)) : 0u;
+        lo[e] = __float_as_uint(l);
       }
       // all the high parts, then all the low ones: eight products lie between two of one sum
       float2 b0[4], b1[4];

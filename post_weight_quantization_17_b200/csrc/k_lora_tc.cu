@@ -787,10 +787,9 @@ __device__ __forceinline__ void turn_grid(const ShrinkParams& p, int i, DeviceSt
 __device__ __forceinline__ void write_low_rank(const ShrinkParams& p, int t, int j, float u) {
   if (p.U && j < p.R) p.U[(long long)t * p.R + j] = u;
   if (p.parts) {
-    const float hi = tc::tf32_rna(u);
-    // a non-finite or huge value has no low part
-    const float lo = fabsf(hi) <= 3.0e38f ? u - hi : 0.f;
-    p.parts[(long long)t * p.Rp + j] = fabsf(u) <= 3.0e38f ? hi : u;
+    float hi, lo;
+    tc::tf32_parts(u, hi, lo);
+    p.parts[(long long)t * p.Rp + j] = hi;
     p.parts[((long long)p.T_rows + t) * p.Rp + j] = lo;
   }
 }

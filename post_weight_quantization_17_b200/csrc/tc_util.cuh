@@ -271,6 +271,15 @@ __device__ __forceinline__ void mma_tf32_pair(uint32_t tmem_d, uint64_t adesc, u
 __device__ __forceinline__ float tf32_rna(float x) {
   return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xFFFFE000u);
 }
+// v as the sum of two tf32 numbers, to within 2^-22 of it: hi is the largest one below it in magnitude,
+// lo what is left (at most 14 bits, rounded to 11).  Both have v's sign and neither is zero unless v is, so
+// that hi·w + lo·w is what v·w is for an infinite w, too; an infinite or NaN v is both of them.
+__device__ __forceinline__ void tf32_parts(float v, float& hi, float& lo) {
+  const uint32_t b = __float_as_uint(v);
+  const bool number = (b << 1) - 1u < 0xFEFFFFFFu;   // neither zero nor infinite nor NaN
+  hi = number ? __uint_as_float((b - 1u) & 0xFFFFE000u) : v;
+  lo = number ? tf32_rna(v - hi) : v;
+}
 // Arrives on `bar` in both CTAs of the pair once every pair MMA issued so far has completed.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
   asm volatile(

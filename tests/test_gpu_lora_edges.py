@@ -30,3 +30,46 @@ def test_bad_ids_are_reported_by_every_gradient_alone(ctx, dtype, part, bad):
     with pytest.raises(G.GPTQError) as e:
         G.gptq_sync_status(ctx)
     assert e.value.code == G.GPTQ_ERR_ARG
+
+
+def _same_where_not_finite(got, want, what):
+    want = want.to(torch.float64)
+    assert torch.equal(got.isnan(), want.isnan()), f"{what}: NaN elsewhere"
+    inf = want.isinf()
+    assert torch.equal(got.double()[inf], want[inf]), f"{what}: other infinities"
+    assert torch.isfinite(got[torch.isfinite(want)]).all(), f"{what}: non-finite elsewhere"
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("T", [5, 40, 150, 300])
+@pytest.mark.parametrize("where", ["X", "A", "B"])
+def test_an_infinity_is_what_the_formula_makes_of_it(ctx, dtype, T, where):
+    c = Case(T, 200, 256, 4, 128, 8, 3, dtype, "mixed", 42)
+    c.adapter[:3] = torch.arange(3, dtype=torch.int32)
+    t = {"X": c.X, "A": c.A[1], "B": c.B[1]}[where]
+    t[1, 7] = -torch.inf
+    Y, U = torch.zeros(T, 200, device="cuda"), torch.zeros(T, 8, device="cuda")
+    G.gptq_lora_matmul(ctx, c.X, *c.layer(), Y, U=U)
+    G.gptq_sync_status(ctx)
+    y, _, u, _ = c.forward(F32)
+    _same_where_not_finite(U, u, "U")
+    _same_where_not_finite(Y, y, "Y")
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("T", [5, 40, 150, 300])
+@pytest.mark.parametrize("where", ["X", "dY", "A", "B", "U"])
+def test_an_infinity_in_the_backward_pass(ctx, dtype, T, where):
+    c = Case(T, 200, 256, 4, 128, 8, 3, dtype, "mixed", 43)
+    c.adapter[:3] = torch.arange(3, dtype=torch.int32)
+    U = c.low(c.X, c.A)[0].float()
+    t = {"X": c.X, "dY": c.dY, "A": c.A[1], "B": c.B[1], "U": U}[where]
+    t[1, 7] = -torch.inf
+    dX = torch.zeros_like(c.X)
+    dA, dB = torch.zeros(3, 8, 256, device="cuda"), torch.zeros(3, 8, 200, device="cuda")
+    G.gptq_lora_backward(ctx, c.dY, c.X, *c.layer(), U, dX=dX, dA=dA, dB=dB)
+    G.gptq_sync_status(ctx)
+    (dx, _), (da, _), (db, _) = c.backward(U.double(), False)
+    _same_where_not_finite(dX, dx, "dX")
+    _same_where_not_finite(dA, da, "dA")
+    _same_where_not_finite(dB, db, "dB")
