@@ -322,7 +322,7 @@ int gptq_lora_matmul(gptq_ctx* ctx, const void* X, int x_dtype, int64_t T, int64
  *   accumulate  0: dA and dB are overwritten (adapters without tokens get 0); 1: they are added to.
  * On the tensor cores Ŵ enters dX as two numbers of x_dtype, good to 2^-14 of each weight (2^-19 for
  * GPTQ_F16), with products and sums in fp32, so dX is off by its own rounding; GPTQ_F16 asks for
- * |Ŵ| < 255, else ARG via gptq_sync_status.  dA and dB are sums over tokens
+ * |Δ| < 17 (so |Ŵ| < 255), else ARG via gptq_sync_status.  dA and dB are sums over tokens
  * in a fixed order: two calls on the same inputs give the same bits.  Non-finite values of a token
  * reach its own row of dX and its own adapter's gradients only.  T = 0 clears dA and dB (or leaves
  * them, with accumulate).  Errors as for gptq_lora_matmul. */

@@ -14,8 +14,9 @@
 //   Backward: Δ differs along the contraction, so it has to be in the operand.  Δ (c - z) enters as two
 //   16-bit parts, a stage each against the same tokens, and keeps 14 bits of bf16 (16 in the mean) or 19
 //   of fp16, far below half a step of dX; as one 16-bit number it made dX 1.41 times as far from the
-//   exact sum as its own rounding, for half the products.  (fp16 operands carry a factor of 256, taken
-//   out at the end, so that small Δ stay normal numbers.)
+//   exact sum as its own rounding, for half the products.  (fp16 operands carry a power of two, taken
+//   out at the end, that brings the largest Δ of the columns' group to 2^11 and more: with a factor for
+//   all layers, small Δ were subnormal and lost their bits.)
 //   Adapters: each adapter that occurs among the tile's tokens ("slot") adds one more partial sum,
 //   whose operands are the adapter's 16-bit rows and U in two tf32 parts (22 bits), both fp32 in
 //   shared memory (kind::tf32); the epilogue adds it to that adapter's tokens only, so one request's
@@ -53,7 +54,6 @@ namespace gptq {
 constexpr int LT_THREADS = 640;
 constexpr int LT_A_BYTES = 128 * 128;      // weight operand of a stage
 constexpr int LT_DELTAS = 8;               // forward: partial sums whose Δ wait in shared memory
-constexpr float LT_F16_SCALE = 256.f;
 
 template <bool FWD, int BN>
 struct LtCfg {
@@ -75,6 +75,7 @@ struct LtParams {
   int T;
   int group_steps;          // groups in 128-column steps; 0: one grid per row
   const float2* grid;       // [n_g, m_pad] (Δ, z), zero behind m
+  const uint32_t* group_max;   // [n_g] bits of the largest |Δ| (fp16, backward)
   int m_pad, used;          // its columns, and how many n_g there are
   int mtiles, ttiles, splits;
   int units, per;           // the contraction in 128-column (forward) or 64-row (backward) units of two
@@ -90,6 +91,19 @@ struct LtParams {
   float* part;              // [splits, T, M] or null
   uint32_t idesc, idesc_tf32;
 };
+
+// The group of the columns that start at a multiple of 128 (the second CTA's may lie behind the last:
+// they are not stored).
+__device__ __forceinline__ int lt_group(const LtParams& p, int column) {
+  return p.group_steps ? min(column / 128 / p.group_steps, p.used - 1) : 0;
+}
+// The power of two that brings the group's largest |Δ| into [2^11, 2^12): |Δ (c - z)| stays below 61441.
+// (Only within 2^±100: beyond, fp32 products would leave their own range.)
+__device__ __forceinline__ int lt_f16_exponent(const LtParams& p, int column) {
+  const int e = (int)(p.group_max[lt_group(p, column)] >> 23) - 127;
+  return 11 - min(max(e, -89), 100);
+}
+__device__ __forceinline__ float lt_power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 __device__ __forceinline__ bool lt_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -437,8 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
             ok = false;
             break;
           }
-          // (the second CTA's columns may lie behind the last group: they are not stored)
-          const int g = p.group_steps ? min((FWD ? u : t.f0 / 128) / p.group_steps, p.used - 1) : 0;
+          const int g = lt_group(p, FWD ? 128 * u : t.f0);
           const int row = FWD ? t.f0 : 64 * u;
           tc::mbar_expect_tx(&full_c[bar.i], Cfg::C_BYTES + Cfg::G_BYTES);
           tc::tma_load_2d(codes + ring.i * Cfg::C_BYTES, &tmC, &full_c[bar.i],
@@ -489,6 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       const int32_t* slots = p.slots + t.nt * (BN + 1);
       const int fr = tid & 127, jh = tid >> 7, f = t.f0 + fr;
       const int chunks = p.rank_chunks ? slots[0] * p.rank_chunks : 0;
+      const float scale = FWD || BF16 ? 1.f : lt_power(lt_f16_exponent(p, t.f0));
       uint16_t next[16];
       auto fetch = [&](int q) {
         const int j0 = 32 * (q % p.rank_chunks) + 16 * jh;
@@ -539,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
             const uint32_t zz = zero_pair<BF16>((int)dz[h].y);
             const uint32_t words[4] = {code[h].x, code[h].y, code[h].z, code[h].w};
             WeightParts<BF16> parts;
-            if (!FWD) parts = WeightParts<BF16>(BF16 ? dz[h].x : dz[h].x * LT_F16_SCALE);
+            if (!FWD) parts = WeightParts<BF16>(BF16 ? dz[h].x : dz[h].x * scale);
             const int row = brow + 32 * (h0 + h);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -620,6 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       float acc[EBN];
 #pragma unroll
       for (int e = 0; e < EBN; ++e) acc[e] = 0.f;
+      const float unscale = FWD || BF16 ? 1.f : lt_power(-lt_f16_exponent(p, t.f0));
       // acc += factor · the next partial sum; in a forward base partial the factor is the row's Δ.
       // Eight columns are on their way from TMEM while eight are added.
       auto take = [&](bool scaled, const uint32_t* mask) {
@@ -632,7 +647,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         }
         tc::fence_after_sync();
         const float factor = scaled ? deltas[(pc % LT_DELTAS) * 128 + r]
-                                    : (FWD || BF16 || mask ? 1.f : 1.f / LT_F16_SCALE);
+                                    : (FWD || BF16 || mask ? 1.f : unscale);
         const uint64_t ff = pack_f32x2(factor, factor);
         uint32_t v[2][8];
         const uint32_t base = lane_base + dr.i * BN;
@@ -744,11 +759,12 @@ struct ShrinkParams {
   int32_t* slots;        // or null
   int BN, ttiles;
   int shrink_ctas, cluster;
-  // the grid: grid[g, r] = (Δ[r, g], z[r, g]) for g < used, zero for r in [m, m_pad); limit > 0: |Δ| must
-  // be below it
+  // the grid: grid[g, r] = (Δ[r, g], z[r, g]) for g < used, zero for r in [m, m_pad); group_max, where it
+  // is given (all zero): the bits of the largest |Δ|; limit > 0: |Δ| must be below it
   const float* scales;
   const int32_t* zeros;
   float2* grid;
+  uint32_t* group_max;
   int m, ng, used, m_pad, grid_ctas;
   float limit;
 };
@@ -779,6 +795,10 @@ __device__ __forceinline__ void turn_grid(const ShrinkParams& p, int i, DeviceSt
       }
       bad = bad || (p.limit > 0.f && !(fabsf(d[e]) < p.limit));
       if (g0 + e < p.used) p.grid[(long long)(g0 + e) * p.m_pad + r] = make_float2(d[e], (float)z[e]);
+      if (p.group_max) {   // of non-negative floats, NaN above all, as their bits
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(d[e])));
+        if (lane == 0 && g0 + e < p.used) atomicMax(&p.group_max[g0 + e], most);
+      }
     }
   }
   if (bad) raise_error(st, GPTQ_ERR_ARG, i);
@@ -1086,12 +1106,13 @@ constexpr size_t kMaxParts = 8;   // splits' partial sums that the asked-for wor
 // Workspace in bytes: U, its parts, the lists, rows that have to be padded, widened codes, splits.
 size_t lora_tc_bytes(const LoraLayer& l) {
   const size_t Rp = (size_t)round_up(l.R, 32), T = l.T, F = std::max(l.m, l.d);
-  size_t b = 256 * 9;
+  size_t b = 256 * 10;
   b += T * l.R * 4 + 2 * T * Rp * 4;
   b += (T / 64 + 1) * 65 * 4 + (T / 256 + 1) * 257 * 4;
   b += T * round_up(F, 8) * 2;                                  // a padded X or dY
   b += (size_t)l.m * round_up((l.d + 7) / 8, 4) * 4;            // widened codes
   b += (size_t)round_up(l.m, 256) * ((l.d + 127) / 128) * 8;    // the grid, column-major
+  b += (size_t)((l.d + 127) / 128) * 4;                         // its largest |Δ|
   if (T <= 1024) b += kMaxParts * T * F * 4;
   return b;
 }
@@ -1117,6 +1138,7 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   const int m_pad = (int)round_up(l.m, 256);
   const int used = l.group == -1 ? 1 : (l.d + l.group - 1) / l.group;
   float2* grid2 = out ? cv.take<float2>((size_t)used * m_pad) : nullptr;
+  uint32_t* group_max = out && !forward && !bf ? cv.take<uint32_t>(used) : nullptr;
   float* u_tmp = low ? low : cv.take<float>((size_t)l.T * l.R);
   float* parts = cv.take<float>((size_t)2 * l.T * Rp);
   int32_t* slots = cv.take<int32_t>((size_t)(l.T / 64 + 1) * 65 + (size_t)(l.T / 256 + 1) * 257);
@@ -1125,6 +1147,7 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   float* part = cv.take<float>(0);
   const size_t part_floats = cv.ok() ? (c->ws_bytes - cv.off) / sizeof(float) : 0;
 
+  if (group_max) GPTQ_CUDA_CHECK(c, cudaMemsetAsync(group_max, 0, (size_t)used * 4, c->stream));
   if (widen) {
     // rows in the grid's y: in pieces, should there be more than it holds
     for (int r0 = 0; r0 < l.m; r0 += 65535) {
@@ -1162,6 +1185,7 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   s.scales = l.scales;
   s.zeros = l.zeros;
   s.grid = grid2;
+  s.group_max = group_max;
   s.m = l.m; s.ng = l.ng; s.used = used; s.m_pad = m_pad;
   s.grid_ctas = out ? std::min(64, ((used + 7) / 8 * (m_pad / 32) + 7) / 8) : 0;
   s.limit = !forward && !bf ? 17.f : 0.f;
@@ -1206,6 +1230,7 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   p.T = l.T;
   p.group_steps = l.group == -1 ? 0 : l.group / 128;
   p.grid = grid2;
+  p.group_max = group_max;
   p.m_pad = m_pad;
   p.used = used;
   p.mtiles = (M + 255) / 256;

@@ -34,3 +34,21 @@ def test_dx_comes_from_unrounded_weights(ctx, T, m, d, bits, group, dtype):
     within(dX, want, bound + 1.01 * kept * (c.dY.double().abs() @ c.W.abs()), "dX")
     rounded = (want.to(dtype).double() - want).norm()
     assert (dX.double() - want).norm() <= 1.1 * rounded
+
+
+@pytest.mark.parametrize("T", [20, 300])
+@pytest.mark.parametrize("factor", [2.0 ** -22, 2.0 ** -12, 2.0 ** 8])
+def test_dx_of_fp16_keeps_small_weights(ctx, T, factor):
+    """Δ from some 2e-10 up (2^-22 of the usual), where an fp16 weight is far below the smallest normal number;
+    the last group's Δ is another 2^20 smaller than the others'."""
+    c = Case(T, 384, 320, 4, 128, 8, 2, HF, "none", 32)
+    for k in range(3):
+        s = factor if k < 2 else factor * 2.0 ** -20
+        c.scales[:, k] *= s
+        c.W[:, 128 * k:128 * (k + 1)] *= s
+    dX = torch.full_like(c.X, float("nan"))
+    c.dY.mul_(2.0 ** 14 if factor < 1 else 1.0)
+    G.gptq_lora_backward(ctx, c.dY, None, *c.layer(), None, dX=dX)
+    G.gptq_sync_status(ctx)
+    (want, bound), _, _ = c.backward(torch.zeros(T, 8, dtype=torch.float64, device="cuda"), False)
+    within(dX, want, bound + 1.01 * 2.0 ** -19 * (c.dY.double().abs() @ c.W.abs()), "dX")
