@@ -297,7 +297,8 @@ int gptq_dequant_matmul_tiled(gptq_ctx* ctx, const void* X, int x_dtype, int64_t
  * its own adapter only: non-finite values in other rows or adapters do not reach it.
  * 16-bit X with 1- to 4-bit codes, group -1 or a multiple of 128 and no group_id runs on the
  * tensor cores (the zeros must then lie in 0..15); every other format on CUDA cores.
- * Workspace: gptq_lora_workspace_bytes covers this call and gptq_lora_backward.  Calls of one context,
+ * Workspace: gptq_lora_workspace_bytes covers this call and gptq_lora_backward; with that much or more,
+ * equal inputs give equal bits (with less, the sums may be split otherwise).  Calls of one context,
  * and graphs captured from them, share its workspace: they may follow one another on its stream (graphs
  * on any stream), not overlap; work at the same time takes a context each.  Asynchronous.  Errors: ARG (also an adapter id outside
  * [-1, n_adapters), which then counts as -1, a group_id entry outside [0, n_g) or a zero outside

@@ -1,5 +1,7 @@
 """The adapter calls where their documentation allows more than a plain training step or a decoding batch
 shows: parts of a backward pass, values without a number, calls side by side."""
+import ctypes
+
 import pytest
 import torch
 
@@ -73,3 +75,30 @@ def test_an_infinity_in_the_backward_pass(ctx, dtype, T, where):
     _same_where_not_finite(dX, dx, "dX")
     _same_where_not_finite(dA, da, "dA")
     _same_where_not_finite(dB, db, "dB")
+
+
+@pytest.mark.parametrize("T, m, d, R", [(1, 128, 8192, 8), (24, 640, 4096, 16), (33, 128, 8192, 8), (80, 8192, 256, 8),
+                                        (200, 640, 4096, 16), (500, 256, 4096, 8)])
+def test_equal_bits_from_any_workspace_that_covers_the_call(T, m, d, R):
+    c = Case(T, m, d, 4, 128, R, 3, BF, "mixed", 44)
+    asked = G.gptq_lora_workspace_bytes(T, m, d, 4, 3, R, BF)
+    got = []
+    for more in (0, 1 << 20, 256 << 20):
+        ctx = G.Context(1, 1, workspace_bytes=asked + more)
+        if not more:   # no more than was asked for, whatever the context would have made of it
+            ctx.close()
+            ctx.workspace, ctx.handle = torch.empty(asked, dtype=torch.uint8, device="cuda"), ctypes.c_void_p()
+            assert G._lib.gptq_create(ctypes.byref(ctx.handle), ctypes.c_void_p(ctx.stream.cuda_stream),
+                                      ctypes.c_void_p(ctx.workspace.data_ptr()), asked) == G.GPTQ_OK
+        try:
+            Y, U, dX = torch.empty(T, m, device="cuda"), torch.empty(T, R, device="cuda"), torch.empty_like(c.X)
+            dA, dB = torch.empty(3, R, d, device="cuda"), torch.empty(3, R, m, device="cuda")
+            G.gptq_lora_matmul(ctx, c.X, *c.layer(), Y, U=U)
+            G.gptq_lora_backward(ctx, c.dY, c.X, *c.layer(), U, dX=dX, dA=dA, dB=dB)
+            G.gptq_sync_status(ctx)
+            got.append((Y, U, dX, dA, dB))
+        finally:
+            ctx.close()
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert torch.equal(a, b)
