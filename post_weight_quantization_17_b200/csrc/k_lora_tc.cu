@@ -307,8 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   // The kernel right before (A X or B dY of this call) has itself waited for everything earlier, so X
-  // and dY may be read now; only its own results (the grid, slots, the split U) wait for it.
-  pdl_release();
+  // and dY may be read now; only its own results (the grid, slots, the split U) wait for it, in each role.
   // the leader's barriers
   const uint32_t lead_full_x = tc::map_to_rank(full_x, 0), lead_full_a = tc::map_to_rank(full_a, 0);
   const uint32_t lead_d_empty = tc::map_to_rank(d_empty, 0);
@@ -621,6 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     uint32_t pc = 0;
     bool ok = true;
     pdl_wait();   // the slots
+    pdl_release();
     for (int i = pair; i < items && ok && !*abort_flag; i += npairs) {
       const LtTile t(p, i, BN, rank);
       const int f = t.f0 + r, tok = t.t0 + half * EBN;
