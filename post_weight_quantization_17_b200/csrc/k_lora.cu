@@ -258,7 +258,9 @@ int lora_forward(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool y_f32,
   Carver cv(c);
   if (lora_tensor_format(l) && lora_small_applies(l, X)) {
     float* ws = cv.take<float>(0);
-    const size_t floats = cv.ok() ? (c->ws_bytes - cv.off) / sizeof(float) : 0;
+    // of a workspace larger than asked for no more, so that the splits follow from the call's sizes alone
+    const size_t end = std::min(c->ws_bytes, lora_workspace_bytes(l));
+    const size_t floats = end > cv.off ? (end - cv.off) / sizeof(float) : 0;
     return lora_forward_small(c, l, X, Y, y_f32, U, ws, floats);
   }
   if (lora_tensor_format(l)) return lora_tc(c, l, true, X, Y, y_f32, U, kStatusBytes);

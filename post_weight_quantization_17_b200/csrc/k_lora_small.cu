@@ -500,13 +500,11 @@ bool lora_small_applies(const LoraLayer& l, const void* X) {
 }
 
 // Floats of workspace: U's parts and the splits' (at most 64 of them, and no more than fill two
-// waves of CTAs; a larger workspace holds no more, so that a call's sums have one order).
-static size_t small_part_floats(const LoraLayer& l) {
-  const size_t rows = (l.m + 127) / 128;
-  return std::min<size_t>(64, std::max<size_t>(1, 512 / rows + 1)) * l.T * l.m;
-}
+// waves of CTAs).
 size_t lora_small_floats(const LoraLayer& l) {
-  return (size_t)small_chunks(l.d) * l.T * l.R + 64 + small_part_floats(l);
+  const size_t rows = (l.m + 127) / 128;
+  const size_t splits = std::min<size_t>(64, std::max<size_t>(1, 512 / rows + 1));
+  return (size_t)small_chunks(l.d) * l.T * l.R + 64 + splits * l.T * l.m;
 }
 
 int lora_forward_small(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool y_f32, float* U,
@@ -530,7 +528,7 @@ int lora_forward_small(Ctx* c, const LoraLayer& l, const void* X, void* Y, bool 
   const long long parts = (long long)p.chunks * l.T * l.R;
   p.ranks = (int)std::min<long long>(l.R, (parts + 1023) / 1024);
   const long long warps = (long long)p.chunks * l.T * ((l.R + p.ranks - 1) / p.ranks);
-  const int splits = small_splits(l.m, l.d, l.T, c->num_sms, std::min(ws_floats - uf, small_part_floats(l)));
+  const int splits = small_splits(l.m, l.d, l.T, c->num_sms, ws_floats - uf);
   p.per = (p.steps + splits - 1) / splits;
   p.row_ctas = (l.m + LS_ROWS - 1) / LS_ROWS;
   const int piece = l.bits == 4 ? 4 : 2;   // words per load of codes

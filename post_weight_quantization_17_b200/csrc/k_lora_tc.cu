@@ -1099,9 +1099,7 @@ int launch_tc_any(Ctx* c, int BN, bool bf, const CUtensorMap& mx, const CUtensor
   return bf ? launch_tc<FWD, 256, true>(c, mx, mu, mc, p) : launch_tc<FWD, 256, false>(c, mx, mu, mc, p);
 }
 
-// Splits' partial sums that the asked-for workspace holds.  A call uses no more of a larger one: its splits,
-// and with them the order of its sums, follow from its sizes alone.
-constexpr size_t kMaxParts = 8;
+constexpr size_t kMaxParts = 8;   // splits' partial sums that the asked-for workspace holds
 
 }  // namespace
 
@@ -1147,7 +1145,10 @@ int lora_tc(Ctx* c, const LoraLayer& l, bool forward, const void* x, void* out, 
   if (!cv.ok())
     GPTQ_SET_ERR(c, GPTQ_ERR_NOMEM, "lora: workspace %zu < %zu bytes", c->ws_bytes, cv.off);
   float* part = cv.take<float>(0);
-  const size_t part_floats = std::min(cv.ok() ? (c->ws_bytes - cv.off) / sizeof(float) : 0, kMaxParts * l.T * M);
+  // of a workspace larger than asked for no more: the splits, and with them the order of the sums, then
+  // follow from the call's sizes alone
+  const size_t end = std::min(c->ws_bytes, lora_workspace_bytes(l));
+  const size_t part_floats = end > cv.off ? (end - cv.off) / sizeof(float) : 0;
 
   if (group_max) GPTQ_CUDA_CHECK(c, cudaMemsetAsync(group_max, 0, (size_t)used * 4, c->stream));
   if (widen) {

@@ -77,8 +77,8 @@ def test_an_infinity_in_the_backward_pass(ctx, dtype, T, where):
     _same_where_not_finite(dB, db, "dB")
 
 
-@pytest.mark.parametrize("T, m, d, R", [(1, 128, 8192, 8), (24, 640, 4096, 16), (33, 128, 8192, 8), (80, 8192, 256, 8),
-                                        (200, 640, 4096, 16), (500, 256, 4096, 8)])
+@pytest.mark.parametrize("T, m, d, R", [(1, 128, 8192, 8), (24, 640, 4096, 16), (33, 128, 8192, 8), (75, 841, 768, 16),
+                                        (110, 1408, 1408, 16), (63, 1462, 1536, 16), (200, 640, 4096, 16), (500, 256, 4096, 8)])
 def test_equal_bits_from_any_workspace_that_covers_the_call(T, m, d, R):
     c = Case(T, m, d, 4, 128, R, 3, BF, "mixed", 44)
     asked = G.gptq_lora_workspace_bytes(T, m, d, 4, 3, R, BF)
