@@ -10,6 +10,7 @@ import concurrent.futures
 import glob
 import hashlib
 import os
+import re
 import subprocess
 import sys
 
@@ -20,6 +21,9 @@ LIB = os.path.join(HERE, "libgptq_b200.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
+# Kernels whose roles hand registers to one another (setmaxnreg): a launch has to bring this many a thread, or
+# a role would wait for registers that the block does not own.
+LAUNCH_REGISTERS = {"k_lora_tc": 96}
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include")]
 
 
@@ -39,6 +43,22 @@ def _digest(extra: list[str]) -> str:
     return h.hexdigest()
 
 
+def check_registers(log: str) -> int:
+    """ptxas -v output: raises if a kernel of LAUNCH_REGISTERS got fewer registers; how many it found."""
+    found, name = 0, None
+    for line in log.splitlines():
+        entry = re.search(r"Compiling entry function '(\w+)'", line)
+        used = re.search(r"Used (\d+) registers", line)
+        if entry:
+            name = next((k for k in LAUNCH_REGISTERS if f"{len(k)}{k}I" in entry.group(1)), None)
+        elif used and name:
+            if int(used.group(1)) < LAUNCH_REGISTERS[name]:
+                raise RuntimeError(f"{name} was compiled with {used.group(1)} registers, it needs "
+                                   f"{LAUNCH_REGISTERS[name]}")
+            found, name = found + 1, None
+    return found
+
+
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
     digest = _digest(extra)
@@ -51,10 +71,13 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-        cmd = [NVCC, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
+        counted = os.path.splitext(os.path.basename(src))[0] in LAUNCH_REGISTERS
+        cmd = [NVCC, *ARCH, *FLAGS, *(["-Xptxas", "-v"] if counted else extra), "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
+        if counted and not check_registers(r.stderr):
+            raise RuntimeError(f"no register counts for {src}:\n{r.stderr}")
         return obj, r.stderr
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as ex:
