@@ -293,6 +293,7 @@ int gptq_dequant_matmul_tiled(gptq_ctx* ctx, const void* X, int x_dtype, int64_t
  *   Y        [T, m] out, of type y_dtype: GPTQ_F32 or x_dtype (rounded once, from fp32).
  *   U        [T, rank] fp32 out, device, or NULL (then it stays in the workspace); a later
  *            gptq_lora_backward takes it.
+ * Neither Y nor U may overlap an input or the other.
  * Ŵ, U and every sum are kept in fp32 or better.  A token's result depends on its own row of X and
  * its own adapter only: non-finite values in other rows or adapters do not reach it.
  * 16-bit X with 1- to 4-bit codes, group -1 or a multiple of 128 and no group_id runs on the
@@ -320,6 +321,8 @@ int gptq_lora_matmul(gptq_ctx* ctx, const void* X, int x_dtype, int64_t T, int64
  *   X, U     the forward call's input and its U (X may be NULL without dA, U without dB).
  *   dX       [T, d] of type x_dtype out; dA [n_adapters, rank, d] and dB [n_adapters, rank, m]
  *            fp32 out.  Any of the three may be NULL, not all.
+ *            None may overlap another or an input that is read (X is, for dA, and U, for dB; so dX may
+ *            be X where no dA is asked for, but never dY).
  *   accumulate  0: dA and dB are overwritten (adapters without tokens get 0); 1: they are added to.
  * On the tensor cores Ŵ enters dX as two numbers of x_dtype, good to 2^-14 of each weight (2^-19 for
  * GPTQ_F16), with products and sums in fp32, so dX is off by its own rounding; GPTQ_F16 asks for

@@ -74,6 +74,17 @@ bool aligned_to(const void* p, int dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == GPTQ_F32 ? 3 : 1)) == 0;
 }
 
+// A piece of device memory that a call reads or writes.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+size_t type_bytes(int dtype) { return dtype == GPTQ_F32 ? 4 : 2; }
+
 bool lora_sizes_ok(int64_t T, int64_t m, int64_t d, int bits, int64_t n, int64_t rank) {
   return T >= 0 && T <= 65535LL * 8 && m >= 1 && m <= (1 << 24) && d >= 1 && d <= (1 << 24) &&
          bits >= 1 && bits <= 8 && n >= 1 && n <= gptq::kLoraMaxAdapters && rank >= 1 &&
@@ -95,6 +106,24 @@ bool make_lora_layer(gptq::LoraLayer* l, int64_t T, int64_t m, int64_t d, int bi
   if (!aligned_to(A, dtype) || !aligned_to(B, dtype)) return false;
   *l = {(int)T, (int)m, (int)d, bits, group, (int)n_g, packed, group_id, scales, zeros, dtype,
         (int)n, (int)rank, adapter, A, B, scaling};
+  return true;
+}
+
+// Whether the outputs keep clear of one another, of the layer and its adapters, and of `inputs`.
+bool lora_outputs_apart(const gptq::LoraLayer& l, std::initializer_list<Span> outputs,
+                        std::initializer_list<Span> inputs) {
+  const size_t m = l.m, d = l.d, grid = m * l.ng * 4, e = type_bytes(l.dtype), nR = (size_t)l.n * l.R;
+  const Span layer[] = {{l.packed, m * ((d * l.bits + 31) / 32) * 4}, {l.group_id, d * 4}, {l.scales, grid},
+                        {l.zeros, grid}, {l.adapter, (size_t)l.T * 4}, {l.scaling, (size_t)l.n * 4},
+                        {l.A, nR * d * e}, {l.B, nR * m * e}};
+  for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span& s : layer)
+      if (overlap(*o, s)) return false;
+    for (const Span& s : inputs)
+      if (overlap(*o, s)) return false;
+    for (const Span* other = o + 1; other != outputs.end(); ++other)
+      if (overlap(*o, *other)) return false;
+  }
   return true;
 }
 
@@ -494,6 +523,10 @@ int gptq_lora_matmul(gptq_ctx* h, const void* X, int x_dtype, int64_t T, int64_t
                  (long long)T, (long long)d, (long long)m, bits, group, (long long)n_g,
                  (long long)n_adapters, (long long)rank);
   if (T == 0) return GPTQ_OK;
+  const size_t tokens = (size_t)T;
+  if (!lora_outputs_apart(l, {{Y, tokens * m * type_bytes(y_dtype)}, {U, tokens * rank * 4}},
+                          {{X, tokens * d * type_bytes(x_dtype)}}))
+    GPTQ_SET_ERR(c, GPTQ_ERR_ARG, "lora_matmul: an output overlaps an input or the other output");
   DeviceScope dev(c);
   if (!dev.ok) GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "lora_matmul: the context's device is not usable");
   gptq::StageScope stage(c, GPTQ_STAGE_LORA);
@@ -517,6 +550,11 @@ int gptq_lora_backward(gptq_ctx* h, const void* dY, const void* X, int x_dtype, 
     GPTQ_SET_ERR(c, GPTQ_ERR_ARG, "lora_backward: bad argument (T=%lld d=%lld m=%lld bits=%d group=%d n_g=%lld adapters=%lld rank=%lld)",
                  (long long)T, (long long)d, (long long)m, bits, group, (long long)n_g,
                  (long long)n_adapters, (long long)rank);
+  const size_t tokens = (size_t)T, e = type_bytes(x_dtype), low = (size_t)n_adapters * rank * 4;
+  if (!lora_outputs_apart(l, {{dX, tokens * d * e}, {dA, low * d}, {dB, low * m}},
+                          {{dY, tokens * m * e}, {dA ? X : nullptr, tokens * d * e},
+                           {dB ? U : nullptr, tokens * rank * 4}}))
+    GPTQ_SET_ERR(c, GPTQ_ERR_ARG, "lora_backward: an output overlaps an input or another output");
   DeviceScope dev(c);
   if (!dev.ok) GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "lora_backward: the context's device is not usable");
   gptq::StageScope stage(c, GPTQ_STAGE_LORA);

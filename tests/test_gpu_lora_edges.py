@@ -102,3 +102,36 @@ def test_equal_bits_from_any_workspace_that_covers_the_call(T, m, d, R):
     for other in got[1:]:
         for a, b in zip(got[0], other):
             assert torch.equal(a, b)
+
+
+def _refused(call):
+    with pytest.raises(G.GPTQError) as e:
+        call()
+    assert e.value.code == G.GPTQ_ERR_ARG and "overlaps" in str(e.value)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_overlapping_outputs_are_refused(ctx, dtype):
+    c = Case(6, 128, 128, 4, 128, 8, 2, dtype, "mixed", 45)
+    Y, U = torch.zeros(6, 128, dtype=dtype, device="cuda"), torch.zeros(6, 8, device="cuda")
+    dA, dB = torch.zeros(2, 8, 128, device="cuda"), torch.zeros(2, 8, 128, device="cuda")
+    _refused(lambda: G.gptq_lora_matmul(ctx, c.X, *c.layer(), c.X))
+    _refused(lambda: G.gptq_lora_matmul(ctx, c.X, *c.layer(), Y, U=Y.view(-1)[-48 * (2 if dtype == BF else 1):].view(F32).view(6, 8)))
+    _refused(lambda: G.gptq_lora_matmul(ctx, c.X, *c.layer(), c.B.view(-1)[:6 * 128].view(6, 128)))
+    back = lambda X, U, **out: G.gptq_lora_backward(ctx, c.dY, X, *c.layer(), U, **out)  # noqa: E731
+    _refused(lambda: back(c.X, U, dX=c.dY))
+    _refused(lambda: back(c.X, U, dX=c.X, dA=dA))
+    _refused(lambda: back(c.X, U, dA=dA, dB=dA))
+    _refused(lambda: back(c.X, dB.view(-1)[40:88].view(6, 8), dB=dB))
+    rows = torch.zeros(12, 128, dtype=dtype, device="cuda")     # beside one another is fine
+    rows[6:] = c.X
+    G.gptq_lora_matmul(ctx, rows[6:], *c.layer(), rows[:6], U=U)
+    Y2 = torch.zeros(6, 128, dtype=dtype, device="cuda")
+    G.gptq_lora_matmul(ctx, c.X, *c.layer(), Y2)
+    G.gptq_sync_status(ctx)
+    assert torch.equal(rows[:6], Y2)
+    want = torch.zeros_like(c.X)
+    back(None, U, dX=want, dB=dB)
+    back(c.X, U, dX=c.X, dB=dB)                                 # X is not read without dA
+    G.gptq_sync_status(ctx)
+    assert torch.equal(c.X, want)
