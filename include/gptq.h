@@ -81,7 +81,7 @@ uint64_t gptq_kernel_launches(const gptq_ctx* ctx);
  * error quickly and for testing that path.  Errors: ARG (cycles < 0). */
 int gptq_set_wait_budget(gptq_ctx* ctx, int64_t cycles);
 
-/* Stages that gptq_timing_read reports; every kernel launch counts under one of them.  The
+/* Stages that gptq_timing_read_stages reports; every kernel launch counts under one of them.  The
  * a-numbers are the steps of the hot path: a1 Hessian, a2 preconditioning, a3 factorization
  * (base blocks, recursion GEMMs, copies), a4 grid fit, a5 column loop (working copy, column
  * blocks), a6 lazy trailing updates, a7 outputs in original order, a8 packing; then the W4A16
@@ -92,8 +92,9 @@ enum {
   GPTQ_STAGE_FACTOR_GEMM = 3, GPTQ_STAGE_FACTOR_COPY = 4, GPTQ_STAGE_GRID = 5,
   GPTQ_STAGE_COLUMN = 6, GPTQ_STAGE_UPDATE = 7, GPTQ_STAGE_OUTPUT = 8, GPTQ_STAGE_PACK = 9,
   GPTQ_STAGE_DEQUANT = 10, GPTQ_STAGE_TWOSIDED = 11, GPTQ_STAGE_OTHER = 12,
+  GPTQ_NUM_STAGES = 13,   /* of gptq_timing_read: callers' arrays have this length */
   GPTQ_STAGE_LORA = 13, GPTQ_STAGE_DISTILL = 14,
-  GPTQ_NUM_STAGES = 15
+  GPTQ_ALL_STAGES = 15
 };
 
 /* Per-stage kernel timing, for measurement.  on != 0: from now on every kernel this context
@@ -105,8 +106,12 @@ enum {
 int gptq_timing_enable(gptq_ctx* ctx, int on);
 
 /* Synchronizes on the last timed launch and adds up, per stage, the time between each timed
- * launch's two events (ms, host double[GPTQ_NUM_STAGES]) and the number of timed launches (host
- * int64_t[GPTQ_NUM_STAGES]); then drops the records.  Errors: ARG, CUDA. */
+ * launch's two events (ms, host double[n]) and the number of timed launches (launches, host
+ * int64_t[n]); then drops the records.  n > GPTQ_STAGE_OTHER: the first n stages; launches of a later
+ * one count under GPTQ_STAGE_OTHER, and entries from GPTQ_ALL_STAGES on are 0.  Errors: ARG, CUDA. */
+int gptq_timing_read_stages(gptq_ctx* ctx, int n, double* ms, int64_t* launches);
+
+/* gptq_timing_read_stages with n = GPTQ_NUM_STAGES. */
 int gptq_timing_read(gptq_ctx* ctx, double* ms, int64_t* launches);
 
 /* Synchronizes the context stream, returns and clears the device status word

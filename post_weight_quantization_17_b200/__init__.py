@@ -27,7 +27,7 @@ STATUS_NAMES = {0: "OK", 1: "ERR_ARG", 2: "ERR_CUDA", 3: "ERR_NOT_PD", 4: "ERR_N
 
 _DTYPE_CODE = {torch.bfloat16: GPTQ_BF16, torch.float16: GPTQ_F16, torch.float32: GPTQ_F32}
 
-# stages of gptq_timing_read, in the order of the GPTQ_STAGE_* constants
+# stages of gptq_timing_read_stages, in the order of the GPTQ_STAGE_* constants
 STAGES = ("hessian", "prepare", "factor_base", "factor_gemm", "factor_copy", "grid", "column",
           "update", "output", "pack", "dequant", "twosided", "other", "lora", "distill")
 
@@ -53,6 +53,7 @@ _SIGS = {
     "gptq_sync_status": (_i32, [_vp]),
     "gptq_set_wait_budget": (_i32, [_vp, _i64]),
     "gptq_timing_enable": (_i32, [_vp, _i32]),
+    "gptq_timing_read_stages": (_i32, [_vp, _i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
     "gptq_timing_read": (_i32, [_vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
     "gptq_hessian_accumulate": (_i32, [_vp, _vp, _i32, _i64, _i64, _vp, ctypes.POINTER(_i64)]),
     "gptq_prepare_hinv": (_i32, [_vp, _vp, _i64, _i64, ctypes.c_float, _i32, _vp, _vp, _vp,
@@ -167,7 +168,7 @@ def gptq_timing_read(ctx: Context) -> dict:
     """{stage: (milliseconds summed over its timed launches, launches)} since the last read."""
     ms = (ctypes.c_double * len(STAGES))()
     n = (_i64 * len(STAGES))()
-    ctx.check(_lib.gptq_timing_read(ctx.handle, ms, n), "gptq_timing_read")
+    ctx.check(_lib.gptq_timing_read_stages(ctx.handle, len(STAGES), ms, n), "gptq_timing_read")
     return {name: (ms[k], int(n[k])) for k, name in enumerate(STAGES) if n[k]}
 
 

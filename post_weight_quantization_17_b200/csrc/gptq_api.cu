@@ -215,9 +215,13 @@ int gptq_timing_enable(gptq_ctx* h, int on) {
 }
 
 int gptq_timing_read(gptq_ctx* h, double* ms, int64_t* launches) {
-  if (!h || !ms || !launches) return GPTQ_ERR_ARG;
+  return gptq_timing_read_stages(h, GPTQ_NUM_STAGES, ms, launches);
+}
+
+int gptq_timing_read_stages(gptq_ctx* h, int n, double* ms, int64_t* launches) {
+  if (!h || !ms || !launches || n <= GPTQ_STAGE_OTHER) return GPTQ_ERR_ARG;
   Ctx* c = &h->c;
-  for (int k = 0; k < GPTQ_NUM_STAGES; ++k) {
+  for (int k = 0; k < n; ++k) {
     ms[k] = 0.0;
     launches[k] = 0;
   }
@@ -227,7 +231,7 @@ int gptq_timing_read(gptq_ctx* h, double* ms, int64_t* launches) {
     GPTQ_CUDA_CHECK(c, cudaEventSynchronize(t.stop));
     float e = 0.f;
     GPTQ_CUDA_CHECK(c, cudaEventElapsedTime(&e, t.start, t.stop));
-    const int k = (t.stage >= 0 && t.stage < GPTQ_NUM_STAGES) ? t.stage : GPTQ_STAGE_OTHER;
+    const int k = (t.stage >= 0 && t.stage < n) ? t.stage : GPTQ_STAGE_OTHER;
     ms[k] += e;
     launches[k] += 1;
   }

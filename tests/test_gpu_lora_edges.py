@@ -135,3 +135,26 @@ def test_overlapping_outputs_are_refused(ctx, dtype):
     back(c.X, U, dX=c.X, dB=dB)                                 # X is not read without dA
     G.gptq_sync_status(ctx)
     assert torch.equal(c.X, want)
+
+
+def test_stage_times_fit_the_arrays_of_older_programs():
+    """gptq_timing_read fills the 13 entries that it always has; newer stages count under the last of them."""
+    c, own = Case(80, 128, 256, 4, 128, 8, 2, BF, "runs", 46), G.Context(1, 1, workspace_bytes=32 << 20)
+    Y = torch.empty(80, 128, device="cuda")
+    n, other = len(G.STAGES), G.STAGES.index("other")
+    try:
+        G.gptq_timing_enable(own, True)
+        seen = {}
+        for name in ("gptq_timing_read", "gptq_timing_read_stages"):
+            G.gptq_lora_matmul(own, c.X, *c.layer(), Y)
+            ms, k = (ctypes.c_double * (n + 3))(*[-7.0] * (n + 3)), (ctypes.c_int64 * (n + 3))(*[-7] * (n + 3))
+            args = (own.handle, ms, k) if name == "gptq_timing_read" else (own.handle, n, ms, k)
+            assert getattr(G._lib, name)(*args) == G.GPTQ_OK
+            seen[name] = list(k)
+            end = 13 if name == "gptq_timing_read" else n
+            assert all(v == -7.0 for v in ms[end:]) and all(v == -7 for v in k[end:])
+        assert seen["gptq_timing_read"][other] == seen["gptq_timing_read_stages"][G.STAGES.index("lora")] > 0
+        short = (ctypes.c_double * 1)(), (ctypes.c_int64 * 1)()
+        assert G._lib.gptq_timing_read_stages(own.handle, 1, *short) == G.GPTQ_ERR_ARG
+    finally:
+        own.close()
