@@ -29,9 +29,10 @@
 //   warp 16       TMA producer of the tokens' operand (BN / 2 rows x 128 bytes per stage)
 //   warp 17       MMA issuer (the leader's), owner of TMEM (two partial-sum buffers of BN columns)
 //   warp 18       copies of the codes (TMA boxes) and of the grid, some units ahead; 19 idle
-// The barriers' arrivals and waits are the plain ones, also across the pair: each CTA's shared memory is
-// written, fenced for the tensor core's proxy and read by that same SM's tensor core, and what crosses
-// the pair is the order alone.  With cluster-wide release and acquire a stage took 0.87 us for 0.53.
+// Across the pair the order is the memory model's: every wait acquires in cluster scope, and a weight warp
+// releases what it wrote by a cluster-scope fence of shared memory alone before its arrivals (neither costs
+// anything measurable; arrivals that release all memory took a stage from 0.53 us to 0.87, and passed on
+// by one warp for both stages of a unit the call of 4096 tokens from 445 us to 502).
 // The grid is first turned column-major (turn_grid), so that the (Δ, z) of a unit's rows are one
 // contiguous copy: read in place they are 128 scattered words per step, and loads of codes and grid
 // into the weight warps' registers, though issued two to four stages ahead, took as long as the
@@ -109,7 +110,7 @@ __device__ __forceinline__ bool lt_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(ok)
       : "r"(tc::smem_u32(bar)), "r"(parity), "r"(20000u)
@@ -120,17 +121,22 @@ __device__ __forceinline__ bool lt_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(ok)
       : "r"(tc::smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
 }
+// What this warp's lanes wrote to shared memory before a __syncwarp is visible to whoever sees the arrivals
+// that follow, in either CTA.
+__device__ __forceinline__ void lt_release() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
 // `count` arrivals on a barrier of either CTA (a shared::cluster address; this CTA's shared::cta
-// addresses are among them).
+// addresses are among them), after lt_release.
 __device__ __forceinline__ void lt_arrive_remote(uint32_t cluster_addr, uint32_t count) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr), "r"(count)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr), "r"(count)
                : "memory");
 }
 // Waits for a phase, suspended in hardware between tries; false after `budget` cycles.
@@ -575,6 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
+          lt_release();
           lt_arrive_remote(lead_full_a + 8u * ring.i, 2);
           lt_arrive_remote(lead_full_a + 8u * second.i, 2);
           lt_arrive_remote(tc::smem_u32(&empty_c[slot]), 2);
@@ -607,7 +614,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) lt_arrive_remote(lead_full_a + 8u * ring.i, 1);
+          if (lane == 0) {
+            lt_release();
+            lt_arrive_remote(lead_full_a + 8u * ring.i, 1);
+          }
           ring.next();
         }
       }

@@ -28,3 +28,17 @@ def test_the_kernel_takes_its_barriers_from_the_rule():
     assert "NB = lora_code_barriers(NC)" in src
     assert re.search(r"NC = FWD \? kLoraCodeSlotsForward : kLoraCodeSlotsBackward", src)
 
+
+
+def test_barriers_across_the_pair_have_cluster_scope():
+    with open(os.path.join(CSRC, "k_lora_tc.cu")) as f:
+        src = f.read()
+    waits = re.findall(r'"mbarrier\.(?:try|test)_wait[^ ]*', src)
+    assert len(waits) == 2 and all(".acquire.cluster." in w for w in waits)
+    arrivals = re.findall(r'"mbarrier\.arrive[^ ]*', src)
+    assert len(arrivals) == 1 and ".relaxed.cluster." in arrivals[0]
+    assert "fence.release.sync_restrict::shared::cta.cluster;" in src
+    body = src[src.index("k_lora_tc(const"):]
+    body = body[:body.index("\n}")]
+    groups = re.findall(r"lt_release\(\);\s*(?:(?:lt_arrive_remote\([^;]*\);\s*)+)", body)
+    assert sum(g.count("lt_arrive_remote") for g in groups) == body.count("lt_arrive_remote") == 4
