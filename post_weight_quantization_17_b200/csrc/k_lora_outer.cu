@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(LO_THREADS, 2) k_lora_outer(const __grid_const
   };
   // The tensor cores' own additions round towards zero, so that a long run of them drifts (2.4e-6 of dA
   // after 36 pairs); LO_RUN pairs on, the sums go to the warp's place in shared memory, by IEEE additions
-  // (every 8 pairs 8.9e-7 and 114 us, every 4 6.4e-7 and 119).
+  // (every 8 pairs 8.9e-7 and 114 us, every 4 6.7e-7 and 116 to 119).
   // Tile i's column n is feature 8 n + i: a lane holds features 16 t4 + (0..7) and + 8.
   float* mine = sums + warp * LO_RANKS * LO_PAD;
   bool fresh = true;

@@ -39,8 +39,9 @@
 // whole stage (0.74 us of 256 tokens; without them 0.45).
 // Few tokens: the contraction is split over CTAs and k_lora_join adds the splits and the adapter.
 //
-// 4096 tokens, 11008 x 4096, rank 64, forward: 355 us (1.04 PFLOP/s of 1.67 measured); 4096 x 11008, rank
-// 32, backward: 323 us (1.14).  Both run at the power limit.  Of the forward's 375 us before its rows
+// 4096 tokens, 11008 x 4096, rank 64, forward: 368 us (1.00 PFLOP/s of 1.67 measured); 4096 x 11008, rank
+// 32, backward: 527 us (0.70 of the formula's operations, 1.40 of the products that the two parts make: the
+// tensor cores' sustained rate).  Both run at the power limit.  Of the forward's 375 us before its rows
 // were written four features at a time, the adapters' partial sums were 48 us, the output 40, the fp32
 // additions of the base partials 40.
 #include <algorithm>

@@ -158,3 +158,35 @@ def test_stage_times_fit_the_arrays_of_older_programs():
         assert G._lib.gptq_timing_read_stages(own.handle, 1, *short) == G.GPTQ_ERR_ARG
     finally:
         own.close()
+
+
+@pytest.mark.parametrize("T", [20, 300])
+def test_captured_fp16_backward(T):
+    """The largest Δ of every column group is found anew in each replay: with smaller scales, too."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c = Case(T, 256, 384, 4, 128, 8, 3, HF, "mixed", 47)
+    ctx = G.Context(1, 1, workspace_bytes=32 << 20, stream=s)
+    U = c.low(c.X, c.A)[0].float()
+    dX, dA = torch.empty_like(c.X), torch.empty(3, 8, 384, device="cuda")
+    torch.cuda.synchronize()
+    step = lambda: G.gptq_lora_backward(ctx, c.dY, c.X, *c.layer(), U, dX=dX, dA=dA)  # noqa: E731
+    try:
+        with torch.cuda.stream(s):
+            step()
+            s.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                step()
+            for factor in (1.0, 2.0 ** -12, 2.0 ** 18):
+                c.scales.mul_(factor)
+                step()
+                want = dX.clone(), dA.clone()
+                dX.zero_(), dA.zero_()
+                graph.replay()
+                s.synchronize()
+                assert torch.equal(dX, want[0]) and torch.equal(dA, want[1])
+        G.gptq_sync_status(ctx)
+    finally:
+        torch.cuda.synchronize()
+        ctx.close()
