@@ -332,7 +332,7 @@ int gptq_lora_matmul(gptq_ctx* ctx, const void* X, int x_dtype, int64_t T, int64
  *   dX       [T, d] of type x_dtype out; dA [n_adapters, rank, d] and dB [n_adapters, rank, m]
  *            fp32 out.  Any of the three may be NULL, not all.
  *            None may overlap another or an input that is read (X is, for dA, and U, for dB; so dX may
- *            be X where no dA is asked for, but never dY).
+ *            be X where no dA is asked for, but never dY), but dA and dB may be A and B of fp32.
  *   accumulate  0: dA and dB are overwritten (adapters without tokens get 0); 1: they are added to.
  * On the tensor cores Ŵ enters dX as two numbers of x_dtype, good to 2^-14 of each weight (2^-19 for
  * GPTQ_F16), with products and sums in fp32, so dX is off by its own rounding; GPTQ_F16 asks for

@@ -109,16 +109,18 @@ bool make_lora_layer(gptq::LoraLayer* l, int64_t T, int64_t m, int64_t d, int bi
   return true;
 }
 
-// Whether the outputs keep clear of one another, of the layer and its adapters, and of `inputs`.
-bool lora_outputs_apart(const gptq::LoraLayer& l, std::initializer_list<Span> outputs,
-                        std::initializer_list<Span> inputs) {
+// Whether an output keeps clear of the layer and its adapters.
+bool apart_from_layer(const gptq::LoraLayer& l, const Span& out) {
   const size_t m = l.m, d = l.d, grid = m * l.ng * 4, e = type_bytes(l.dtype), nR = (size_t)l.n * l.R;
-  const Span layer[] = {{l.packed, m * ((d * l.bits + 31) / 32) * 4}, {l.group_id, d * 4}, {l.scales, grid},
-                        {l.zeros, grid}, {l.adapter, (size_t)l.T * 4}, {l.scaling, (size_t)l.n * 4},
-                        {l.A, nR * d * e}, {l.B, nR * m * e}};
+  for (const Span& s : {Span{l.packed, m * ((d * l.bits + 31) / 32) * 4}, Span{l.group_id, d * 4},
+                        Span{l.scales, grid}, Span{l.zeros, grid}, Span{l.adapter, (size_t)l.T * 4},
+                        Span{l.scaling, (size_t)l.n * 4}, Span{l.A, nR * d * e}, Span{l.B, nR * m * e}})
+    if (overlap(out, s)) return false;
+  return true;
+}
+// Whether the outputs keep clear of one another and of `inputs`.
+bool apart(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
   for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
-    for (const Span& s : layer)
-      if (overlap(*o, s)) return false;
     for (const Span& s : inputs)
       if (overlap(*o, s)) return false;
     for (const Span* other = o + 1; other != outputs.end(); ++other)
@@ -528,8 +530,8 @@ int gptq_lora_matmul(gptq_ctx* h, const void* X, int x_dtype, int64_t T, int64_t
                  (long long)n_adapters, (long long)rank);
   if (T == 0) return GPTQ_OK;
   const size_t tokens = (size_t)T;
-  if (!lora_outputs_apart(l, {{Y, tokens * m * type_bytes(y_dtype)}, {U, tokens * rank * 4}},
-                          {{X, tokens * d * type_bytes(x_dtype)}}))
+  const Span y{Y, tokens * m * type_bytes(y_dtype)}, u{U, tokens * rank * 4};
+  if (!apart({y, u}, {{X, tokens * d * type_bytes(x_dtype)}}) || !apart_from_layer(l, y) || !apart_from_layer(l, u))
     GPTQ_SET_ERR(c, GPTQ_ERR_ARG, "lora_matmul: an output overlaps an input or the other output");
   DeviceScope dev(c);
   if (!dev.ok) GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "lora_matmul: the context's device is not usable");
@@ -555,9 +557,12 @@ int gptq_lora_backward(gptq_ctx* h, const void* dY, const void* X, int x_dtype, 
                  (long long)T, (long long)d, (long long)m, bits, group, (long long)n_g,
                  (long long)n_adapters, (long long)rank);
   const size_t tokens = (size_t)T, e = type_bytes(x_dtype), low = (size_t)n_adapters * rank * 4;
-  if (!lora_outputs_apart(l, {{dX, tokens * d * e}, {dA, low * d}, {dB, low * m}},
-                          {{dY, tokens * m * e}, {dA ? X : nullptr, tokens * d * e},
-                           {dB ? U : nullptr, tokens * rank * 4}}))
+  const Span dx{dX, tokens * d * e};
+  // (the layer and the adapters have been read when dA and dB are written: these may be A and B)
+  if (!apart({dx, {dA, low * d}, {dB, low * m}},
+             {{dY, tokens * m * e}, {dA ? X : nullptr, tokens * d * e}, {dB ? U : nullptr, tokens * rank * 4},
+              {adapter, tokens * 4}}) ||
+      !apart_from_layer(l, dx))
     GPTQ_SET_ERR(c, GPTQ_ERR_ARG, "lora_backward: an output overlaps an input or another output");
   DeviceScope dev(c);
   if (!dev.ok) GPTQ_SET_ERR(c, GPTQ_ERR_CUDA, "lora_backward: the context's device is not usable");

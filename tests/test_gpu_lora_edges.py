@@ -190,3 +190,14 @@ def test_captured_fp16_backward(T):
     finally:
         torch.cuda.synchronize()
         ctx.close()
+
+
+def test_fp32_gradients_may_be_added_to_the_adapters_themselves(ctx):
+    c = Case(40, 96, 128, 4, 128, 8, 2, F32, "mixed", 48)
+    U = c.low(c.X, c.A)[0].float()
+    dA, dB = torch.empty_like(c.A), torch.empty_like(c.B)
+    G.gptq_lora_backward(ctx, c.dY, c.X, *c.layer(), U, dA=dA, dB=dB)
+    A, B = c.A + dA, c.B + dB
+    G.gptq_lora_backward(ctx, c.dY, c.X, *c.layer(), U, dA=c.A, dB=c.B, accumulate=True)
+    G.gptq_sync_status(ctx)
+    assert torch.equal(c.A, A) and torch.equal(c.B, B)
