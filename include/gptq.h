@@ -335,9 +335,10 @@ int gptq_lora_matmul(gptq_ctx* ctx, const void* X, int x_dtype, int64_t T, int64
  *            be X where no dA is asked for, but never dY), but dA and dB may be A and B of fp32.
  *   accumulate  0: dA and dB are overwritten (adapters without tokens get 0); 1: they are added to.
  * On the tensor cores Ŵ enters dX as two numbers of x_dtype, good to 2^-14 of each weight (GPTQ_F16:
- * 2^-19, or 2^-36 of the largest Δ among the rows of its column group), with products and sums in fp32, so dX is off by its own rounding; GPTQ_F16 asks for
- * |Δ| < 17 (so |Ŵ| < 255), else ARG via gptq_sync_status.  dA and dB are sums over tokens
- * in a fixed order: two calls on the same inputs give the same bits.  Non-finite values of a token
+ * 2^-19, or 2^-36 of the largest Δ among the rows of its column group), with products and sums in
+ * fp32, so dX is off by its own rounding; GPTQ_F16 asks for |Δ| < 17 (so |Ŵ| < 255), else ARG via
+ * gptq_sync_status.  dA and dB are sums over tokens in a fixed order: two calls on the same inputs
+ * give the same bits.  Non-finite values of a token
  * reach its own row of dX and its own adapter's gradients only.  T = 0 clears dA and dB (or leaves
  * them, with accumulate).  Errors as for gptq_lora_matmul. */
 int gptq_lora_backward(gptq_ctx* ctx, const void* dY, const void* X, int x_dtype, int64_t T,
